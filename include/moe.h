@@ -66,6 +66,9 @@ extern "C" {
 #define MOE_OUT_BF16 0
 #define MOE_OUT_F32 1
 
+#define MOE_IN_BF16 0
+#define MOE_IN_F32 1
+
 #define MOE_CLAMP_SYMMETRIC 0  /* gate and up clamped to [-L, L] */
 #define MOE_CLAMP_GATE_UPPER 1 /* gate clamped to (-inf, L], up to [-L, L] */
 
@@ -318,6 +321,62 @@ int moe_quantize_mxfp8(const uint16_t* a, long long rows, int K, uint8_t* codes,
                        void* stream);
 
 /* ------------------------------------------------------------------------
+ * 8-bit operators with one fp32 scale for each block of 128 [TW quick start:
+ * FP8 checkpoints converted for training; CN outlook: FP8 training].  Codes
+ * are OCP E4M3; the scale of value (r, c) of rows [rows, K] is
+ * scales[r, c / 128] ([rows, ceil(K / 128)]), of matrices [G, N, K]
+ * scales[g, n / 128, c / 128] ([G, ceil(N / 128), ceil(K / 128)]); the last
+ * block of a side may be short.  Codes and scales are row-major: weights are
+ * taken as checkpoints hold them, with no packing.
+ *
+ * Quantisation.  Per block, X = the least integer with max |v| <= 448 * 2^X
+ * in [-126, 120] (0 for a block of zeros), scale = 2^X, code = E4M3(v / 2^X),
+ * nearest, ties to even: exact, and never saturating.  Values that are not
+ * finite take no part in the maximum and get the code NaN.
+ *   a [rows, K] or w [G, N, K], bf16 (MOE_IN_BF16) or fp32 (MOE_IN_F32); K a
+ *   multiple of 16; a, w, codes 16-byte aligned, scales 4-byte; at most
+ *   2^31 - 1 blocks.
+ */
+int moe_quantize_fp8_block(const void* a, int in_dtype, long long rows, int K, uint8_t* codes,
+                           float* scales, void* stream);
+int moe_quantize_weights_fp8_block(const void* w, int in_dtype, int G, int N, int K,
+                                   uint8_t* codes, float* scales, void* stream);
+
+/* Grouped matrix product: for offsets[g] <= r < offsets[g+1],
+ *   out[r, n] = sum_b a_scale[r, b] w_scale[g, n / 128, b]
+ *                     sum_{k in block b} a[r, k] w[g, n, k],
+ * out bf16 (MOE_OUT_BF16) or fp32 (MOE_OUT_F32); rows outside every group
+ * are left untouched.  The forward's products and, on the transposed
+ * weights' codes and scales, the input gradients.  Sums are fp32.  With an
+ * fp32 output the products are exact (on the bf16 matrix cores);
+ * with a bf16 output they run on the 8-bit matrix cores, whose alignment of
+ * products within a step costs up to about 4e-5 of the result, below the
+ * output's rounding.  Scales may be any fp32 values.
+ *   a8 [rows, K] codes, a_scale, w8 [G, N, K] codes, w_scale as above;
+ *   offsets [G+1] int32 in DEVICE memory, non-decreasing within [0, rows]
+ *   (entries outside are clamped into range).  K, N multiples of 16, up to
+ *   2^22; 16-byte aligned codes and out.  No workspace.
+ */
+int moe_grouped_gemm_fp8_block(const uint8_t* a8, const float* a_scale, const int32_t* offsets,
+                               int G, int rows, int K, int N, const uint8_t* w8,
+                               const float* w_scale, int out_dtype, void* out, void* stream);
+
+/* Grouped expert FFN on such rows and weights [HP 2.3 MegaMoE]:
+ *   G, U = the grouped products with w_gate, w_up [G, F, d] (fp32, exact
+ *   products), clamped as in moe_expert_ffn; h = silu(G) U in fp32; h8, h_scale = h quantised
+ *   along F (the rule of moe_quantize_fp8_block); y = the grouped product of
+ *   h8 with w_down [G, d, F].
+ *   h8 [rows, F] codes, h_scale [rows, ceil(F / 128)], y [rows, d] bf16 or
+ *   fp32 (written for rows inside a group only).  d, F multiples of 16.
+ */
+int moe_expert_ffn_fp8_block(const uint8_t* a8, const float* a_scale, const int32_t* offsets,
+                             int G, int rows, int d, int F, const uint8_t* w_gate,
+                             const float* w_gate_scale, const uint8_t* w_up,
+                             const float* w_up_scale, const uint8_t* w_down,
+                             const float* w_down_scale, float clamp_limit, int clamp_mode,
+                             uint8_t* h8, float* h_scale, int out_dtype, void* y, void* stream);
+
+/* ------------------------------------------------------------------------
  * Result return merged by routing weight [TW], plus the always-on shared
  * expert with weight 1 [MS]:
  *   y[t,o] = y_shared[t,o] + sum_j topk_w[t,j] * y_perm[dest[t,j], o]
@@ -453,10 +512,18 @@ typedef struct moe_weights {
     const uint8_t* w_gate_scale;  /* MOE_WEIGHTS_FP8 / FP4: block scales */
     const uint8_t* w_up_scale;    /* MOE_WEIGHTS_FP8 / FP4 */
     const uint8_t* w_down_scale;  /* MOE_WEIGHTS_FP8 / FP4 */
+    /* MOE_WEIGHTS_FP8_BLOCK (moe_forward_few): w_gate, w_up, w_down, s_gate,
+     * s_up and s_down hold E4M3 codes [out, in] (one byte each), w_*_scale
+     * (fp32 here) and s_*_scale their fp32 scales of 128 x 128 blocks; w_g
+     * stays bf16 [E, d] */
+    const float* s_gate_scale;    /* MOE_WEIGHTS_FP8_BLOCK */
+    const float* s_up_scale;      /* MOE_WEIGHTS_FP8_BLOCK */
+    const float* s_down_scale;    /* MOE_WEIGHTS_FP8_BLOCK */
 } moe_weights;
 #define MOE_WEIGHTS_FP8 2
 #define MOE_WEIGHTS_FP4 3
 #define MOE_WEIGHTS_A8W4 4
+#define MOE_WEIGHTS_FP8_BLOCK 5
 
 /* Workspace for moe_forward (all intermediates: logits, routing, permutation,
  * x_perm, h, y_perm and the shared expert's h and y) [HP 2.3 MegaMoE: one
@@ -496,6 +563,29 @@ int moe_forward_timed(const moe_cfg* cfg, const moe_weights* w, const uint16_t* 
                       const int32_t* input_ids, const uint8_t* modality, void* y,
                       float* logits_out, int32_t* ids_out, float* w_out, uint32_t* d_flags,
                       void* ws, size_t ws_bytes, void* stream, void* const* events);
+
+/* ------------------------------------------------------------------------
+ * Whole layer forward for a few tokens (decoding): the layer of moe_forward
+ * for T <= MOE_FEW_MAX_T tokens, on weights as checkpoints hold them, in three
+ * kernels without a dispatch permutation.  Arguments, limits and outputs as
+ * moe_forward, with
+ *   w->packed == 0: bf16 matrices [out, in], or MOE_WEIGHTS_FP8_BLOCK: 8-bit
+ *   codes with fp32 scales of 128 x 128 blocks (moe_weights); activations
+ *   stay bf16 (x is not quantised, h is rounded to bf16), sums are fp32;
+ *   8-bit products are exact.  Other packings and T > MOE_FEW_MAX_T return
+ *   MOE_ERR_UNSUPPORTED.
+ * Routes and weights are those of moe_route on the logits that this call
+ * computes (and writes to logits_out).  A hash-routed token whose id or
+ * experts are out of range gets ids -1, weights 0 and the shared expert's
+ * output alone.  ws: moe_forward_few_workspace_size(cfg) bytes (0 for an
+ * invalid cfg), 256-byte aligned; nothing in it needs to start at zero.
+ */
+#define MOE_FEW_MAX_T 64
+size_t moe_forward_few_workspace_size(const moe_cfg* cfg);
+int moe_forward_few(const moe_cfg* cfg, const moe_weights* w, const uint16_t* x,
+                    const int32_t* input_ids, const uint8_t* modality, void* y,
+                    float* logits_out, int32_t* ids_out, float* w_out, uint32_t* d_flags,
+                    void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
  * Whole layer backward [HP 2.3: MegaGate's fused backward chain of the gate's

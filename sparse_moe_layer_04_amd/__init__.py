@@ -7,5 +7,7 @@ The layer runs in hand-written HIP kernels behind the C ABI declared in
 from . import ops  # noqa: F401
 from .ops import (  # noqa: F401
     MoeLayer, gate_logits, route, permute, expert_ffn, combine,
+    quantize_fp8_block, quantize_weights_fp8_block, grouped_gemm_fp8_block,
+    expert_ffn_fp8_block,
     MODE_TOPK, MODE_HASH, OUT_BF16, OUT_F32,
 )

@@ -1,0 +1,473 @@
+// Grouped matrix product of 8-bit rows and weights with a scale for each
+// block of 128: for the rows r of group g,
+//   out[r, n] = sum_b a_scale[r, b] w_scale[g, n / 128, b]
+//                     sum_{k in block b} a[r, k] w[g, n, k],
+// codes E4M3, scales fp32, weights as checkpoints hold them ([G, N, K]
+// row-major codes, [G, N / 128, K / 128] scales).  K and N are multiples of
+// 16; the last block of either may be short.
+//
+// The sum over a block of 128 is one accumulation on the matrix cores from
+// zero; it is then multiplied by the product of the two scales and added to
+// the running fp32 sum on the vector units (one fma an output and block),
+// beside the next block's matrix products.
+//
+// Which matrix cores.  The 8-bit ones align the products of a step before
+// they add them and drop what falls below: 1.5e-5 of the result for normal
+// codes (4e-5 where magnitudes vary by 2^+-2), against 7e-8 for the bf16
+// ones, on which a product of two E4M3 values is exact (measured over 4096
+// terms against 64-bit sums).  An output rounded to bf16 (2^-9) takes the
+// 8-bit ones; an fp32 output and the SwiGLU's quantised h take the bf16 ones
+// at half the rate, their codes decoded in registers: the first would show
+// the loss, and of the second the codes of small values would move by
+// several steps (E4M3 goes down to 2^-18 of a block's largest value).
+//
+// Tile: up to 128 rows x 256 weight rows (SwiGLU: 128 features, gate and up
+// rows interleaved by 16 so that a wave holds both of a feature), 8 waves,
+// one 128-wide block of K a stage.  Both operands go through a 2-slot LDS
+// ring as codes (48 KB a stage): a wave's 64 lanes load 8 rows x 128 bytes
+// (whole lines of the row-major operands), two stages ahead of the matrix
+// products in registers, one stage ahead in LDS, one barrier a stage.
+// LDS row r holds its 16-byte chunk c at c ^ ((r >> 1) & 7), so that the
+// lanes of an operand read (32 rows, one chunk index) spread over the banks.
+#include <type_traits>
+
+#include "fp8_block.h"
+
+namespace moe {
+namespace {
+
+constexpr int BM = 128;                    // rows a tile
+constexpr int BN = 256;                    // weight rows a tile
+constexpr int BK = 128;                    // K a stage: one block
+constexpr int kThreads = 512;
+constexpr int kSlotW = BN * BK;
+constexpr int kSlot = (BN + BM) * BK;
+constexpr int kRing = 2 * kSlot;
+constexpr int kLdsLimit = 160 * 1024;
+constexpr int kStaticLds = 256;
+constexpr int kRowF32 = BN * 4 + 16;       // epilogue staging rows, padded
+constexpr int kRowBf16 = BN * 2 + 16;
+constexpr int kRowH = 128 + 16;
+static_assert(64 * kRowF32 <= kRing && BM * kRowBf16 <= kRing, "epilogue staging fits the ring");
+
+__device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
+
+struct Tile {
+    int tid, lane, wave, half, l32;
+    int g, row0, valid, n0;                // n0: first weight row (SwiGLU: feature)
+};
+
+template <int EPI, int MB>
+__device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t,
+                                         unsigned char* ring) {
+    // waves: WM along the rows x WN along the weight rows, each MI x NJ
+    // blocks of 32 x 32
+    constexpr int WM = MB == 4 ? 2 : 1, WN = 8 / WM, MI = MB / WM, NJ = 8 / WN;
+    constexpr int NA = MB == 4 ? 2 : 1;    // row loads a thread and stage
+    constexpr bool SW = EPI == FP8_SWIGLU;
+    constexpr bool EXACT = EPI != FP8_OUT_BF16;
+    const int wm = t.wave / WN, wn = t.wave % WN;
+    const int K = p.K, N = p.N;
+    const int S = (K + BK - 1) / BK;
+    const int nbn = (N + 127) / 128;
+
+    // loads: chunk c of LDS row lr + 64 q
+    const int c = t.tid & 7, lr = t.tid >> 3;
+    const uint8_t* wp[4];
+    const uint8_t* ap[NA];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int R = lr + 64 * q;
+        if constexpr (SW) {
+            const int f = min(t.n0 + 16 * (R >> 5) + (R & 15), N - 1);
+            wp[q] = (R & 16 ? p.w2 : p.w1) + ((size_t)t.g * N + f) * K;
+        } else {
+            wp[q] = p.w1 + ((size_t)t.g * N + min(t.n0 + R, N - 1)) * K;
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < NA; ++q)
+        ap[q] = p.a + (size_t)(t.row0 + min(lr + 64 * q, t.valid - 1)) * K;
+    const bool loads_a = MB > 1 || t.tid < 256;     // (32 rows: the first four waves)
+
+    u32x4 wr[2][4], ar[2][NA];
+    auto load = [&](int j, auto set) {
+        constexpr int P = decltype(set)::value;
+        // (past K: the row's last chunk, zeroed when it goes to LDS)
+        const int k = min(min(j, S - 1) * BK + 16 * c, K - 16);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) wr[P][q] = *(const u32x4*)(wp[q] + k);
+        if (loads_a) {
+#pragma unroll
+            for (int q = 0; q < NA; ++q) ar[P][q] = *(const u32x4*)(ap[q] + k);
+        }
+    };
+    auto store = [&](int j, auto set) {
+        constexpr int P = decltype(set)::value;
+        unsigned char* slot = ring + (j & 1) * kSlot;
+        if (j * BK + BK > K) {                      // the short last block
+            const bool in = j * BK + 16 * c < K;
+            const u32x4 z = {0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) wr[P][q] = in ? wr[P][q] : z;
+            if (loads_a) {
+#pragma unroll
+                for (int q = 0; q < NA; ++q) ar[P][q] = in ? ar[P][q] : z;
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int R = lr + 64 * q;
+            *(u32x4*)(slot + R * BK + ((c ^ swz(R)) << 4)) = wr[P][q];
+        }
+        if (loads_a) {
+#pragma unroll
+            for (int q = 0; q < NA; ++q) {
+                const int R = lr + 64 * q;
+                *(u32x4*)(slot + kSlotW + R * BK + ((c ^ swz(R)) << 4)) = ar[P][q];
+            }
+        }
+    };
+
+    // scales: this lane's rows, and the 128-block of this wave's weight rows
+    // (of gate and up)
+    const float* sap[MI];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+        sap[i] = p.as + (size_t)(t.row0 + min((wm * MI + i) * 32 + t.l32, t.valid - 1)) * S;
+    const int nblk = min((t.n0 + (SW ? 0 : wn * NJ * 32)) / 128, nbn - 1);
+    const float* swp1 = p.s1 + ((size_t)t.g * nbn + nblk) * S;
+    const float* swp2 = SW ? p.s2 + ((size_t)t.g * nbn + nblk) * S : swp1;
+    float sa[MI], sw1, sw2;
+    auto load_s = [&](int j) {
+        const int jj = min(j, S - 1);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) sa[i] = sap[i][jj];
+        sw1 = swp1[jj];
+        sw2 = SW ? swp2[jj] : sw1;
+    };
+
+    f32x16 acc[MI][NJ];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int n = 0; n < NJ; ++n)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][n][e] = 0.0f;
+
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    load(0, I0());
+    load(1, I1());
+    load_s(0);
+    store(0, I0());
+
+    auto stage = [&](int j, auto par) {
+        constexpr int P = decltype(par)::value;      // j % 2
+        __syncthreads();                             // slot P holds block j
+        load(j + 2, par);
+        const unsigned char* sl = ring + P * kSlot;
+        const unsigned char* sla = sl + kSlotW;
+        float s1[MI], s2[MI];
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            s1[i] = sa[i] * sw1;
+            s2[i] = sa[i] * sw2;
+        }
+        load_s(j + 1);
+        f32x16 part[MI][NJ];
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int n = 0; n < NJ; ++n)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) part[i][n][e] = 0.0f;
+        if constexpr (EXACT) {
+            // 16 codes a lane and chunk pair: two 16-wide bf16 steps
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                bf16x8 a[MI][2], w[NJ][2];
+                auto read = [&](const unsigned char* s, int blk, bf16x8 (&o)[2]) {
+                    const int r = blk * 32 + t.l32;
+                    const u32x4 v =
+                        *(const u32x4*)(s + r * BK + (((2 * q + t.half) ^ swz(r)) << 4));
+                    o[0] = fp8x8_to_bf16x8(u32x2{v[0], v[1]}, 1.0f);
+                    o[1] = fp8x8_to_bf16x8(u32x2{v[2], v[3]}, 1.0f);
+                };
+#pragma unroll
+                for (int n = 0; n < NJ; ++n) read(sl, wn * NJ + n, w[n]);
+#pragma unroll
+                for (int i = 0; i < MI; ++i) read(sla, wm * MI + i, a[i]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < MI; ++i)
+#pragma unroll
+                        for (int n = 0; n < NJ; ++n)
+                            part[i][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                                w[n][h], a[i][h], part[i][n], 0, 0, 0);
+            }
+        } else {
+            // (any order of K within the block will do, the same for both)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                v8i a[MI], w[NJ];
+                auto read = [&](const unsigned char* b, int blk) {
+                    const int r = blk * 32 + t.l32;
+                    const u32x4 lo =
+                        *(const u32x4*)(b + r * BK + (((4 * s + t.half) ^ swz(r)) << 4));
+                    const u32x4 hi =
+                        *(const u32x4*)(b + r * BK + (((4 * s + 2 + t.half) ^ swz(r)) << 4));
+                    return v8i{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
+                               (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+                };
+#pragma unroll
+                for (int n = 0; n < NJ; ++n) w[n] = read(sl, wn * NJ + n);
+#pragma unroll
+                for (int i = 0; i < MI; ++i) a[i] = read(sla, wm * MI + i);
+#pragma unroll
+                for (int i = 0; i < MI; ++i)
+#pragma unroll
+                    for (int n = 0; n < NJ; ++n)
+                        part[i][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                            w[n], a[i], part[i][n], 0, 0, 0, 127, 0, 127);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int n = 0; n < NJ; ++n)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    acc[i][n][e] =
+                        __builtin_fmaf(part[i][n][e], SW && e >= 8 ? s2[i] : s1[i], acc[i][n][e]);
+        if (j + 1 < S) store(j + 1, std::integral_constant<int, P ^ 1>());
+    };
+    for (int j = 0; j < S; j += 2) {
+        stage(j, I0());
+        if (j + 1 < S) stage(j + 1, I1());
+    }
+
+    // Epilogues: lane l holds, of row l % 32 of its block, weight rows
+    // 8 (e / 4) + 4 (l / 32) + e % 4; through LDS into whole-line stores.
+    __syncthreads();
+    if constexpr (EPI == FP8_OUT_F32) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            if (i) __syncthreads();
+#pragma unroll
+            for (int n = 0; n < NJ; ++n)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int col = (wn * NJ + n) * 32 + 8 * q + 4 * t.half;
+                    *(f32x4*)(ring + (wm * 32 + t.l32) * kRowF32 + col * 4) =
+                        f32x4{acc[i][n][4 * q], acc[i][n][4 * q + 1], acc[i][n][4 * q + 2],
+                              acc[i][n][4 * q + 3]};
+                }
+            __syncthreads();
+            const int col = 4 * t.lane;
+            for (int sr = t.wave; sr < WM * 32; sr += 8) {
+                const int r = ((sr >> 5) * MI + i) * 32 + (sr & 31);
+                if (r < t.valid && t.n0 + col < N)
+                    *(f32x4*)((float*)p.out + (size_t)(t.row0 + r) * N + t.n0 + col) =
+                        *(const f32x4*)(ring + sr * kRowF32 + col * 4);
+            }
+        }
+    } else if constexpr (EPI == FP8_OUT_BF16) {
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int n = 0; n < NJ; ++n)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int col = (wn * NJ + n) * 32 + 8 * q + 4 * t.half;
+                    uint32_t v[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        v[h] = (uint32_t)f32_to_bf16(acc[i][n][4 * q + 2 * h]) |
+                               ((uint32_t)f32_to_bf16(acc[i][n][4 * q + 2 * h + 1]) << 16);
+                    *(u32x2*)(ring + ((wm * MI + i) * 32 + t.l32) * kRowBf16 + col * 2) =
+                        u32x2{v[0], v[1]};
+                }
+        __syncthreads();
+        const int col = 8 * t.l32;
+        for (int r = 2 * t.wave + t.half; r < t.valid; r += 16)
+            if (t.n0 + col < N)
+                *(u32x4*)((uint16_t*)p.out + (size_t)(t.row0 + r) * N + t.n0 + col) =
+                    *(const u32x4*)(ring + r * kRowBf16 + col * 2);
+    } else {
+        // h = SwiGLU in fp32, quantised along the tile's 128 features: the
+        // row maximum over this lane's features, its half-wave partner's and
+        // the other waves'
+        float* rm = (float*)ring;                     // [WN][BM]
+        unsigned char* stg = ring + 8 * BM * 4;       // [BM][kRowH] codes
+        float h[MI][NJ][8];
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            float m = 0.0f;
+#pragma unroll
+            for (int n = 0; n < NJ; ++n) {
+                const bool in = t.n0 + 16 * (wn * NJ + n) < N;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float v = clamped_swiglu(acc[i][n][e], acc[i][n][e + 8], p.clamp_limit,
+                                                   p.clamp_mode);
+                    h[i][n][e] = in ? v : 0.0f;
+                    m = fmaxf(m, finite_abs(h[i][n][e]));
+                }
+            }
+            m = fmaxf(m, __shfl_xor(m, 32, 64));
+            if (t.half == 0) rm[wn * BM + (wm * MI + i) * 32 + t.l32] = m;
+        }
+        __syncthreads();
+        const int nbf = (N + 127) / 128;
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            const int r = (wm * MI + i) * 32 + t.l32;
+            float m = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WN; ++w) m = fmaxf(m, rm[w * BM + r]);
+            const int X = block_exponent(m);
+            const float inv = pow2(-X);
+#pragma unroll
+            for (int n = 0; n < NJ; ++n)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int f = 16 * (wn * NJ + n) + 8 * q + 4 * t.half;
+                    *(uint32_t*)(stg + r * kRowH + f) =
+                        e4m3_pack4(h[i][n][4 * q], h[i][n][4 * q + 1], h[i][n][4 * q + 2],
+                                   h[i][n][4 * q + 3], inv);
+                }
+            if (wn == 0 && t.half == 0 && r < t.valid)
+                p.out_scale[(size_t)(t.row0 + r) * nbf + t.n0 / 128] = pow2(X);
+        }
+        __syncthreads();
+        for (int r = lr; r < t.valid; r += 64)
+            if (t.n0 + 16 * c < N)
+                *(u32x4*)((uint8_t*)p.out + (size_t)(t.row0 + r) * N + t.n0 + 16 * c) =
+                    *(const u32x4*)(stg + r * kRowH + 16 * c);
+    }
+}
+
+// Persistent grid, one workgroup a CU.  Items are (group, n-tile, m-tile),
+// the 8 XCDs take contiguous ranges, so that the m-tiles of a weight tile and
+// the n-tiles of a group's rows meet in one XCD's L2; a group's rows split
+// evenly over its ceil(n / 128) m-tiles.
+template <int EPI>
+__global__ __launch_bounds__(kThreads) void gemm_fp8_block_kernel(Fp8GemmArgs p) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ int scan_sh[8];
+    constexpr int TN = EPI == FP8_SWIGLU ? BN / 2 : BN;
+    Tile t;
+    t.tid = threadIdx.x;
+    t.lane = t.tid & 63;
+    t.wave = __builtin_amdgcn_readfirstlane(t.tid >> 6);
+    t.half = t.lane >> 5;
+    t.l32 = t.lane & 31;
+    const int G = p.G, rows = p.rows;
+    int* prefix = (int*)(smem + kRing);              // [G + 1] items before group g
+    const int NT = (p.N + TN - 1) / TN;
+    auto group_rows = [&](int g, int& lo, int& hi) {
+        lo = min(max(p.offsets[g], 0), rows);
+        hi = max(lo, min(max(p.offsets[g + 1], 0), rows));
+    };
+    {
+        const int per = (G + kThreads - 1) / kThreads;
+        const int g0 = t.tid * per;
+        int local = 0;
+        for (int g = g0; g < g0 + per && g < G; ++g) {
+            int lo, hi;
+            group_rows(g, lo, hi);
+            const int items = NT * ((hi - lo + BM - 1) / BM);
+            prefix[g] = items;
+            local += items;
+        }
+        int x = local;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const int y = __shfl_up(x, off, 64);
+            if (t.lane >= off) x += y;
+        }
+        if (t.lane == 63) scan_sh[t.wave] = x;
+        __syncthreads();
+        int before = 0, total = 0;
+        for (int w = 0; w < 8; ++w) {
+            if (w < t.wave) before += scan_sh[w];
+            total += scan_sh[w];
+        }
+        int run = before + x - local;
+        for (int g = g0; g < g0 + per && g < G; ++g) {
+            const int v = prefix[g];
+            prefix[g] = run;
+            run += v;
+        }
+        if (t.tid == 0) prefix[G] = total;
+        __syncthreads();
+    }
+    const long long Q = prefix[G];
+    const int xcd = blockIdx.x & 7;
+    const int hi_item = (int)(Q * (xcd + 1) / 8);
+    for (int q = (int)(Q * xcd / 8) + (int)(blockIdx.x >> 3); q < hi_item; q += gridDim.x >> 3) {
+        int lo = 0, hi = G;
+        while (lo < hi) {                            // the last g with prefix[g] <= q
+            const int mid = (lo + hi + 1) >> 1;
+            if (prefix[mid] <= q) lo = mid; else hi = mid - 1;
+        }
+        t.g = __builtin_amdgcn_readfirstlane(lo);
+        int r0, r1;
+        group_rows(t.g, r0, r1);
+        const int n = r1 - r0, mt = (n + BM - 1) / BM;
+        const int per = ((n + mt - 1) / mt + 31) & ~31;
+        const int local = q - prefix[t.g];
+        t.n0 = local / mt * TN;
+        t.row0 = r0 + local % mt * per;
+        t.valid = min(per, r1 - t.row0);
+        if (t.valid > 64)
+            run_tile<EPI, 4>(p, t, smem);
+        else if (t.valid > 32)
+            run_tile<EPI, 2>(p, t, smem);
+        else
+            run_tile<EPI, 1>(p, t, smem);
+        __syncthreads();                             // the ring is free again
+    }
+}
+
+template <int EPI>
+hipError_t launch(const Fp8GemmArgs& g, hipStream_t stream) {
+    static DeviceSetup setup;
+    long long grid = 0, static_lds = 0;
+    const hipError_t err =
+        device_setup(setup, grid, static_lds, [](int, long long& gr, long long& st) {
+            const void* fn = (const void*)gemm_fp8_block_kernel<EPI>;
+            hipFuncAttributes fa;
+            hipError_t e = hipFuncGetAttributes(&fa, fn);
+            if (e != hipSuccess) return e;
+            if (fa.sharedSizeBytes > (size_t)kStaticLds) return hipErrorInvalidValue;
+            e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                    kLdsLimit - (int)fa.sharedSizeBytes);
+            if (e != hipSuccess) return e;
+            st = (long long)fa.sharedSizeBytes;
+            gr = (device_cu_count() + 7) & ~7;
+            return hipSuccess;
+        });
+    if (err != hipSuccess) return err;
+    const size_t lds = kRing + (size_t)(g.G + 1) * sizeof(int);
+    if (lds + (size_t)static_lds > (size_t)kLdsLimit) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((gemm_fp8_block_kernel<EPI>), dim3((unsigned)grid), dim3(kThreads),
+                       lds, stream, g);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_grouped_gemm_fp8_block(int epilogue, const Fp8GemmArgs& g, hipStream_t stream) {
+    if (g.K < 16 || g.K % 16 || g.N < 16 || g.N % 16 || g.G < 1) return hipErrorInvalidValue;
+    switch (epilogue) {
+        case FP8_OUT_BF16: return launch<FP8_OUT_BF16>(g, stream);
+        case FP8_OUT_F32: return launch<FP8_OUT_F32>(g, stream);
+        case FP8_SWIGLU: return launch<FP8_SWIGLU>(g, stream);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace moe

@@ -45,11 +45,19 @@ class MoeCfg(ctypes.Structure):
 
 
 WEIGHT_NAMES = ("w_g", "logit_offset", "score_bias", "tid2eid", "w_gate", "w_up", "w_down",
-                "s_gate", "s_up", "s_down", "w_gate_scale", "w_up_scale", "w_down_scale")
+                "s_gate", "s_up", "s_down", "w_gate_scale", "w_up_scale", "w_down_scale",
+                "s_gate_scale", "s_up_scale", "s_down_scale")
 # moe_weights.packed values of MXFP8 / MXFP4 routed-expert weights
 WEIGHTS_FP8 = 2
 WEIGHTS_FP4 = 3
 WEIGHTS_A8W4 = 4
+# E4M3 codes with fp32 scales of 128 x 128 blocks (forward_few)
+WEIGHTS_FP8_BLOCK = 5
+# scaled block of the 8-bit operators, largest T of forward_few
+FP8_BLOCK = 128
+FEW_MAX_T = 64
+IN_BF16 = 0
+IN_F32 = 1
 MATRIX_NAMES = ("w_g", "w_gate", "w_up", "w_down", "s_gate", "s_up", "s_down")
 
 
@@ -115,6 +123,13 @@ def lib():
     L.moe_pack_weights_fp4.argtypes = [P, I, I, I, I, P, P, P]
     L.moe_quantize_mxfp8.argtypes = [P, ctypes.c_longlong, I, P, P, P]
     L.moe_expert_ffn_a8w4.argtypes = [P, P, P, I, I, I, I, P, P, P, P, P, P, F, I, P, P, P, P]
+    L.moe_quantize_fp8_block.argtypes = [P, I, ctypes.c_longlong, I, P, P, P]
+    L.moe_quantize_weights_fp8_block.argtypes = [P, I, I, I, I, P, P, P]
+    L.moe_grouped_gemm_fp8_block.argtypes = [P, P, P, I, I, I, I, P, P, I, P, P]
+    L.moe_expert_ffn_fp8_block.argtypes = [P, P, P, I, I, I, I, P, P, P, P, P, P, F, I, P, P, I,
+                                           P, P]
+    L.moe_forward_few_workspace_size.argtypes = [ctypes.POINTER(MoeCfg)]
+    L.moe_forward_few_workspace_size.restype = S
     L.moe_forward_workspace_size.argtypes = [ctypes.POINTER(MoeCfg)]
     L.moe_forward_workspace_size.restype = S
     L.moe_workspace_size.argtypes = [ctypes.POINTER(MoeCfg)]
@@ -123,6 +138,7 @@ def lib():
     L.moe_forward.argtypes = [ctypes.POINTER(MoeCfg), ctypes.POINTER(MoeWeights), P, P, P, P,
                               P, P, P, P, P, S, P]
     L.moe_forward_timed.argtypes = L.moe_forward.argtypes + [P]
+    L.moe_forward_few.argtypes = L.moe_forward.argtypes
     L.moe_backward_workspace_size.argtypes = [ctypes.POINTER(MoeCfg)]
     L.moe_backward_workspace_size.restype = S
     L.moe_backward.argtypes = [ctypes.POINTER(MoeCfg), ctypes.POINTER(MoeWeights),
@@ -132,7 +148,9 @@ def lib():
                  "moe_expert_ffn_packed",
                  "moe_combine", "moe_forward", "moe_forward_timed", "moe_pack_weights",
                  "moe_pack_weights_fp8", "moe_pack_weights_fp4", "moe_quantize_mxfp8",
-                 "moe_expert_ffn_a8w4"):
+                 "moe_expert_ffn_a8w4", "moe_quantize_fp8_block",
+                 "moe_quantize_weights_fp8_block", "moe_grouped_gemm_fp8_block",
+                 "moe_expert_ffn_fp8_block", "moe_forward_few"):
         getattr(L, name).restype = I
     _lib = L
     return L
@@ -528,6 +546,113 @@ def pack_weights_fp4(w, panel_rows):
     return codes, scales
 
 
+def _in_dtype(t, name):
+    if t is None:
+        raise MoeError(f"{name} is required")
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise MoeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    return IN_F32 if t.dtype == torch.float32 else IN_BF16
+
+
+def _codes8(t, name, shape):
+    """8-bit codes: uint8 or float8_e4m3fn (the same bytes)."""
+    if t is not None and t.dtype == torch.float8_e4m3fn:
+        return _need(t, torch.float8_e4m3fn, name, shape=shape)
+    return _need(t, torch.uint8, name, shape=shape)
+
+
+def _blocks(n):
+    return -(-n // FP8_BLOCK)
+
+
+def quantize_fp8_block(a, codes=None, scales=None):
+    """Rows a [rows, K] (bf16 or fp32, K a multiple of 16) as E4M3 codes with
+    one power-of-two scale per 128 values of a row (moe_quantize_fp8_block):
+    returns (codes uint8 [rows, K], scales fp32 [rows, ceil(K / 128)])."""
+    dt = _in_dtype(a, "a")
+    _need(a, a.dtype, "a", 2)
+    rows, K = a.shape
+    codes = _out(codes, torch.uint8, "codes", (rows, K), a.device)
+    scales = _out(scales, torch.float32, "scales", (rows, _blocks(K)), a.device)
+    _check(lib().moe_quantize_fp8_block(_ptr(a), dt, rows, K, _ptr(codes), _ptr(scales),
+                                        _stream()), "moe_quantize_fp8_block")
+    return codes, scales
+
+
+def quantize_weights_fp8_block(w, codes=None, scales=None):
+    """Matrices w [G, N, K] or [N, K] (bf16 or fp32, K a multiple of 16) as
+    E4M3 codes with one power-of-two scale per 128 x 128 block
+    (moe_quantize_weights_fp8_block): returns (codes uint8 of w's shape,
+    scales fp32 [(G,) ceil(N / 128), ceil(K / 128)])."""
+    dt = _in_dtype(w, "w")
+    if w.dim() not in (2, 3):
+        raise MoeError("w must have 2 or 3 dims")
+    _need(w, w.dtype, "w")
+    shape = tuple(w.shape)
+    G, N, K = (1,) + shape if w.dim() == 2 else shape
+    codes = _out(codes, torch.uint8, "codes", shape, w.device)
+    scales = _out(scales, torch.float32, "scales", shape[:-2] + (_blocks(N), _blocks(K)),
+                  w.device)
+    _check(lib().moe_quantize_weights_fp8_block(_ptr(w), dt, G, N, K, _ptr(codes), _ptr(scales),
+                                                _stream()), "moe_quantize_weights_fp8_block")
+    return codes, scales
+
+
+def grouped_gemm_fp8_block(a8, a_scale, offsets, w8, w_scale, out_dtype=OUT_BF16, out=None):
+    """out[r] = a[r] @ w[g].T for the rows of group g, operands as codes and
+    block scales (moe_grouped_gemm_fp8_block): a8 [rows, K], a_scale [rows,
+    ceil(K / 128)], w8 [G, N, K], w_scale [G, ceil(N / 128), ceil(K / 128)],
+    offsets [G + 1] int32.  Codes uint8 or float8_e4m3fn, scales fp32; K, N
+    multiples of 16.  Rows outside every group are not written."""
+    _codes8(a8, "a8", (None, None))
+    rows, K = a8.shape
+    _codes8(w8, "w8", (None, None, K))
+    G, N, _ = w8.shape
+    _need(a_scale, torch.float32, "a_scale", shape=(rows, _blocks(K)))
+    _need(w_scale, torch.float32, "w_scale", shape=(G, _blocks(N), _blocks(K)))
+    _need(offsets, torch.int32, "offsets", shape=(G + 1,))
+    dt = torch.float32 if out_dtype == OUT_F32 else torch.bfloat16
+    out = _out(out, dt, "out", (rows, N), a8.device)
+    _check(lib().moe_grouped_gemm_fp8_block(_ptr(a8), _ptr(a_scale), _ptr(offsets), G, rows, K, N,
+                                            _ptr(w8), _ptr(w_scale), int(out_dtype), _ptr(out),
+                                            _stream()), "moe_grouped_gemm_fp8_block")
+    return out
+
+
+def expert_ffn_fp8_block(a8, a_scale, offsets, w_gate, w_up, w_down, clamp_limit=10.0,
+                         clamp_mode=CLAMP_SYMMETRIC, out_dtype=OUT_F32, h8=None, h_scale=None,
+                         y=None):
+    """Grouped FFN on rows and weights in 128-block 8 bits
+    (moe_expert_ffn_fp8_block): a8 / a_scale from quantize_fp8_block, w_* =
+    (codes [G, out, in], scales) pairs as quantize_weights_fp8_block gives
+    them.  Returns (h8 uint8 [rows, F], h_scale fp32 [rows, ceil(F / 128)],
+    y [rows, d] of out_dtype)."""
+    _codes8(a8, "a8", (None, None))
+    rows, d = a8.shape
+    (cg, sg), (cu, su), (cd, sd) = w_gate, w_up, w_down
+    _codes8(cg, "w_gate", (None, None, d))
+    G, F, _ = cg.shape
+    _codes8(cu, "w_up", (G, F, d))
+    _codes8(cd, "w_down", (G, d, F))
+    bd, bf = _blocks(d), _blocks(F)
+    _need(a_scale, torch.float32, "a_scale", shape=(rows, bd))
+    _need(sg, torch.float32, "w_gate scales", shape=(G, bf, bd))
+    _need(su, torch.float32, "w_up scales", shape=(G, bf, bd))
+    _need(sd, torch.float32, "w_down scales", shape=(G, bd, bf))
+    _need(offsets, torch.int32, "offsets", shape=(G + 1,))
+    dev = a8.device
+    h8 = _out(h8, torch.uint8, "h8", (rows, F), dev)
+    h_scale = _out(h_scale, torch.float32, "h_scale", (rows, bf), dev)
+    dt = torch.float32 if out_dtype == OUT_F32 else torch.bfloat16
+    y = _out(y, dt, "y", (rows, d), dev)
+    _check(lib().moe_expert_ffn_fp8_block(_ptr(a8), _ptr(a_scale), _ptr(offsets), G, rows, d, F,
+                                          _ptr(cg), _ptr(sg), _ptr(cu), _ptr(su), _ptr(cd),
+                                          _ptr(sd), float(clamp_limit), int(clamp_mode), _ptr(h8),
+                                          _ptr(h_scale), int(out_dtype), _ptr(y), _stream()),
+           "moe_expert_ffn_fp8_block")
+    return h8, h_scale, y
+
+
 class MoeLayer:
     """One fine-grained MoE layer on the device: holds the weights, the config
     and a preallocated workspace; ``forward`` is one C-ABI call."""
@@ -541,14 +666,21 @@ class MoeLayer:
         self.weights = dict(weights)
         self.plain = dict(weights)     # the [out, in] matrices (for the backward's layouts)
         self.bw = None
+        self.few_ws = None             # forward_few's workspace, made at its first call
+        block = packed == "fp8_block"
         _need(self.weights["w_g"], torch.bfloat16, "w_g", shape=(E, d))
-        _need(self.weights["w_gate"], torch.bfloat16, "w_gate", shape=(E, F, d))
-        _need(self.weights["w_up"], torch.bfloat16, "w_up", shape=(E, F, d))
-        _need(self.weights["w_down"], torch.bfloat16, "w_down", shape=(E, d, F))
+        shapes = dict(w_gate=(E, F, d), w_up=(E, F, d), w_down=(E, d, F))
         if F_shared > 0:
-            _need(self.weights["s_gate"], torch.bfloat16, "s_gate", shape=(F_shared, d))
-            _need(self.weights["s_up"], torch.bfloat16, "s_up", shape=(F_shared, d))
-            _need(self.weights["s_down"], torch.bfloat16, "s_down", shape=(d, F_shared))
+            shapes.update(s_gate=(F_shared, d), s_up=(F_shared, d), s_down=(d, F_shared))
+        for n, shape in shapes.items():
+            if block:
+                # codes and fp32 block scales, as the caller's checkpoint has
+                # them or quantize_weights_fp8_block makes them
+                _codes8(self.weights.get(n), n, shape)
+                _need(self.weights.get(n + "_scale"), torch.float32, n + "_scale",
+                      shape=shape[:-2] + (_blocks(shape[-2]), _blocks(shape[-1])))
+            else:
+                _need(self.weights[n], torch.bfloat16, n, shape=shape)
         _opt(self.weights.get("logit_offset"), torch.float32, "logit_offset", shape=(E,))
         if mode == MODE_TOPK and n_bias > 0:
             _need(self.weights.get("score_bias"), torch.float32, "score_bias",
@@ -558,7 +690,7 @@ class MoeLayer:
         fp8 = packed == "fp8"
         a8w4 = packed == "a8w4"
         fp4 = packed == "fp4" or a8w4
-        if packed:
+        if packed and not block:
             # one-time layout change at load time (moe_pack_weights; with
             # packed="fp8" / "fp4" the routed expert matrices are quantised to
             # MXFP8 / MXFP4 by moe_pack_weights_fp8 / _fp4 instead; "a8w4":
@@ -573,7 +705,7 @@ class MoeLayer:
                 else:
                     self.weights[key] = pack_weights(self.weights[key], PANEL_ROWS[key])
         self.packed = (WEIGHTS_FP8 if fp8 else WEIGHTS_A8W4 if a8w4 else WEIGHTS_FP4 if fp4
-                       else int(bool(packed)))
+                       else WEIGHTS_FP8_BLOCK if block else int(bool(packed)))
         self.cw = MoeWeights(packed=self.packed,
                              **{n: _ptr(self.weights.get(n)) for n in WEIGHT_NAMES})
         self.device = self.weights["w_g"].device
@@ -662,4 +794,35 @@ class MoeLayer:
                                        _ptr(ids), _ptr(w), _ptr(self.flags),
                                        _ptr(self.workspace), self.ws_bytes, _stream(), ev),
                "moe_forward")
+        return y
+
+    def forward_few(self, x, input_ids=None, modality=None, y=None, logits=None, ids=None,
+                    w=None):
+        """The layer forward for a few tokens (decoding), one C-ABI call
+        (moe_forward_few): x [t, d] with t up to the layer's T and at most
+        FEW_MAX_T.  Takes plain bf16 weights (packed=False) or 8-bit ones with
+        block scales (packed="fp8_block")."""
+        c = self.cfg
+        _need(x, torch.bfloat16, "x", shape=(None, c.d))
+        T = x.shape[0]
+        if T > min(c.T, FEW_MAX_T):
+            raise MoeError(f"forward_few takes at most {min(c.T, FEW_MAX_T)} tokens, got {T}")
+        _opt(input_ids, torch.int32, "input_ids", shape=(T,))
+        _opt(modality, torch.uint8, "modality", shape=(T,))
+        _opt(logits, torch.float32, "logits", shape=(T, c.E))
+        _opt(ids, torch.int32, "ids", shape=(T, c.k))
+        _opt(w, torch.float32, "w", shape=(T, c.k))
+        dt = torch.float32 if c.out_dtype == OUT_F32 else torch.bfloat16
+        y = _out(y, dt, "y", (T, c.d), x.device)
+        if self.few_ws is None:
+            self.few_cfg = MoeCfg.from_buffer_copy(c)
+            self.few_cfg.T = min(c.T, FEW_MAX_T)
+            self.few_ws_bytes = int(lib().moe_forward_few_workspace_size(
+                ctypes.byref(self.few_cfg)))
+            self.few_ws = torch.empty(self.few_ws_bytes, dtype=torch.uint8, device=self.device)
+        self.few_cfg.T = T
+        _check(lib().moe_forward_few(ctypes.byref(self.few_cfg), ctypes.byref(self.cw), _ptr(x),
+                                     _ptr(input_ids), _ptr(modality), _ptr(y), _ptr(logits),
+                                     _ptr(ids), _ptr(w), _ptr(self.flags), _ptr(self.few_ws),
+                                     self.few_ws_bytes, _stream()), "moe_forward_few")
         return y
