@@ -31,6 +31,22 @@ constexpr int kTiles = MOE_FEW_MAX_T / 16; // column tiles of 16 tokens
 constexpr int kMaxPairs = MOE_FEW_MAX_T * MOE_MAX_K;
 static_assert(kMaxPairs <= kThreads, "one thread a (token, slot) pair");
 
+// Values that other workgroups of the same launch read: stored and loaded at
+// device scope (past the XCD's own L2, which is not coherent with the other
+// seven), a store complete for every XCD once the wave's store counter says
+// so.  A device-wide fence instead would write the whole L2 back at every
+// item (133 us instead of 12 for the down products of one token).
+__device__ __forceinline__ void put_shared(float* p, float v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float get_shared(const float* p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// this wave's stores have completed
+__device__ __forceinline__ void stores_done() {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
 struct Lane {
     int tid, lane, wave, r16, grp;         // r16 = lane % 16, grp = lane / 16
 };
@@ -393,10 +409,15 @@ __device__ __forceinline__ void combine_chunk(const FewArgs& p, int chunk, int t
     for (int i = tid; i < p.T * 16; i += kThreads) {
         const int t = i >> 4;
         const size_t o = (size_t)chunk * 16 + (i & 15);
-        float v = p.Fs > 0 ? p.part[(size_t)(P + t) * p.d + o] : 0.0f;
-        for (int j = 0; j < p.k; ++j)
-            if (p.ids[t * p.k + j] >= 0)
-                v = __builtin_fmaf(p.w[t * p.k + j], p.part[(size_t)(t * p.k + j) * p.d + o], v);
+        float e[MOE_MAX_K];
+#pragma unroll
+        for (int j = 0; j < MOE_MAX_K; ++j)
+            e[j] = j < p.k && p.ids[t * p.k + j] >= 0
+                       ? get_shared(&p.part[(size_t)(t * p.k + j) * p.d + o]) : 0.0f;
+        float v = p.Fs > 0 ? get_shared(&p.part[(size_t)(P + t) * p.d + o]) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < MOE_MAX_K; ++j)
+            if (j < p.k && p.ids[t * p.k + j] >= 0) v = __builtin_fmaf(p.w[t * p.k + j], e[j], v);
         if (p.out_dtype == MOE_OUT_F32)
             ((float*)p.y)[(size_t)t * p.d + o] = v;
         else
@@ -459,19 +480,19 @@ __global__ __launch_bounds__(kThreads, 2) void few_down_kernel(FewArgs p) {
                 if (r < m) {
                     const size_t slot =
                         shared ? (size_t)p.T * p.k + r : (size_t)p.pairs[s + m0 + r];
-                    p.part[slot * p.d + 16 * chunk + o] = sum_partials(red, ct, r >> 4, o, r & 15);
+                    put_shared(&p.part[slot * p.d + 16 * chunk + o],
+                               sum_partials(red, ct, r >> 4, o, r & 15));
                 }
             }
         }
-        __threadfence();                   // the partial outputs, before the count
+        stores_done();                     // the partial outputs, before the count
         __syncthreads();
         int* last = &last_sh[parity];
-        if (l.tid == 0) *last = atomicAdd(&p.count[chunk], 1u) == (unsigned)(n + sh - 1);
+        if (l.tid == 0)
+            *last = __hip_atomic_fetch_add(&p.count[chunk], 1u, __ATOMIC_RELAXED,
+                                           __HIP_MEMORY_SCOPE_AGENT) == (unsigned)(n + sh - 1);
         __syncthreads();
-        if (*last) {
-            __threadfence();
-            combine_chunk(p, chunk, l.tid);
-        }
+        if (*last) combine_chunk(p, chunk, l.tid);
     }
 }
 
