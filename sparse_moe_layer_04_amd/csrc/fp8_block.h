@@ -37,6 +37,12 @@ __device__ __forceinline__ uint32_t e4m3_pack4(float a, float b, float c, float 
     return (uint32_t)r;
 }
 
+// two fp32 values as bf16 (nearest, ties to even, NaN kept), a in the low half
+__device__ __forceinline__ uint32_t bf16_pack2(float a, float b) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+}
+
 // maximum of v >= 0 over the 16 lanes of a DPP row, in every lane
 __device__ __forceinline__ float row16_max(float v) {
 #define MOE_DPP_MAX(CTRL)                                                                   \

@@ -52,6 +52,17 @@ static_assert(64 * kRowF32 <= kRing && BM * kRowBf16 <= kRing, "epilogue staging
 
 __device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
 
+// Buffer resource over [base, base + bytes), wave-uniform (read from the
+// first lane, so that it lives in scalar registers)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void* base, size_t bytes) {
+    const uint64_t p = (uint64_t)(uintptr_t)base;
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)p);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32));
+    const int n = __builtin_amdgcn_readfirstlane((int)min(bytes, (size_t)0x7fffffff));
+    return __builtin_amdgcn_make_buffer_rsrc((void*)(uintptr_t)(((uint64_t)hi << 32) | lo), 0, n,
+                                             0x00020000);
+}
+
 struct Tile {
     int tid, lane, wave, half, l32;
     int g, row0, valid, n0;                // n0: first weight row (SwiGLU: feature)
@@ -71,80 +82,98 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t,
     const int S = (K + BK - 1) / BK;
     const int nbn = (N + 127) / 128;
 
-    // loads: chunk c of LDS row lr + 64 q
-    const int c = t.tid & 7, lr = t.tid >> 3;
-    const uint8_t* wp[4];
-    const uint8_t* ap[NA];
+    // Addresses.  Loads go through buffer resources over the tile's rows
+    // (wave-uniform base, 32-bit offsets), rows past the tile's or the
+    // matrix's end clamped to the last.  LDS rows 64 (loads) or 32 (operand
+    // reads) apart share their swizzle, so the rest of an LDS address is an
+    // immediate; the chunk index enters it by exclusive or.
+    const int c = t.tid & 7, lr = t.tid >> 3;       // loads: chunk c of row lr + 64 q
+    // SwiGLU: LDS row R is row R & 15 of 16 features' gate (R & 16 == 0) or up
+    // rows; R & 16 is the same for a wave and all q
+    const bool up = SW && (t.wave & 2);
+    const size_t wfirst = ((size_t)t.g * N + t.n0) * K;
+    const int wrows = N - t.n0;                     // (>= 1)
+    const __amdgpu_buffer_rsrc_t wsrc =
+        uniform_rsrc((up ? p.w2 : p.w1) + wfirst, (size_t)min(wrows, BN) * K);
+    const __amdgpu_buffer_rsrc_t asrc =
+        uniform_rsrc(p.a + (size_t)t.row0 * K, (size_t)t.valid * K);
+    int wo[4], ao[NA];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         const int R = lr + 64 * q;
-        if constexpr (SW) {
-            const int f = min(t.n0 + 16 * (R >> 5) + (R & 15), N - 1);
-            wp[q] = (R & 16 ? p.w2 : p.w1) + ((size_t)t.g * N + f) * K;
-        } else {
-            wp[q] = p.w1 + ((size_t)t.g * N + min(t.n0 + R, N - 1)) * K;
-        }
+        wo[q] = min(SW ? 16 * (R >> 5) + (R & 15) : R, wrows - 1) * K + 16 * c;
     }
 #pragma unroll
-    for (int q = 0; q < NA; ++q)
-        ap[q] = p.a + (size_t)(t.row0 + min(lr + 64 * q, t.valid - 1)) * K;
-    const bool loads_a = MB > 1 || t.tid < 256;     // (32 rows: the first four waves)
+    for (int q = 0; q < NA; ++q) ao[q] = min(lr + 64 * q, t.valid - 1) * K + 16 * c;
+    // bytes that this thread's chunk of the last stage reaches past K
+    const int past = max(0, (S - 1) * BK + 16 * c + 16 - K);
+    const bool loads_a = MB > 1 || t.wave < 4;      // (32 rows: the first four waves)
+    unsigned char* st = ring + lr * BK + ((c ^ swz(lr)) << 4);
+    const int rd0 = t.l32 * BK + ((t.half ^ swz(t.l32)) << 4);
+    const int rdw = wn * NJ * 32 * BK + rd0;
+    const int rda = kSlotW + wm * MI * 32 * BK + rd0;
 
     u32x4 wr[2][4], ar[2][NA];
     auto load = [&](int j, auto set) {
         constexpr int P = decltype(set)::value;
-        // (past K: the row's last chunk, zeroed when it goes to LDS)
-        const int k = min(min(j, S - 1) * BK + 16 * c, K - 16);
+        const int k = min(j, S - 1) * BK;
+        const int back = j >= S - 1 ? past : 0;     // (a chunk past K: the row's last one)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) wr[P][q] = *(const u32x4*)(wp[q] + k);
+        for (int q = 0; q < 4; ++q)
+            wr[P][q] = __builtin_bit_cast(
+                u32x4, __builtin_amdgcn_raw_buffer_load_b128(wsrc, wo[q] - back, k, 0));
         if (loads_a) {
 #pragma unroll
-            for (int q = 0; q < NA; ++q) ar[P][q] = *(const u32x4*)(ap[q] + k);
+            for (int q = 0; q < NA; ++q)
+                ar[P][q] = __builtin_bit_cast(
+                    u32x4, __builtin_amdgcn_raw_buffer_load_b128(asrc, ao[q] - back, k, 0));
         }
     };
     auto store = [&](int j, auto set) {
         constexpr int P = decltype(set)::value;
-        unsigned char* slot = ring + (j & 1) * kSlot;
-        if (j * BK + BK > K) {                      // the short last block
-            const bool in = j * BK + 16 * c < K;
+        unsigned char* slot = st + P * kSlot;
+        if (j == S - 1 && K % BK) {                 // the short last block: zeros past K
             const u32x4 z = {0u, 0u, 0u, 0u};
 #pragma unroll
-            for (int q = 0; q < 4; ++q) wr[P][q] = in ? wr[P][q] : z;
+            for (int q = 0; q < 4; ++q) wr[P][q] = past ? z : wr[P][q];
             if (loads_a) {
 #pragma unroll
-                for (int q = 0; q < NA; ++q) ar[P][q] = in ? ar[P][q] : z;
+                for (int q = 0; q < NA; ++q) ar[P][q] = past ? z : ar[P][q];
             }
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int R = lr + 64 * q;
-            *(u32x4*)(slot + R * BK + ((c ^ swz(R)) << 4)) = wr[P][q];
-        }
+        for (int q = 0; q < 4; ++q) *(u32x4*)(slot + q * 64 * BK) = wr[P][q];
         if (loads_a) {
 #pragma unroll
-            for (int q = 0; q < NA; ++q) {
-                const int R = lr + 64 * q;
-                *(u32x4*)(slot + kSlotW + R * BK + ((c ^ swz(R)) << 4)) = ar[P][q];
-            }
+            for (int q = 0; q < NA; ++q) *(u32x4*)(slot + kSlotW + q * 64 * BK) = ar[P][q];
         }
     };
 
     // scales: this lane's rows, and the 128-block of this wave's weight rows
-    // (of gate and up)
-    const float* sap[MI];
+    // (of gate and up); vector loads, whose counter is in order (a scalar
+    // load in flight would make every LDS wait a wait for it)
+    const __amdgpu_buffer_rsrc_t sasrc =
+        uniform_rsrc(p.as + (size_t)t.row0 * S, (size_t)t.valid * S * 4);
+    int so[MI];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
-        sap[i] = p.as + (size_t)(t.row0 + min((wm * MI + i) * 32 + t.l32, t.valid - 1)) * S;
+        so[i] = min((wm * MI + i) * 32 + t.l32, t.valid - 1) * S * 4;
     const int nblk = min((t.n0 + (SW ? 0 : wn * NJ * 32)) / 128, nbn - 1);
-    const float* swp1 = p.s1 + ((size_t)t.g * nbn + nblk) * S;
-    const float* swp2 = SW ? p.s2 + ((size_t)t.g * nbn + nblk) * S : swp1;
+    const size_t sfirst = ((size_t)t.g * nbn + nblk) * S;
+    const __amdgpu_buffer_rsrc_t s1src = uniform_rsrc(p.s1 + sfirst, (size_t)S * 4);
+    const __amdgpu_buffer_rsrc_t s2src =
+        uniform_rsrc((SW ? p.s2 : p.s1) + sfirst, (size_t)S * 4);
     float sa[MI], sw1, sw2;
     auto load_s = [&](int j) {
-        const int jj = min(j, S - 1);
+        const int k = min(j, S - 1) * 4;
 #pragma unroll
-        for (int i = 0; i < MI; ++i) sa[i] = sap[i][jj];
-        sw1 = swp1[jj];
-        sw2 = SW ? swp2[jj] : sw1;
+        for (int i = 0; i < MI; ++i)
+            sa[i] = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(sasrc, so[i], k, 0));
+        sw1 = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(s1src, 0, k, 0));
+        if constexpr (SW)
+            sw2 = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(s2src, 0, k, 0));
+        else
+            sw2 = sw1;
     };
 
     f32x16 acc[MI][NJ];
@@ -158,23 +187,23 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t,
     using I0 = std::integral_constant<int, 0>;
     using I1 = std::integral_constant<int, 1>;
     load(0, I0());
-    load(1, I1());
     load_s(0);
+    load(1, I1());
     store(0, I0());
 
     auto stage = [&](int j, auto par) {
         constexpr int P = decltype(par)::value;      // j % 2
         __syncthreads();                             // slot P holds block j
-        load(j + 2, par);
-        const unsigned char* sl = ring + P * kSlot;
-        const unsigned char* sla = sl + kSlotW;
         float s1[MI], s2[MI];
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
             s1[i] = sa[i] * sw1;
             s2[i] = sa[i] * sw2;
         }
+        // (the scales before the operands: the memory counter is in order, and
+        // what is needed at the next stage must not wait for the one after)
         load_s(j + 1);
+        load(j + 2, par);
         f32x16 part[MI][NJ];
 #pragma unroll
         for (int i = 0; i < MI; ++i)
@@ -182,22 +211,27 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t,
             for (int n = 0; n < NJ; ++n)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) part[i][n][e] = 0.0f;
+        // 16 codes: chunk pair q of block blk's rows
+        auto read = [&](int at, int blk, int q) {
+            return *(const u32x4*)(ring + (at ^ (q << 5)) + P * kSlot + blk * 32 * BK);
+        };
         if constexpr (EXACT) {
             // 16 codes a lane and chunk pair: two 16-wide bf16 steps
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 bf16x8 a[MI][2], w[NJ][2];
-                auto read = [&](const unsigned char* s, int blk, bf16x8 (&o)[2]) {
-                    const int r = blk * 32 + t.l32;
-                    const u32x4 v =
-                        *(const u32x4*)(s + r * BK + (((2 * q + t.half) ^ swz(r)) << 4));
-                    o[0] = fp8x8_to_bf16x8(u32x2{v[0], v[1]}, 1.0f);
-                    o[1] = fp8x8_to_bf16x8(u32x2{v[2], v[3]}, 1.0f);
-                };
 #pragma unroll
-                for (int n = 0; n < NJ; ++n) read(sl, wn * NJ + n, w[n]);
+                for (int n = 0; n < NJ; ++n) {
+                    const u32x4 v = read(rdw, n, q);
+                    w[n][0] = fp8x8_to_bf16x8(u32x2{v[0], v[1]}, 1.0f);
+                    w[n][1] = fp8x8_to_bf16x8(u32x2{v[2], v[3]}, 1.0f);
+                }
 #pragma unroll
-                for (int i = 0; i < MI; ++i) read(sla, wm * MI + i, a[i]);
+                for (int i = 0; i < MI; ++i) {
+                    const u32x4 v = read(rda, i, q);
+                    a[i][0] = fp8x8_to_bf16x8(u32x2{v[0], v[1]}, 1.0f);
+                    a[i][1] = fp8x8_to_bf16x8(u32x2{v[2], v[3]}, 1.0f);
+                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -212,19 +246,15 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t,
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 v8i a[MI], w[NJ];
-                auto read = [&](const unsigned char* b, int blk) {
-                    const int r = blk * 32 + t.l32;
-                    const u32x4 lo =
-                        *(const u32x4*)(b + r * BK + (((4 * s + t.half) ^ swz(r)) << 4));
-                    const u32x4 hi =
-                        *(const u32x4*)(b + r * BK + (((4 * s + 2 + t.half) ^ swz(r)) << 4));
+                auto pair = [&](int at, int blk) {
+                    const u32x4 lo = read(at, blk, 2 * s), hi = read(at, blk, 2 * s + 1);
                     return v8i{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
                                (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
                 };
 #pragma unroll
-                for (int n = 0; n < NJ; ++n) w[n] = read(sl, wn * NJ + n);
+                for (int n = 0; n < NJ; ++n) w[n] = pair(rdw, n);
 #pragma unroll
-                for (int i = 0; i < MI; ++i) a[i] = read(sla, wm * MI + i);
+                for (int i = 0; i < MI; ++i) a[i] = pair(rda, i);
 #pragma unroll
                 for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -281,13 +311,9 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t,
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const int col = (wn * NJ + n) * 32 + 8 * q + 4 * t.half;
-                    uint32_t v[2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        v[h] = (uint32_t)f32_to_bf16(acc[i][n][4 * q + 2 * h]) |
-                               ((uint32_t)f32_to_bf16(acc[i][n][4 * q + 2 * h + 1]) << 16);
                     *(u32x2*)(ring + ((wm * MI + i) * 32 + t.l32) * kRowBf16 + col * 2) =
-                        u32x2{v[0], v[1]};
+                        u32x2{bf16_pack2(acc[i][n][4 * q], acc[i][n][4 * q + 1]),
+                              bf16_pack2(acc[i][n][4 * q + 2], acc[i][n][4 * q + 3])};
                 }
         __syncthreads();
         const int col = 8 * t.l32;
