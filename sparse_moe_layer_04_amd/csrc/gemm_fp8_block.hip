@@ -23,10 +23,12 @@
 //
 // Tile: up to 128 rows x 256 weight rows (SwiGLU: 128 features, gate and up
 // rows interleaved by 16 so that a wave holds both of a feature), 8 waves,
-// one 128-wide block of K a stage.  Both operands go through a 2-slot LDS
+// one 128-wide block of K a stage.  Both operands go through a 3-slot LDS
 // ring as codes (48 KB a stage): a wave's 64 lanes load 8 rows x 128 bytes
-// (whole lines of the row-major operands), two stages ahead of the matrix
-// products in registers, one stage ahead in LDS, one barrier a stage.
+// (whole lines of the row-major operands) into registers a stage before they
+// go to LDS, which is two stages before they are multiplied, so that the
+// operand reads can run one step ahead of the matrix products all the way
+// through; one barrier a stage.
 // LDS row r holds its 16-byte chunk c at c ^ ((r >> 1) & 7), so that the
 // lanes of an operand read (32 rows, one chunk index) spread over the banks.
 #include <type_traits>
@@ -40,6 +42,7 @@ constexpr int BM = 128;                    // rows a tile
 constexpr int BN = 256;                    // weight rows a tile
 constexpr int BK = 128;                    // K a stage: one block
 constexpr int kThreads = 512;
+constexpr int kEntries = 1024;             // of the group table in LDS
 constexpr int kSlotW = BN * BK;
 constexpr int kSlot = (BN + BM) * BK;
 constexpr int kRing = 2 * kSlot;
@@ -74,7 +77,7 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t,
     // waves: WM along the rows x WN along the weight rows, each MI x NJ
     // blocks of 32 x 32
     constexpr int WM = MB == 4 ? 2 : 1, WN = 8 / WM, MI = MB / WM, NJ = 8 / WN;
-    constexpr int NA = MB == 4 ? 2 : 1;    // row loads a thread and stage
+    constexpr int NA = (MB + 1) / 2;       // row loads a thread and stage
     constexpr bool SW = EPI == FP8_SWIGLU;
     constexpr bool EXACT = EPI != FP8_OUT_BF16;
     const int wm = t.wave / WN, wn = t.wave % WN;
@@ -104,49 +107,40 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t,
         wo[q] = min(SW ? 16 * (R >> 5) + (R & 15) : R, wrows - 1) * K + 16 * c;
     }
 #pragma unroll
-    for (int q = 0; q < NA; ++q) ao[q] = min(lr + 64 * q, t.valid - 1) * K + 16 * c;
-    // bytes that this thread's chunk of the last stage reaches past K
-    const int past = max(0, (S - 1) * BK + 16 * c + 16 - K);
-    const bool loads_a = MB > 1 || t.wave < 4;      // (32 rows: the first four waves)
-    unsigned char* st = ring + lr * BK + ((c ^ swz(lr)) << 4);
+    for (int q = 0; q < NA; ++q) {
+        // (an odd number of blocks: the last 32 rows twice, the same bytes to
+        // the same place, so that no wave branches off)
+        const int R = (MB % 2 && q == NA - 1 ? lr & 31 : lr) + 64 * q;
+        ao[q] = min(R, t.valid - 1) * K + 16 * c;
+    }
+    // a chunk past the end of K, in the last stage: an offset past the
+    // resource, which loads zeros
+    const int past = (S - 1) * BK + 16 * c >= K ? (int)0x80000000 : 0;
+    const int st = lr * BK + ((c ^ swz(lr)) << 4);
+    const int st_last = (MB % 2 ? lr & 31 : lr) * BK + ((c ^ swz(lr)) << 4);
     const int rd0 = t.l32 * BK + ((t.half ^ swz(t.l32)) << 4);
     const int rdw = wn * NJ * 32 * BK + rd0;
     const int rda = kSlotW + wm * MI * 32 * BK + rd0;
 
-    u32x4 wr[2][4], ar[2][NA];
-    auto load = [&](int j, auto set) {
-        constexpr int P = decltype(set)::value;
+    u32x4 wr[4], ar[NA];
+    auto load = [&](int j) {
         const int k = min(j, S - 1) * BK;
-        const int back = j >= S - 1 ? past : 0;     // (a chunk past K: the row's last one)
+        const int o = j >= S - 1 ? past : 0;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            wr[P][q] = __builtin_bit_cast(
-                u32x4, __builtin_amdgcn_raw_buffer_load_b128(wsrc, wo[q] - back, k, 0));
-        if (loads_a) {
+            wr[q] = __builtin_bit_cast(
+                u32x4, __builtin_amdgcn_raw_buffer_load_b128(wsrc, wo[q] | o, k, 0));
 #pragma unroll
-            for (int q = 0; q < NA; ++q)
-                ar[P][q] = __builtin_bit_cast(
-                    u32x4, __builtin_amdgcn_raw_buffer_load_b128(asrc, ao[q] - back, k, 0));
-        }
+        for (int q = 0; q < NA; ++q)
+            ar[q] = __builtin_bit_cast(
+                u32x4, __builtin_amdgcn_raw_buffer_load_b128(asrc, ao[q] | o, k, 0));
     };
-    auto store = [&](int j, auto set) {
-        constexpr int P = decltype(set)::value;
-        unsigned char* slot = st + P * kSlot;
-        if (j == S - 1 && K % BK) {                 // the short last block: zeros past K
-            const u32x4 z = {0u, 0u, 0u, 0u};
+    auto store = [&](int at) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) wr[P][q] = past ? z : wr[P][q];
-            if (loads_a) {
+        for (int q = 0; q < 4; ++q) *(u32x4*)(ring + st + at + q * 64 * BK) = wr[q];
 #pragma unroll
-                for (int q = 0; q < NA; ++q) ar[P][q] = past ? z : ar[P][q];
-            }
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) *(u32x4*)(slot + q * 64 * BK) = wr[P][q];
-        if (loads_a) {
-#pragma unroll
-            for (int q = 0; q < NA; ++q) *(u32x4*)(slot + kSlotW + q * 64 * BK) = ar[P][q];
-        }
+        for (int q = 0; q < NA; ++q)
+            *(u32x4*)(ring + (q == NA - 1 ? st_last : st) + at + kSlotW + q * 64 * BK) = ar[q];
     };
 
     // scales: this lane's rows, and the 128-block of this wave's weight rows
@@ -163,7 +157,7 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t,
     const __amdgpu_buffer_rsrc_t s1src = uniform_rsrc(p.s1 + sfirst, (size_t)S * 4);
     const __amdgpu_buffer_rsrc_t s2src =
         uniform_rsrc((SW ? p.s2 : p.s1) + sfirst, (size_t)S * 4);
-    float sa[MI], sw1, sw2;
+    float sa[MI] = {}, sw1 = 0.0f, sw2 = 0.0f;
     auto load_s = [&](int j) {
         const int k = min(j, S - 1) * 4;
 #pragma unroll
@@ -184,99 +178,183 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t,
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][n][e] = 0.0f;
 
-    using I0 = std::integral_constant<int, 0>;
-    using I1 = std::integral_constant<int, 1>;
-    load(0, I0());
-    load_s(0);
-    load(1, I1());
-    store(0, I0());
-
-    auto stage = [&](int j, auto par) {
-        constexpr int P = decltype(par)::value;      // j % 2
-        __syncthreads();                             // slot P holds block j
-        float s1[MI], s2[MI];
+    // The stage's pipeline, in steps of 16 (bf16) or 64 (8-bit) of K.  In a
+    // step the matrix cores take the operands made ready in the step before,
+    // the vector units decode the next step's and, in the stage's first one,
+    // scale and add the sums of the block before (tile by tile, ahead of the
+    // product that starts the tile's new block), and LDS reads run two (one)
+    // steps ahead.  The barrier stands where the last reads of block j have
+    // been issued and the first of block j + 1 are next.
+    f32x16 part[MI][NJ];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int n = 0; n < NJ; ++n)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) part[i][n][e] = 0.0f;
+    float s1[MI], s2[MI];
+    auto scales = [&]() {
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
             s1[i] = sa[i] * sw1;
             s2[i] = sa[i] * sw2;
         }
-        // (the scales before the operands: the memory counter is in order, and
-        // what is needed at the next stage must not wait for the one after)
-        load_s(j + 1);
-        load(j + 2, par);
-        f32x16 part[MI][NJ];
+    };
+    auto add_part = [&](int i, int n) {
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
+        for (int e = 0; e < 16; ++e)
+            acc[i][n][e] =
+                __builtin_fmaf(part[i][n][e], SW && e >= 8 ? s2[i] : s1[i], acc[i][n][e]);
+    };
+    f32x16 zero;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) zero[e] = 0.0f;
+    constexpr int NT = MI * NJ;
+
+    load(0);
+    store(0);
+    load(1);
+    __syncthreads();
+
+    if constexpr (EXACT) {
+        u32x4 rw[2][NJ], ra[2][MI];        // 32 of K: the codes of two steps
+        bf16x8 w[2][NJ], a[2][MI];         // operands of a step
+        auto read = [&](int slot, int q, auto set) {
+            constexpr int B = decltype(set)::value;
 #pragma unroll
             for (int n = 0; n < NJ; ++n)
+                rw[B][n] = *(const u32x4*)(ring + ((rdw + slot) ^ (q << 5)) + n * 32 * BK);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) part[i][n][e] = 0.0f;
-        // 16 codes: chunk pair q of block blk's rows
-        auto read = [&](int at, int blk, int q) {
-            return *(const u32x4*)(ring + (at ^ (q << 5)) + P * kSlot + blk * 32 * BK);
+            for (int i = 0; i < MI; ++i)
+                ra[B][i] = *(const u32x4*)(ring + ((rda + slot) ^ (q << 5)) + i * 32 * BK);
         };
-        if constexpr (EXACT) {
-            // 16 codes a lane and chunk pair: two 16-wide bf16 steps
+        // step h of the block from raw set h / 2 % 2 into operand set h % 2
+        auto decode = [&](auto step) {
+            constexpr int h = decltype(step)::value, B = (h >> 1) & 1, o = 2 * (h & 1);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                bf16x8 a[MI][2], w[NJ][2];
+            for (int n = 0; n < NJ; ++n)
+                w[h & 1][n] = fp8x8_to_bf16x8(u32x2{rw[B][n][o], rw[B][n][o + 1]}, 1.0f);
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+                a[h & 1][i] = fp8x8_to_bf16x8(u32x2{ra[B][i][o], ra[B][i][o + 1]}, 1.0f);
+        };
+        auto multiply = [&](auto step) {
+            constexpr int h = decltype(step)::value;
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
 #pragma unroll
                 for (int n = 0; n < NJ; ++n) {
-                    const u32x4 v = read(rdw, n, q);
-                    w[n][0] = fp8x8_to_bf16x8(u32x2{v[0], v[1]}, 1.0f);
-                    w[n][1] = fp8x8_to_bf16x8(u32x2{v[2], v[3]}, 1.0f);
+                    if constexpr (h == 0) add_part(i, n);
+                    part[i][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        w[h & 1][n], a[h & 1][i], h == 0 ? zero : part[i][n], 0, 0, 0);
                 }
+        };
+        using std::integral_constant;
+        auto step = [&](auto st) {
+            constexpr int h = decltype(st)::value;
+            decode(integral_constant<int, (h + 1) & 7>());
+            multiply(st);
+            // one product, then its share of the vector instructions
+            constexpr int V = 4 * (MI + NJ) / NT + (h == 0 ? 16 : 0);
 #pragma unroll
-                for (int i = 0; i < MI; ++i) {
-                    const u32x4 v = read(rda, i, q);
-                    a[i][0] = fp8x8_to_bf16x8(u32x2{v[0], v[1]}, 1.0f);
-                    a[i][1] = fp8x8_to_bf16x8(u32x2{v[2], v[3]}, 1.0f);
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int i = 0; i < MI; ++i)
-#pragma unroll
-                        for (int n = 0; n < NJ; ++n)
-                            part[i][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                                w[n][h], a[i][h], part[i][n], 0, 0, 0);
+            for (int i = 0; i < NT; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x002, h == 0 ? V : 0, 0);
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, h == 0 ? 0 : V, 0);
             }
-        } else {
-            // (any order of K within the block will do, the same for both)
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        using H0 = integral_constant<int, 0>;
+        using H1 = integral_constant<int, 1>;
+        read(0, 0, H0());
+        read(0, 1, H1());
+        decode(H0());
+        int slot = 0;
+        for (int j = 0; j < S; ++j) {
+            const int next = kSlot - slot;
+            scales();                               // of block j - 1
+            load_s(j);
+            step(H0());
+            read(slot, 2, H0());
+            step(H1());
+            step(integral_constant<int, 2>());
+            read(slot, 3, H1());
+            store(next);                            // block j + 1 (past the end: not used)
+            step(integral_constant<int, 3>());
+            load(j + 2);
+            step(integral_constant<int, 4>());
+            __syncthreads();
+            read(next, 0, H0());
+            step(integral_constant<int, 5>());
+            step(integral_constant<int, 6>());
+            read(next, 1, H1());
+            step(integral_constant<int, 7>());
+            slot = next;
+        }
+    } else {
+        // (any order of K within the block will do, the same for both)
+        u32x4 rw[2][NJ][2], ra[2][MI][2];
+        auto read = [&](int slot, auto set) {
+            constexpr int B = decltype(set)::value;
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                v8i a[MI], w[NJ];
-                auto pair = [&](int at, int blk) {
-                    const u32x4 lo = read(at, blk, 2 * s), hi = read(at, blk, 2 * s + 1);
-                    return v8i{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
-                               (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
-                };
+            for (int r = 0; r < 2; ++r) {
 #pragma unroll
-                for (int n = 0; n < NJ; ++n) w[n] = pair(rdw, n);
-#pragma unroll
-                for (int i = 0; i < MI; ++i) a[i] = pair(rda, i);
+                for (int n = 0; n < NJ; ++n)
+                    rw[B][n][r] =
+                        *(const u32x4*)(ring + ((rdw + slot) ^ ((2 * B + r) << 5)) + n * 32 * BK);
 #pragma unroll
                 for (int i = 0; i < MI; ++i)
-#pragma unroll
-                    for (int n = 0; n < NJ; ++n)
-                        part[i][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                            w[n], a[i], part[i][n], 0, 0, 0, 127, 0, 127);
+                    ra[B][i][r] =
+                        *(const u32x4*)(ring + ((rda + slot) ^ ((2 * B + r) << 5)) + i * 32 * BK);
             }
+        };
+        auto cat = [](const u32x4 (&r)[2]) {
+            return v8i{(int)r[0][0], (int)r[0][1], (int)r[0][2], (int)r[0][3],
+                       (int)r[1][0], (int)r[1][1], (int)r[1][2], (int)r[1][3]};
+        };
+        auto multiply = [&](auto set) {
+            constexpr int B = decltype(set)::value;
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int n = 0; n < NJ; ++n) {
+                    if constexpr (B == 0) add_part(i, n);
+                    part[i][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                        cat(rw[B][n]), cat(ra[B][i]), B == 0 ? zero : part[i][n], 0, 0, 0, 127, 0,
+                        127);
+                }
+            if constexpr (B == 0) {
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x002, 16, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        using B0 = std::integral_constant<int, 0>;
+        using B1 = std::integral_constant<int, 1>;
+        read(0, B0());
+        int slot = 0;
+        for (int j = 0; j < S; ++j) {
+            const int next = kSlot - slot;
+            scales();                               // of block j - 1
+            load_s(j);
+            read(slot, B1());
+            multiply(B0());
+            store(next);                            // block j + 1 (past the end: not used)
+            load(j + 2);
+            __syncthreads();
+            read(next, B0());
+            multiply(B1());
+            slot = next;
         }
-#pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-            for (int n = 0; n < NJ; ++n)
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    acc[i][n][e] =
-                        __builtin_fmaf(part[i][n][e], SW && e >= 8 ? s2[i] : s1[i], acc[i][n][e]);
-        if (j + 1 < S) store(j + 1, std::integral_constant<int, P ^ 1>());
-    };
-    for (int j = 0; j < S; j += 2) {
-        stage(j, I0());
-        if (j + 1 < S) stage(j + 1, I1());
     }
+    scales();
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int n = 0; n < NJ; ++n) add_part(i, n);
 
     // Epilogues: lane l holds, of row l % 32 of its block, weight rows
     // 8 (e / 4) + 4 (l / 32) + e % 4; through LDS into whole-line stores.
@@ -391,21 +469,28 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_block_kernel(Fp8GemmArgs p)
     t.half = t.lane >> 5;
     t.l32 = t.lane & 31;
     const int G = p.G, rows = p.rows;
-    int* prefix = (int*)(smem + kRing);              // [G + 1] items before group g
+    // [entries + 1] items before each run of `run` groups (a run: what a
+    // table of kEntries entries asks for)
+    int* prefix = (int*)(smem + kRing);
+    const int run = (G + kEntries - 1) / kEntries, entries = (G + run - 1) / run;
     const int NT = (p.N + TN - 1) / TN;
     auto group_rows = [&](int g, int& lo, int& hi) {
         lo = min(max(p.offsets[g], 0), rows);
         hi = max(lo, min(max(p.offsets[g + 1], 0), rows));
     };
+    auto group_items = [&](int g) {
+        int lo, hi;
+        group_rows(g, lo, hi);
+        return NT * ((hi - lo + BM - 1) / BM);
+    };
     {
-        const int per = (G + kThreads - 1) / kThreads;
-        const int g0 = t.tid * per;
+        const int per = (entries + kThreads - 1) / kThreads;
+        const int e0 = t.tid * per;
         int local = 0;
-        for (int g = g0; g < g0 + per && g < G; ++g) {
-            int lo, hi;
-            group_rows(g, lo, hi);
-            const int items = NT * ((hi - lo + BM - 1) / BM);
-            prefix[g] = items;
+        for (int e = e0; e < e0 + per && e < entries; ++e) {
+            int items = 0;
+            for (int g = e * run; g < (e + 1) * run && g < G; ++g) items += group_items(g);
+            prefix[e] = items;
             local += items;
         }
         int x = local;
@@ -421,35 +506,42 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_block_kernel(Fp8GemmArgs p)
             if (w < t.wave) before += scan_sh[w];
             total += scan_sh[w];
         }
-        int run = before + x - local;
-        for (int g = g0; g < g0 + per && g < G; ++g) {
-            const int v = prefix[g];
-            prefix[g] = run;
-            run += v;
+        int sum = before + x - local;
+        for (int e = e0; e < e0 + per && e < entries; ++e) {
+            const int v = prefix[e];
+            prefix[e] = sum;
+            sum += v;
         }
-        if (t.tid == 0) prefix[G] = total;
+        if (t.tid == 0) prefix[entries] = total;
         __syncthreads();
     }
-    const long long Q = prefix[G];
+    const long long Q = prefix[entries];
     const int xcd = blockIdx.x & 7;
     const int hi_item = (int)(Q * (xcd + 1) / 8);
     for (int q = (int)(Q * xcd / 8) + (int)(blockIdx.x >> 3); q < hi_item; q += gridDim.x >> 3) {
-        int lo = 0, hi = G;
-        while (lo < hi) {                            // the last g with prefix[g] <= q
+        int lo = 0, hi = entries;
+        while (lo < hi) {                            // the last entry with prefix <= q
             const int mid = (lo + hi + 1) >> 1;
             if (prefix[mid] <= q) lo = mid; else hi = mid - 1;
         }
-        t.g = __builtin_amdgcn_readfirstlane(lo);
+        int local = q - prefix[lo], g = lo * run;
+        for (;; ++g) {                               // (ends: the entry holds item q)
+            const int items = group_items(g);
+            if (local < items) break;
+            local -= items;
+        }
+        t.g = __builtin_amdgcn_readfirstlane(g);
         int r0, r1;
         group_rows(t.g, r0, r1);
         const int n = r1 - r0, mt = (n + BM - 1) / BM;
         const int per = ((n + mt - 1) / mt + 31) & ~31;
-        const int local = q - prefix[t.g];
         t.n0 = local / mt * TN;
         t.row0 = r0 + local % mt * per;
         t.valid = min(per, r1 - t.row0);
-        if (t.valid > 64)
+        if (t.valid > 96)
             run_tile<EPI, 4>(p, t, smem);
+        else if (t.valid > 64)
+            run_tile<EPI, 3>(p, t, smem);
         else if (t.valid > 32)
             run_tile<EPI, 2>(p, t, smem);
         else
@@ -477,7 +569,7 @@ hipError_t launch(const Fp8GemmArgs& g, hipStream_t stream) {
             return hipSuccess;
         });
     if (err != hipSuccess) return err;
-    const size_t lds = kRing + (size_t)(g.G + 1) * sizeof(int);
+    const size_t lds = kRing + (kEntries + 1) * sizeof(int);
     if (lds + (size_t)static_lds > (size_t)kLdsLimit) return hipErrorInvalidValue;
     hipLaunchKernelGGL((gemm_fp8_block_kernel<EPI>), dim3((unsigned)grid), dim3(kThreads),
                        lds, stream, g);
