@@ -38,32 +38,71 @@
 namespace moe {
 namespace {
 
-constexpr int BM = 128;                    // rows a tile
+constexpr int BM = 128;                    // rows a tile, at most
+constexpr int kSplitM = 128;               // rows a tile of a larger group
 constexpr int BN = 256;                    // weight rows a tile
 constexpr int BK = 128;                    // K a stage: one block
 constexpr int kThreads = 512;
-constexpr int kEntries = 1024;             // of the group table in LDS
 constexpr int kSlotW = BN * BK;
-constexpr int kSlot = (BN + BM) * BK;
-constexpr int kRing = 2 * kSlot;
-constexpr int kLdsLimit = 160 * 1024;
-constexpr int kStaticLds = 256;
+constexpr int kSlotS = kSlotW + BM * BK;   // the stage's scales: the rows' (3 x 64
+constexpr int kSlot = kSlotS + 1024;       // words), then two of the weights
+constexpr int kSlots = 3;
+constexpr int kLds = kSlots * kSlot;
+static_assert(kLds <= 160 * 1024 && kSlot % 128 == 0, "three slots of LDS");
 constexpr int kRowF32 = BN * 4 + 16;       // epilogue staging rows, padded
 constexpr int kRowBf16 = BN * 2 + 16;
 constexpr int kRowH = 128 + 16;
-static_assert(64 * kRowF32 <= kRing && BM * kRowBf16 <= kRing, "epilogue staging fits the ring");
+static_assert(64 * kRowF32 <= kLds && BM * kRowBf16 <= kLds, "epilogue staging fits");
+
+// Copies from memory into LDS that pass no register: lane l's 16 (4) bytes go
+// to LDS byte lds + 16 l (4 l), lds wave-uniform.  M0 carries the LDS address
+// when the copy issues (one wait state after the write); the compiler may
+// keep a value of its own there, so each block leaves M0 as it found it.  The
+// compiler does not count these copies: wait_vm does.
+__device__ __forceinline__ void copy16(u32x4 rsrc, int voffset, int soffset, int lds) {
+    const int at = __builtin_amdgcn_readfirstlane(lds);
+    int saved;
+    asm volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %1\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %2, %3, %4 offen lds\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(saved)
+        : "s"(at), "v"(voffset), "s"(rsrc), "s"(soffset)
+        : "memory");
+}
+__device__ __forceinline__ void copy4(const void* from, int lds) {
+    const int at = __builtin_amdgcn_readfirstlane(lds);
+    int saved;
+    asm volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %1\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dword %2, off\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(saved)
+        : "s"(at), "v"(from)
+        : "memory");
+}
+// at most N of this wave's memory operations outstanding
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
 
 __device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
 
 // Buffer resource over [base, base + bytes), wave-uniform (read from the
 // first lane, so that it lives in scalar registers)
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void* base, size_t bytes) {
+__device__ __forceinline__ u32x4 uniform_rsrc(const void* base, size_t bytes) {
     const uint64_t p = (uint64_t)(uintptr_t)base;
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)p);
-    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32));
-    const int n = __builtin_amdgcn_readfirstlane((int)min(bytes, (size_t)0x7fffffff));
-    return __builtin_amdgcn_make_buffer_rsrc((void*)(uintptr_t)(((uint64_t)hi << 32) | lo), 0, n,
-                                             0x00020000);
+    u32x4 r;
+    r[0] = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)p);
+    r[1] = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32)) & 0xffffu;
+    r[2] = (uint32_t)__builtin_amdgcn_readfirstlane((int)min(bytes, (size_t)0x7fffffff));
+    r[3] = 0x00020000u;
+    return r;
 }
 
 struct Tile {
@@ -72,8 +111,13 @@ struct Tile {
 };
 
 template <int EPI, int MB>
-__device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t,
-                                         unsigned char* ring) {
+__device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, Tile t, unsigned char* ring) {
+    // (the thread's place as a value of this variant's own: address terms
+    // shared by the variants would be kept, or spilled, for all of them)
+    asm volatile("" : "+v"(t.tid));
+    t.lane = t.tid & 63;
+    t.half = t.lane >> 5;
+    t.l32 = t.lane & 31;
     // waves: WM along the rows x WN along the weight rows, each MI x NJ
     // blocks of 32 x 32
     constexpr int WM = MB == 4 ? 2 : 1, WN = 8 / WM, MI = MB / WM, NJ = 8 / WN;
@@ -85,89 +129,88 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t,
     const int S = (K + BK - 1) / BK;
     const int nbn = (N + 127) / 128;
 
-    // Addresses.  Loads go through buffer resources over the tile's rows
+    // Addresses.  Copies go through buffer resources over the tile's rows
     // (wave-uniform base, 32-bit offsets), rows past the tile's or the
-    // matrix's end clamped to the last.  LDS rows 64 (loads) or 32 (operand
-    // reads) apart share their swizzle, so the rest of an LDS address is an
-    // immediate; the chunk index enters it by exclusive or.
-    const int c = t.tid & 7, lr = t.tid >> 3;       // loads: chunk c of row lr + 64 q
+    // matrix's end clamped to the last.  A wave's copy fills 8 LDS rows of 128
+    // bytes; the place of a chunk in its row is swizzled, so the lanes fetch
+    // swizzled chunks.  LDS rows 32 apart share their swizzle, so the rest of
+    // an operand's address is an immediate; the chunk index enters it by
+    // exclusive or.
+    const int lr = t.tid >> 3, c = (t.tid & 7) ^ swz(lr);   // chunk c of row lr + 64 q
     // SwiGLU: LDS row R is row R & 15 of 16 features' gate (R & 16 == 0) or up
     // rows; R & 16 is the same for a wave and all q
     const bool up = SW && (t.wave & 2);
     const size_t wfirst = ((size_t)t.g * N + t.n0) * K;
     const int wrows = N - t.n0;                     // (>= 1)
-    const __amdgpu_buffer_rsrc_t wsrc =
-        uniform_rsrc((up ? p.w2 : p.w1) + wfirst, (size_t)min(wrows, BN) * K);
-    const __amdgpu_buffer_rsrc_t asrc =
-        uniform_rsrc(p.a + (size_t)t.row0 * K, (size_t)t.valid * K);
+    const u32x4 wsrc = uniform_rsrc((up ? p.w2 : p.w1) + wfirst, (size_t)min(wrows, BN) * K);
+    const u32x4 asrc = uniform_rsrc(p.a + (size_t)t.row0 * K, (size_t)t.valid * K);
+    // (a chunk past the end of K in the last block: the row's last chunk,
+    // overwritten by zeros before it is read)
+    const int past = max(0, (S - 1) * BK + 16 * c + 16 - K);
     int wo[4], ao[NA];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         const int R = lr + 64 * q;
         wo[q] = min(SW ? 16 * (R >> 5) + (R & 15) : R, wrows - 1) * K + 16 * c;
     }
+    // (an odd number of blocks: the last 32 rows twice, the same bytes to the
+    // same place, so that every wave issues the same number of copies)
+    constexpr int kLastMask = MB % 2 ? 31 : 63;
 #pragma unroll
     for (int q = 0; q < NA; ++q) {
-        // (an odd number of blocks: the last 32 rows twice, the same bytes to
-        // the same place, so that no wave branches off)
-        const int R = (MB % 2 && q == NA - 1 ? lr & 31 : lr) + 64 * q;
+        const int R = (q == NA - 1 ? lr & kLastMask : lr) + 64 * q;
         ao[q] = min(R, t.valid - 1) * K + 16 * c;
     }
-    // a chunk past the end of K, in the last stage: an offset past the
-    // resource, which loads zeros
-    const int past = (S - 1) * BK + 16 * c >= K ? (int)0x80000000 : 0;
-    const int st = lr * BK + ((c ^ swz(lr)) << 4);
-    const int st_last = (MB % 2 ? lr & 31 : lr) * BK + ((c ^ swz(lr)) << 4);
+    const int last_wave = t.wave & (kLastMask >> 3);
+    // scales: waves 0 to 2 fetch the rows', the others (the same ones) the
+    // weights' of the tile's two 128-blocks of rows, or of gate and up
+    const int nb0 = t.n0 / 128;
+    const float* sp;
+    if (t.wave < 3) {
+        sp = p.as + (size_t)(t.row0 + min(64 * t.wave + t.lane, t.valid - 1)) * S;
+    } else if constexpr (SW) {
+        sp = (t.lane & 1 ? p.s2 : p.s1) + ((size_t)t.g * nbn + nb0) * S;
+    } else {
+        sp = p.s1 + ((size_t)t.g * nbn + min(nb0 + (t.lane & 1), nbn - 1)) * S;
+    }
+    constexpr int NI = 4 + NA + 1;                  // copies a wave and stage
+    // Stage 0 takes K's last block, the short one if any, stage j block j - 1.
+    // (Every stage issues its copies: past the last stage with offsets past
+    // the resources, which fetch nothing.)
+    auto fetch = [&](int j, int at) {
+        const int b = j == 0 ? S - 1 : min(j, S) - 1;
+        const int back = j == 0 ? past : 0, out = j < S ? 0 : (int)0x80000000;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            copy16(wsrc, (wo[q] - back) | out, b * BK, at + q * 64 * BK + t.wave * 1024);
+#pragma unroll
+        for (int q = 0; q < NA; ++q)
+            copy16(asrc, (ao[q] - back) | out, b * BK,
+                   at + kSlotW + q * 64 * BK + (q == NA - 1 ? last_wave : t.wave) * 1024);
+        copy4(sp + b, at + kSlotS + min(t.wave, 3) * 256);
+    };
+    // zeros over this thread's own copies past the end of K, once they landed
+    auto zero_past = [&]() {
+        if (!past) return;
+        const u32x4 z = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) *(u32x4*)(ring + q * 64 * BK + t.tid * 16) = z;
+#pragma unroll
+        for (int q = 0; q < NA; ++q)
+            *(u32x4*)(ring + kSlotW + q * 64 * BK +
+                      (q == NA - 1 ? last_wave * 1024 + t.lane * 16 : t.tid * 16)) = z;
+    };
     const int rd0 = t.l32 * BK + ((t.half ^ swz(t.l32)) << 4);
     const int rdw = wn * NJ * 32 * BK + rd0;
     const int rda = kSlotW + wm * MI * 32 * BK + rd0;
-
-    u32x4 wr[4], ar[NA];
-    auto load = [&](int j) {
-        const int k = min(j, S - 1) * BK;
-        const int o = j >= S - 1 ? past : 0;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            wr[q] = __builtin_bit_cast(
-                u32x4, __builtin_amdgcn_raw_buffer_load_b128(wsrc, wo[q] | o, k, 0));
-#pragma unroll
-        for (int q = 0; q < NA; ++q)
-            ar[q] = __builtin_bit_cast(
-                u32x4, __builtin_amdgcn_raw_buffer_load_b128(asrc, ao[q] | o, k, 0));
-    };
-    auto store = [&](int at) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) *(u32x4*)(ring + st + at + q * 64 * BK) = wr[q];
-#pragma unroll
-        for (int q = 0; q < NA; ++q)
-            *(u32x4*)(ring + (q == NA - 1 ? st_last : st) + at + kSlotW + q * 64 * BK) = ar[q];
-    };
-
-    // scales: this lane's rows, and the 128-block of this wave's weight rows
-    // (of gate and up); vector loads, whose counter is in order (a scalar
-    // load in flight would make every LDS wait a wait for it)
-    const __amdgpu_buffer_rsrc_t sasrc =
-        uniform_rsrc(p.as + (size_t)t.row0 * S, (size_t)t.valid * S * 4);
-    int so[MI];
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-        so[i] = min((wm * MI + i) * 32 + t.l32, t.valid - 1) * S * 4;
-    const int nblk = min((t.n0 + (SW ? 0 : wn * NJ * 32)) / 128, nbn - 1);
-    const size_t sfirst = ((size_t)t.g * nbn + nblk) * S;
-    const __amdgpu_buffer_rsrc_t s1src = uniform_rsrc(p.s1 + sfirst, (size_t)S * 4);
-    const __amdgpu_buffer_rsrc_t s2src =
-        uniform_rsrc((SW ? p.s2 : p.s1) + sfirst, (size_t)S * 4);
+    const int rds = kSlotS + (wm * MI * 32 + t.l32) * 4;
+    const int rdsw = kSlotS + 768 + (SW ? 0 : (t.n0 + wn * NJ * 32) / 128 - nb0) * 4;
     float sa[MI] = {}, sw1 = 0.0f, sw2 = 0.0f;
-    auto load_s = [&](int j) {
-        const int k = min(j, S - 1) * 4;
+    auto read_s = [&](int slot) {
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
-            sa[i] = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(sasrc, so[i], k, 0));
-        sw1 = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(s1src, 0, k, 0));
-        if constexpr (SW)
-            sw2 = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(s2src, 0, k, 0));
-        else
-            sw2 = sw1;
+        for (int i = 0; i < MI; ++i) sa[i] = *(const float*)(ring + rds + slot + i * 128);
+        sw1 = *(const float*)(ring + rdsw + slot);
+        sw2 = SW ? *(const float*)(ring + rdsw + slot + 4) : sw1;
     };
 
     f32x16 acc[MI][NJ];
@@ -211,10 +254,20 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t,
     for (int e = 0; e < 16; ++e) zero[e] = 0.0f;
     constexpr int NT = MI * NJ;
 
-    load(0);
-    store(0);
-    load(1);
+    // stages 0 to 2 on their way; stage 0 landed
+    fetch(0, 0);
+    fetch(1, kSlot);
+    fetch(2, 2 * kSlot);
+    wait_vm<2 * NI>();
+    zero_past();
     __syncthreads();
+    // The middle of stage j: stage j + 1's block has landed and every wave has
+    // read stage j's, whose slot takes stage j + 3's.
+    auto turn = [&](int j, int slot) {
+        wait_vm<NI>();
+        __syncthreads();
+        fetch(j + 3, slot);
+    };
 
     if constexpr (EXACT) {
         u32x4 rw[2][NJ], ra[2][MI];        // 32 of K: the codes of two steps
@@ -271,20 +324,18 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t,
         decode(H0());
         int slot = 0;
         for (int j = 0; j < S; ++j) {
-            const int next = kSlot - slot;
+            const int next = slot == 2 * kSlot ? 0 : slot + kSlot;
             scales();                               // of block j - 1
-            load_s(j);
+            read_s(slot);
             step(H0());
             read(slot, 2, H0());
             step(H1());
             step(integral_constant<int, 2>());
             read(slot, 3, H1());
-            store(next);                            // block j + 1 (past the end: not used)
             step(integral_constant<int, 3>());
-            load(j + 2);
             step(integral_constant<int, 4>());
-            __syncthreads();
-            read(next, 0, H0());
+            turn(j, slot);
+            read(next, 0, H0());                    // (past the end: not used)
             step(integral_constant<int, 5>());
             step(integral_constant<int, 6>());
             read(next, 1, H1());
@@ -337,15 +388,13 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t,
         read(0, B0());
         int slot = 0;
         for (int j = 0; j < S; ++j) {
-            const int next = kSlot - slot;
+            const int next = slot == 2 * kSlot ? 0 : slot + kSlot;
             scales();                               // of block j - 1
-            load_s(j);
+            read_s(slot);
             read(slot, B1());
             multiply(B0());
-            store(next);                            // block j + 1 (past the end: not used)
-            load(j + 2);
-            __syncthreads();
-            read(next, B0());
+            turn(j, slot);
+            read(next, B0());                       // (past the end: not used)
             multiply(B1());
             slot = next;
         }
@@ -358,6 +407,7 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t,
 
     // Epilogues: lane l holds, of row l % 32 of its block, weight rows
     // 8 (e / 4) + 4 (l / 32) + e % 4; through LDS into whole-line stores.
+    wait_vm<0>();
     __syncthreads();
     if constexpr (EPI == FP8_OUT_F32) {
 #pragma unroll
@@ -453,14 +503,33 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t,
     }
 }
 
-// Persistent grid, one workgroup a CU.  Items are (group, n-tile, m-tile),
-// the 8 XCDs take contiguous ranges, so that the m-tiles of a weight tile and
-// the n-tiles of a group's rows meet in one XCD's L2; a group's rows split
-// evenly over its ceil(n / 128) m-tiles.
+// Inclusive sum over the wave's lanes
+__device__ __forceinline__ int wave_scan(int x, int lane) {
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int y = __shfl_up(x, off, 64);
+        if (lane >= off) x += y;
+    }
+    return x;
+}
+
+// Row tiles of a group of n rows: one up to BM rows (a second one would fetch
+// the group's weights again), else of up to kSplitM rows each.
+__device__ __forceinline__ int row_tiles(int n) {
+    return n <= BM ? n > 0 : (n + kSplitM - 1) / kSplitM;
+}
+
+// Persistent grid, one workgroup a CU.  Items are (group, n-tile, m-tile), the
+// 8 XCDs take contiguous ranges, so that the m-tiles of a weight tile and the
+// n-tiles of a group's rows meet in one XCD's L2; a group's rows split evenly
+// over its m-tiles.  The group of an item comes from a two-level sum that
+// every wave keeps in registers: lane l holds the items before run l of
+// ceil(G / 64) groups, and looks into the run that holds the item.
+static_assert(MOE_MAX_GROUPS <= 64 * 64, "one lane a run, one lane a group of a run");
+
 template <int EPI>
 __global__ __launch_bounds__(kThreads) void gemm_fp8_block_kernel(Fp8GemmArgs p) {
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ int scan_sh[8];
     constexpr int TN = EPI == FP8_SWIGLU ? BN / 2 : BN;
     Tile t;
     t.tid = threadIdx.x;
@@ -469,83 +538,45 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_block_kernel(Fp8GemmArgs p)
     t.half = t.lane >> 5;
     t.l32 = t.lane & 31;
     const int G = p.G, rows = p.rows;
-    // [entries + 1] items before each run of `run` groups (a run: what a
-    // table of kEntries entries asks for)
-    int* prefix = (int*)(smem + kRing);
-    const int run = (G + kEntries - 1) / kEntries, entries = (G + run - 1) / run;
     const int NT = (p.N + TN - 1) / TN;
     auto group_rows = [&](int g, int& lo, int& hi) {
         lo = min(max(p.offsets[g], 0), rows);
         hi = max(lo, min(max(p.offsets[g + 1], 0), rows));
     };
     auto group_items = [&](int g) {
-        int lo, hi;
-        group_rows(g, lo, hi);
-        return NT * ((hi - lo + BM - 1) / BM);
+        int lo = 0, hi = 0;
+        if (g < G) group_rows(g, lo, hi);
+        return NT * row_tiles(hi - lo);
     };
-    {
-        const int per = (entries + kThreads - 1) / kThreads;
-        const int e0 = t.tid * per;
-        int local = 0;
-        for (int e = e0; e < e0 + per && e < entries; ++e) {
-            int items = 0;
-            for (int g = e * run; g < (e + 1) * run && g < G; ++g) items += group_items(g);
-            prefix[e] = items;
-            local += items;
-        }
-        int x = local;
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-            const int y = __shfl_up(x, off, 64);
-            if (t.lane >= off) x += y;
-        }
-        if (t.lane == 63) scan_sh[t.wave] = x;
-        __syncthreads();
-        int before = 0, total = 0;
-        for (int w = 0; w < 8; ++w) {
-            if (w < t.wave) before += scan_sh[w];
-            total += scan_sh[w];
-        }
-        int sum = before + x - local;
-        for (int e = e0; e < e0 + per && e < entries; ++e) {
-            const int v = prefix[e];
-            prefix[e] = sum;
-            sum += v;
-        }
-        if (t.tid == 0) prefix[entries] = total;
-        __syncthreads();
-    }
-    const long long Q = prefix[entries];
+    const int run = (G + 63) / 64;
+    int mine = 0;
+    for (int i = 0; i < run; ++i) mine += group_items(t.lane * run + i);
+    const int upto = wave_scan(mine, t.lane);
+    const long long Q = __builtin_amdgcn_readlane(upto, 63);
     const int xcd = blockIdx.x & 7;
     const int hi_item = (int)(Q * (xcd + 1) / 8);
     for (int q = (int)(Q * xcd / 8) + (int)(blockIdx.x >> 3); q < hi_item; q += gridDim.x >> 3) {
-        int lo = 0, hi = entries;
-        while (lo < hi) {                            // the last entry with prefix <= q
-            const int mid = (lo + hi + 1) >> 1;
-            if (prefix[mid] <= q) lo = mid; else hi = mid - 1;
-        }
-        int local = q - prefix[lo], g = lo * run;
-        for (;; ++g) {                               // (ends: the entry holds item q)
-            const int items = group_items(g);
-            if (local < items) break;
-            local -= items;
-        }
-        t.g = __builtin_amdgcn_readfirstlane(g);
+        // the first lane whose sum passes q, then the same within its run
+        const int r = __builtin_ctzll(__builtin_amdgcn_ballot_w64(upto > q));
+        int local = q - __builtin_amdgcn_readlane(upto - mine, r);
+        const int items = t.lane < run ? group_items(r * run + t.lane) : 0;
+        const int in_run = wave_scan(items, t.lane);
+        const int l = __builtin_ctzll(__builtin_amdgcn_ballot_w64(in_run > local));
+        local -= __builtin_amdgcn_readlane(in_run - items, l);
+        t.g = r * run + l;
         int r0, r1;
         group_rows(t.g, r0, r1);
-        const int n = r1 - r0, mt = (n + BM - 1) / BM;
+        const int n = r1 - r0, mt = row_tiles(n);
         const int per = ((n + mt - 1) / mt + 31) & ~31;
         t.n0 = local / mt * TN;
         t.row0 = r0 + local % mt * per;
         t.valid = min(per, r1 - t.row0);
-        if (t.valid > 96)
-            run_tile<EPI, 4>(p, t, smem);
-        else if (t.valid > 64)
-            run_tile<EPI, 3>(p, t, smem);
-        else if (t.valid > 32)
-            run_tile<EPI, 2>(p, t, smem);
-        else
-            run_tile<EPI, 1>(p, t, smem);
+        switch ((t.valid + 31) >> 5) {
+            case 1: run_tile<EPI, 1>(p, t, smem); break;
+            case 2: run_tile<EPI, 2>(p, t, smem); break;
+            case 3: run_tile<EPI, 3>(p, t, smem); break;
+            default: run_tile<EPI, 4>(p, t, smem); break;
+        }
         __syncthreads();                             // the ring is free again
     }
 }
@@ -553,26 +584,16 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_block_kernel(Fp8GemmArgs p)
 template <int EPI>
 hipError_t launch(const Fp8GemmArgs& g, hipStream_t stream) {
     static DeviceSetup setup;
-    long long grid = 0, static_lds = 0;
+    long long grid = 0, unused = 0;
     const hipError_t err =
-        device_setup(setup, grid, static_lds, [](int, long long& gr, long long& st) {
-            const void* fn = (const void*)gemm_fp8_block_kernel<EPI>;
-            hipFuncAttributes fa;
-            hipError_t e = hipFuncGetAttributes(&fa, fn);
-            if (e != hipSuccess) return e;
-            if (fa.sharedSizeBytes > (size_t)kStaticLds) return hipErrorInvalidValue;
-            e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                    kLdsLimit - (int)fa.sharedSizeBytes);
-            if (e != hipSuccess) return e;
-            st = (long long)fa.sharedSizeBytes;
+        device_setup(setup, grid, unused, [](int, long long& gr, long long&) {
             gr = (device_cu_count() + 7) & ~7;
-            return hipSuccess;
+            return hipFuncSetAttribute((const void*)gemm_fp8_block_kernel<EPI>,
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
         });
     if (err != hipSuccess) return err;
-    const size_t lds = kRing + (kEntries + 1) * sizeof(int);
-    if (lds + (size_t)static_lds > (size_t)kLdsLimit) return hipErrorInvalidValue;
     hipLaunchKernelGGL((gemm_fp8_block_kernel<EPI>), dim3((unsigned)grid), dim3(kThreads),
-                       lds, stream, g);
+                       kLds, stream, g);
     return hipGetLastError();
 }
 
