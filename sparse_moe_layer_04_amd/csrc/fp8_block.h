@@ -43,6 +43,13 @@ __device__ __forceinline__ uint32_t bf16_pack2(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
 }
 
+// lanes 0-31: a of lane l and of lane l + 32; lanes 32-63: b of lane l - 32
+// and of lane l
+__device__ __forceinline__ u32x2 swap_halves(uint32_t a, uint32_t b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    return u32x2{r[0], r[1]};
+}
+
 // maximum of v >= 0 over the 16 lanes of a DPP row, in every lane
 __device__ __forceinline__ float row16_max(float v) {
 #define MOE_DPP_MAX(CTRL)                                                                   \

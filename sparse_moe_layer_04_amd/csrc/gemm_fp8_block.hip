@@ -46,13 +46,11 @@ constexpr int kThreads = 512;
 constexpr int kSlotW = BN * BK;
 constexpr int kSlotS = kSlotW + BM * BK;   // the stage's scales: the rows' (3 x 64
 constexpr int kSlot = kSlotS + 1024;       // words), then two of the weights
-constexpr int kSlots = 3;
-constexpr int kLds = kSlots * kSlot;
+constexpr int kRing = 3 * kSlot;
+constexpr int kRowMax = 8 * BM * 4;        // SwiGLU: the waves' row maxima
+constexpr int kTable = 2048;               // offsets kept in LDS
+constexpr int kLds = kRing + kRowMax + kTable * 4;
 static_assert(kLds <= 160 * 1024 && kSlot % 128 == 0, "three slots of LDS");
-constexpr int kRowF32 = BN * 4 + 16;       // epilogue staging rows, padded
-constexpr int kRowBf16 = BN * 2 + 16;
-constexpr int kRowH = 128 + 16;
-static_assert(64 * kRowF32 <= kLds && BM * kRowBf16 <= kLds, "epilogue staging fits");
 
 // Copies from memory into LDS that pass no register: lane l's 16 (4) bytes go
 // to LDS byte lds + 16 l (4 l), lds wave-uniform.  M0 carries the LDS address
@@ -106,105 +104,113 @@ __device__ __forceinline__ u32x4 uniform_rsrc(const void* base, size_t bytes) {
 }
 
 struct Tile {
-    int tid, lane, wave, half, l32;
     int g, row0, valid, n0;                // n0: first weight row (SwiGLU: feature)
 };
 
+// The copies of a tile's operands into LDS, set up once per tile: buffer
+// resources over the tile's rows (wave-uniform base, 32-bit offsets; rows past
+// the tile's or the matrix's end lie past them and fetch nothing).  A wave's
+// copy fills 8 LDS rows of 128 bytes; the place of a chunk in its row is
+// swizzled, so the lanes fetch swizzled chunks.
+constexpr int kCopies = 7;                 // copies a wave and stage: 4 W, 2 A, scales
+constexpr int kEarly = 3;                  // of them, issued in the stage before
+template <int EPI>
+struct Fetch {
+    u32x4 wsrc, asrc;
+    int wo[4], ao[2];
+    const float* sp;
+
+    __device__ __forceinline__ void set(const Fp8GemmArgs& p, const Tile& t) {
+        constexpr bool SW = EPI == FP8_SWIGLU;
+        const int tid = threadIdx.x, lane = tid & 63;
+        const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const int K = p.K, N = p.N, S = (K + BK - 1) / BK, nbn = (N + 127) / 128;
+        const int lr = tid >> 3, c = (tid & 7) ^ swz(lr);   // chunk c of row lr + 64 q
+        // SwiGLU: LDS row R is row R & 15 of 16 features' gate (R & 16 == 0)
+        // or up rows; R & 16 is the same for a wave and all q
+        const bool up = SW && (wave & 2);
+        const size_t wfirst = ((size_t)t.g * N + t.n0) * K;
+        wsrc = uniform_rsrc((up ? p.w2 : p.w1) + wfirst, (size_t)min(N - t.n0, BN) * K);
+        asrc = uniform_rsrc(p.a + (size_t)t.row0 * K, (size_t)t.valid * K);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int R = lr + 64 * q;
+            wo[q] = (SW ? 16 * (R >> 5) + (R & 15) : R) * K + 16 * c;
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) ao[q] = (lr + 64 * q) * K + 16 * c;
+        // scales: waves 0 to 2 fetch the rows', the others (the same ones) the
+        // weights' of the tile's two 128-blocks of rows, or of gate and up
+        const int nb0 = t.n0 / 128;
+        if (wave < 3) {
+            sp = p.as + (size_t)(t.row0 + min(64 * wave + lane, t.valid - 1)) * S;
+        } else if constexpr (SW) {
+            sp = (lane & 1 ? p.s2 : p.s1) + ((size_t)t.g * nbn + nb0) * S;
+        } else {
+            sp = p.s1 + ((size_t)t.g * nbn + min(nb0 + (lane & 1), nbn - 1)) * S;
+        }
+    }
+
+    // Copy q (of kCopies) of stage j into the slot at LDS byte `at`.  Stage 0
+    // takes K's last block, the short one if any, stage j block j - 1.  (Every
+    // stage issues its copies: past the last stage with offsets past the
+    // resources.)  `past`: the bytes that this thread's chunk reaches past K in
+    // the last block; it fetches the row's last chunk instead, which is
+    // overwritten by zeros when it has landed.
+    __device__ __forceinline__ void copy(int q, int j, int S, int past, int at) const {
+        const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+        const int b = j == 0 ? S - 1 : min(j, S) - 1;
+        const int back = j == 0 ? past : 0, out = j < S ? 0 : (int)0x80000000;
+        if (q < 4)
+            copy16(wsrc, (wo[q] - back) | out, b * BK, at + q * 64 * BK + wave * 1024);
+        else if (q < 6)
+            copy16(asrc, (ao[q - 4] - back) | out, b * BK,
+                   at + kSlotW + (q - 4) * 64 * BK + wave * 1024);
+        else
+            copy4(sp + b, at + kSlotS + min(wave, 3) * 256);
+    }
+    template <int Q0, int Q1>
+    __device__ __forceinline__ void copies(int j, int S, int past, int at) const {
+#pragma unroll
+        for (int q = Q0; q < Q1; ++q) copy(q, j, S, past, at);
+    }
+    // what is on its way when a tile begins
+    __device__ __forceinline__ void first_stages(int S, int past) const {
+        copies<0, kCopies>(0, S, past, 0);
+        copies<0, kCopies>(1, S, past, kSlot);
+        copies<0, kEarly>(2, S, past, 2 * kSlot);
+    }
+};
+
+// One tile, whose first three stages are on their way into the ring; sends the
+// next tile's (if there are more) off before this one's results are written.
 template <int EPI, int MB>
-__device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, Tile t, unsigned char* ring) {
+__device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t, const Tile& next_t,
+                                         bool more, int past, unsigned char* ring) {
     // (the thread's place as a value of this variant's own: address terms
     // shared by the variants would be kept, or spilled, for all of them)
-    asm volatile("" : "+v"(t.tid));
-    t.lane = t.tid & 63;
-    t.half = t.lane >> 5;
-    t.l32 = t.lane & 31;
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
+    const int lane = tid & 63, half = lane >> 5, l32 = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    Fetch<EPI> f;
+    f.set(p, t);
     // waves: WM along the rows x WN along the weight rows, each MI x NJ
     // blocks of 32 x 32
     constexpr int WM = MB == 4 ? 2 : 1, WN = 8 / WM, MI = MB / WM, NJ = 8 / WN;
-    constexpr int NA = (MB + 1) / 2;       // row loads a thread and stage
     constexpr bool SW = EPI == FP8_SWIGLU;
     constexpr bool EXACT = EPI != FP8_OUT_BF16;
-    const int wm = t.wave / WN, wn = t.wave % WN;
+    const int wm = wave / WN, wn = wave % WN;
     const int K = p.K, N = p.N;
     const int S = (K + BK - 1) / BK;
-    const int nbn = (N + 127) / 128;
 
-    // Addresses.  Copies go through buffer resources over the tile's rows
-    // (wave-uniform base, 32-bit offsets), rows past the tile's or the
-    // matrix's end clamped to the last.  A wave's copy fills 8 LDS rows of 128
-    // bytes; the place of a chunk in its row is swizzled, so the lanes fetch
-    // swizzled chunks.  LDS rows 32 apart share their swizzle, so the rest of
-    // an operand's address is an immediate; the chunk index enters it by
-    // exclusive or.
-    const int lr = t.tid >> 3, c = (t.tid & 7) ^ swz(lr);   // chunk c of row lr + 64 q
-    // SwiGLU: LDS row R is row R & 15 of 16 features' gate (R & 16 == 0) or up
-    // rows; R & 16 is the same for a wave and all q
-    const bool up = SW && (t.wave & 2);
-    const size_t wfirst = ((size_t)t.g * N + t.n0) * K;
-    const int wrows = N - t.n0;                     // (>= 1)
-    const u32x4 wsrc = uniform_rsrc((up ? p.w2 : p.w1) + wfirst, (size_t)min(wrows, BN) * K);
-    const u32x4 asrc = uniform_rsrc(p.a + (size_t)t.row0 * K, (size_t)t.valid * K);
-    // (a chunk past the end of K in the last block: the row's last chunk,
-    // overwritten by zeros before it is read)
-    const int past = max(0, (S - 1) * BK + 16 * c + 16 - K);
-    int wo[4], ao[NA];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const int R = lr + 64 * q;
-        wo[q] = min(SW ? 16 * (R >> 5) + (R & 15) : R, wrows - 1) * K + 16 * c;
-    }
-    // (an odd number of blocks: the last 32 rows twice, the same bytes to the
-    // same place, so that every wave issues the same number of copies)
-    constexpr int kLastMask = MB % 2 ? 31 : 63;
-#pragma unroll
-    for (int q = 0; q < NA; ++q) {
-        const int R = (q == NA - 1 ? lr & kLastMask : lr) + 64 * q;
-        ao[q] = min(R, t.valid - 1) * K + 16 * c;
-    }
-    const int last_wave = t.wave & (kLastMask >> 3);
-    // scales: waves 0 to 2 fetch the rows', the others (the same ones) the
-    // weights' of the tile's two 128-blocks of rows, or of gate and up
-    const int nb0 = t.n0 / 128;
-    const float* sp;
-    if (t.wave < 3) {
-        sp = p.as + (size_t)(t.row0 + min(64 * t.wave + t.lane, t.valid - 1)) * S;
-    } else if constexpr (SW) {
-        sp = (t.lane & 1 ? p.s2 : p.s1) + ((size_t)t.g * nbn + nb0) * S;
-    } else {
-        sp = p.s1 + ((size_t)t.g * nbn + min(nb0 + (t.lane & 1), nbn - 1)) * S;
-    }
-    constexpr int NI = 4 + NA + 1;                  // copies a wave and stage
-    // Stage 0 takes K's last block, the short one if any, stage j block j - 1.
-    // (Every stage issues its copies: past the last stage with offsets past
-    // the resources, which fetch nothing.)
-    auto fetch = [&](int j, int at) {
-        const int b = j == 0 ? S - 1 : min(j, S) - 1;
-        const int back = j == 0 ? past : 0, out = j < S ? 0 : (int)0x80000000;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            copy16(wsrc, (wo[q] - back) | out, b * BK, at + q * 64 * BK + t.wave * 1024);
-#pragma unroll
-        for (int q = 0; q < NA; ++q)
-            copy16(asrc, (ao[q] - back) | out, b * BK,
-                   at + kSlotW + q * 64 * BK + (q == NA - 1 ? last_wave : t.wave) * 1024);
-        copy4(sp + b, at + kSlotS + min(t.wave, 3) * 256);
-    };
-    // zeros over this thread's own copies past the end of K, once they landed
-    auto zero_past = [&]() {
-        if (!past) return;
-        const u32x4 z = {0u, 0u, 0u, 0u};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) *(u32x4*)(ring + q * 64 * BK + t.tid * 16) = z;
-#pragma unroll
-        for (int q = 0; q < NA; ++q)
-            *(u32x4*)(ring + kSlotW + q * 64 * BK +
-                      (q == NA - 1 ? last_wave * 1024 + t.lane * 16 : t.tid * 16)) = z;
-    };
-    const int rd0 = t.l32 * BK + ((t.half ^ swz(t.l32)) << 4);
+    // LDS rows 32 apart share their swizzle, so the rest of an operand's
+    // address is an immediate; the chunk index enters it by exclusive or
+    const int rd0 = l32 * BK + ((half ^ swz(l32)) << 4);
     const int rdw = wn * NJ * 32 * BK + rd0;
     const int rda = kSlotW + wm * MI * 32 * BK + rd0;
-    const int rds = kSlotS + (wm * MI * 32 + t.l32) * 4;
-    const int rdsw = kSlotS + 768 + (SW ? 0 : (t.n0 + wn * NJ * 32) / 128 - nb0) * 4;
+    const int rds = kSlotS + (wm * MI * 32 + l32) * 4;
+    const int rdsw = kSlotS + 768 + (SW ? 0 : wn * NJ * 32 / 128) * 4;
     float sa[MI] = {}, sw1 = 0.0f, sw2 = 0.0f;
     auto read_s = [&](int slot) {
 #pragma unroll
@@ -254,19 +260,22 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, Tile t, unsigned 
     for (int e = 0; e < 16; ++e) zero[e] = 0.0f;
     constexpr int NT = MI * NJ;
 
-    // stages 0 to 2 on their way; stage 0 landed
-    fetch(0, 0);
-    fetch(1, kSlot);
-    fetch(2, 2 * kSlot);
-    wait_vm<2 * NI>();
-    zero_past();
+    // stage 0 has landed; zeros over this thread's own copies past K
+    wait_vm<kCopies + kEarly>();
+    if (past) {
+        const u32x4 z = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int q = 0; q < (BN + BM) / 64; ++q) *(u32x4*)(ring + q * 64 * BK + tid * 16) = z;
+    }
     __syncthreads();
     // The middle of stage j: stage j + 1's block has landed and every wave has
-    // read stage j's, whose slot takes stage j + 3's.
-    auto turn = [&](int j, int slot) {
-        wait_vm<NI>();
+    // read stage j's, whose slot takes stage j + 3's.  The copies are spread
+    // over the steps, one at a time (7 at once hold every wave until the memory
+    // pipeline has taken 48 KB): the first after this barrier, the rest in the
+    // next stage's steps before its own.
+    auto turn = [&]() {
+        wait_vm<kCopies>();
         __syncthreads();
-        fetch(j + 3, slot);
     };
 
     if constexpr (EXACT) {
@@ -325,20 +334,28 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, Tile t, unsigned 
         int slot = 0;
         for (int j = 0; j < S; ++j) {
             const int next = slot == 2 * kSlot ? 0 : slot + kSlot;
+            const int last = next == 2 * kSlot ? 0 : next + kSlot;
             scales();                               // of block j - 1
             read_s(slot);
+            f.template copies<3, 4>(j + 2, S, past, last);
             step(H0());
             read(slot, 2, H0());
+            f.template copies<4, 5>(j + 2, S, past, last);
             step(H1());
+            f.template copies<5, 6>(j + 2, S, past, last);
             step(integral_constant<int, 2>());
             read(slot, 3, H1());
+            f.template copies<6, 7>(j + 2, S, past, last);
             step(integral_constant<int, 3>());
             step(integral_constant<int, 4>());
-            turn(j, slot);
+            turn();
             read(next, 0, H0());                    // (past the end: not used)
+            f.template copies<0, 1>(j + 3, S, past, slot);
             step(integral_constant<int, 5>());
+            f.template copies<1, 2>(j + 3, S, past, slot);
             step(integral_constant<int, 6>());
             read(next, 1, H1());
+            f.template copies<2, 3>(j + 3, S, past, slot);
             step(integral_constant<int, 7>());
             slot = next;
         }
@@ -363,25 +380,24 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, Tile t, unsigned 
             return v8i{(int)r[0][0], (int)r[0][1], (int)r[0][2], (int)r[0][3],
                        (int)r[1][0], (int)r[1][1], (int)r[1][2], (int)r[1][3]};
         };
-        auto multiply = [&](auto set) {
+        // the products of a step, a copy (of up to four) ahead of each
+        auto multiply = [&](auto set, auto copy) {
             constexpr int B = decltype(set)::value;
-#pragma unroll
-            for (int i = 0; i < MI; ++i)
-#pragma unroll
-                for (int n = 0; n < NJ; ++n) {
+            auto tile = [&](auto index) {
+                constexpr int x = decltype(index)::value, i = x / NJ, n = x % NJ;
+                if constexpr (x < NT) {
                     if constexpr (B == 0) add_part(i, n);
                     part[i][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
                         cat(rw[B][n]), cat(ra[B][i]), B == 0 ? zero : part[i][n], 0, 0, 0, 127, 0,
                         127);
                 }
-            if constexpr (B == 0) {
-#pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    __builtin_amdgcn_sched_group_barrier(0x002, 16, 0);
-                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                }
-            }
-            __builtin_amdgcn_sched_barrier(0);
+                copy(index);
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            tile(std::integral_constant<int, 0>());
+            tile(std::integral_constant<int, 1>());
+            tile(std::integral_constant<int, 2>());
+            tile(std::integral_constant<int, 3>());
         };
         using B0 = std::integral_constant<int, 0>;
         using B1 = std::integral_constant<int, 1>;
@@ -389,15 +405,27 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, Tile t, unsigned 
         int slot = 0;
         for (int j = 0; j < S; ++j) {
             const int next = slot == 2 * kSlot ? 0 : slot + kSlot;
+            const int last = next == 2 * kSlot ? 0 : next + kSlot;
             scales();                               // of block j - 1
             read_s(slot);
             read(slot, B1());
-            multiply(B0());
-            turn(j, slot);
+            multiply(B0(), [&](auto q) {
+                f.template copies<3 + decltype(q)::value, 4 + decltype(q)::value>(j + 2, S, past, last);
+            });
+            turn();
             read(next, B0());                       // (past the end: not used)
-            multiply(B1());
+            multiply(B1(), [&](auto q) {
+                if constexpr (decltype(q)::value < kEarly)
+                    f.template copies<decltype(q)::value, decltype(q)::value + 1>(j + 3, S, past, slot);
+            });
             slot = next;
         }
+    }
+    // (every wave has read the last stage; what the ring still holds is unused)
+    if (more) {
+        Fetch<EPI> nf;
+        nf.set(p, next_t);
+        nf.first_stages(S, past);
     }
     scales();
 #pragma unroll
@@ -405,57 +433,49 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, Tile t, unsigned 
 #pragma unroll
         for (int n = 0; n < NJ; ++n) add_part(i, n);
 
-    // Epilogues: lane l holds, of row l % 32 of its block, weight rows
-    // 8 (e / 4) + 4 (l / 32) + e % 4; through LDS into whole-line stores.
-    wait_vm<0>();
-    __syncthreads();
+    // Epilogues, from the registers: lane l holds, of row l % 32 of its block,
+    // weight rows 8 q + 4 (l / 32) + (0 .. 3), q < 4.  The stores of a wave
+    // fill 32 to 64 bytes of a row each; the L2 joins them to lines.
     if constexpr (EPI == FP8_OUT_F32) {
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
-            if (i) __syncthreads();
+            const int r = (wm * MI + i) * 32 + l32;
+            float* o = (float*)p.out + (size_t)(t.row0 + r) * N + t.n0;
 #pragma unroll
             for (int n = 0; n < NJ; ++n)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int col = (wn * NJ + n) * 32 + 8 * q + 4 * t.half;
-                    *(f32x4*)(ring + (wm * 32 + t.l32) * kRowF32 + col * 4) =
-                        f32x4{acc[i][n][4 * q], acc[i][n][4 * q + 1], acc[i][n][4 * q + 2],
-                              acc[i][n][4 * q + 3]};
+                    const int col = (wn * NJ + n) * 32 + 8 * q + 4 * half;
+                    if (r < t.valid && t.n0 + col < N)
+                        *(f32x4*)(o + col) = f32x4{acc[i][n][4 * q], acc[i][n][4 * q + 1],
+                                                   acc[i][n][4 * q + 2], acc[i][n][4 * q + 3]};
                 }
-            __syncthreads();
-            const int col = 4 * t.lane;
-            for (int sr = t.wave; sr < WM * 32; sr += 8) {
-                const int r = ((sr >> 5) * MI + i) * 32 + (sr & 31);
-                if (r < t.valid && t.n0 + col < N)
-                    *(f32x4*)((float*)p.out + (size_t)(t.row0 + r) * N + t.n0 + col) =
-                        *(const f32x4*)(ring + sr * kRowF32 + col * 4);
-            }
         }
     } else if constexpr (EPI == FP8_OUT_BF16) {
+        // (the half-waves exchange, so that a lane holds 8 columns in a row)
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
+        for (int i = 0; i < MI; ++i) {
+            const int r = (wm * MI + i) * 32 + l32;
+            uint16_t* o = (uint16_t*)p.out + (size_t)(t.row0 + r) * N + t.n0;
 #pragma unroll
             for (int n = 0; n < NJ; ++n)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int col = (wn * NJ + n) * 32 + 8 * q + 4 * t.half;
-                    *(u32x2*)(ring + ((wm * MI + i) * 32 + t.l32) * kRowBf16 + col * 2) =
-                        u32x2{bf16_pack2(acc[i][n][4 * q], acc[i][n][4 * q + 1]),
-                              bf16_pack2(acc[i][n][4 * q + 2], acc[i][n][4 * q + 3])};
+                for (int q = 0; q < 4; q += 2) {
+                    const f32x16& v = acc[i][n];
+                    const u32x2 x = swap_halves(bf16_pack2(v[4 * q], v[4 * q + 1]),
+                                                bf16_pack2(v[4 * q + 4], v[4 * q + 5]));
+                    const u32x2 y = swap_halves(bf16_pack2(v[4 * q + 2], v[4 * q + 3]),
+                                                bf16_pack2(v[4 * q + 6], v[4 * q + 7]));
+                    const int col = (wn * NJ + n) * 32 + 8 * (q + half);
+                    if (r < t.valid && t.n0 + col < N)
+                        *(u32x4*)(o + col) = u32x4{x[0], y[0], x[1], y[1]};
                 }
-        __syncthreads();
-        const int col = 8 * t.l32;
-        for (int r = 2 * t.wave + t.half; r < t.valid; r += 16)
-            if (t.n0 + col < N)
-                *(u32x4*)((uint16_t*)p.out + (size_t)(t.row0 + r) * N + t.n0 + col) =
-                    *(const u32x4*)(ring + r * kRowBf16 + col * 2);
+        }
     } else {
         // h = SwiGLU in fp32, quantised along the tile's 128 features: the
         // row maximum over this lane's features, its half-wave partner's and
         // the other waves'
-        float* rm = (float*)ring;                     // [WN][BM]
-        unsigned char* stg = ring + 8 * BM * 4;       // [BM][kRowH] codes
-        float h[MI][NJ][8];
+        float* rm = (float*)(ring + kRing);           // [WN][BM]
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
             float m = 0.0f;
@@ -466,40 +486,35 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, Tile t, unsigned 
                 for (int e = 0; e < 8; ++e) {
                     const float v = clamped_swiglu(acc[i][n][e], acc[i][n][e + 8], p.clamp_limit,
                                                    p.clamp_mode);
-                    h[i][n][e] = in ? v : 0.0f;
-                    m = fmaxf(m, finite_abs(h[i][n][e]));
+                    acc[i][n][e] = in ? v : 0.0f;
+                    m = fmaxf(m, finite_abs(acc[i][n][e]));
                 }
             }
             m = fmaxf(m, __shfl_xor(m, 32, 64));
-            if (t.half == 0) rm[wn * BM + (wm * MI + i) * 32 + t.l32] = m;
+            if (half == 0) rm[wn * BM + (wm * MI + i) * 32 + l32] = m;
         }
         __syncthreads();
         const int nbf = (N + 127) / 128;
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
-            const int r = (wm * MI + i) * 32 + t.l32;
+            const int r = (wm * MI + i) * 32 + l32;
             float m = 0.0f;
 #pragma unroll
             for (int w = 0; w < WN; ++w) m = fmaxf(m, rm[w * BM + r]);
             const int X = block_exponent(m);
             const float inv = pow2(-X);
+            uint8_t* o = (uint8_t*)p.out + (size_t)(t.row0 + r) * N + t.n0;
 #pragma unroll
-            for (int n = 0; n < NJ; ++n)
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int f = 16 * (wn * NJ + n) + 8 * q + 4 * t.half;
-                    *(uint32_t*)(stg + r * kRowH + f) =
-                        e4m3_pack4(h[i][n][4 * q], h[i][n][4 * q + 1], h[i][n][4 * q + 2],
-                                   h[i][n][4 * q + 3], inv);
-                }
-            if (wn == 0 && t.half == 0 && r < t.valid)
+            for (int n = 0; n < NJ; ++n) {
+                const f32x16& v = acc[i][n];
+                const u32x2 w = swap_halves(e4m3_pack4(v[0], v[1], v[2], v[3], inv),
+                                            e4m3_pack4(v[4], v[5], v[6], v[7], inv));
+                const int f0 = 16 * (wn * NJ + n);
+                if (r < t.valid && t.n0 + f0 < N) *(u32x2*)(o + f0 + 8 * half) = w;
+            }
+            if (wn == 0 && half == 0 && r < t.valid)
                 p.out_scale[(size_t)(t.row0 + r) * nbf + t.n0 / 128] = pow2(X);
         }
-        __syncthreads();
-        for (int r = lr; r < t.valid; r += 64)
-            if (t.n0 + 16 * c < N)
-                *(u32x4*)((uint8_t*)p.out + (size_t)(t.row0 + r) * N + t.n0 + 16 * c) =
-                    *(const u32x4*)(stg + r * kRowH + 16 * c);
     }
 }
 
@@ -531,17 +546,20 @@ template <int EPI>
 __global__ __launch_bounds__(kThreads) void gemm_fp8_block_kernel(Fp8GemmArgs p) {
     extern __shared__ __align__(16) unsigned char smem[];
     constexpr int TN = EPI == FP8_SWIGLU ? BN / 2 : BN;
-    Tile t;
-    t.tid = threadIdx.x;
-    t.lane = t.tid & 63;
-    t.wave = __builtin_amdgcn_readfirstlane(t.tid >> 6);
-    t.half = t.lane >> 5;
-    t.l32 = t.lane & 31;
-    const int G = p.G, rows = p.rows;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int G = p.G, rows = p.rows, S = (p.K + BK - 1) / BK;
     const int NT = (p.N + TN - 1) / TN;
+    // the groups' offsets, clamped into [0, rows], in LDS where they fit (a
+    // load from memory would wait for the copies before it)
+    int* table = (int*)(smem + kRing + kRowMax);
+    const bool tabled = G < kTable;
+    auto clamped = [&](int g) { return min(max(p.offsets[g], 0), rows); };
+    if (tabled)
+        for (int g = tid; g <= G; g += kThreads) table[g] = clamped(g);
+    __syncthreads();
     auto group_rows = [&](int g, int& lo, int& hi) {
-        lo = min(max(p.offsets[g], 0), rows);
-        hi = max(lo, min(max(p.offsets[g + 1], 0), rows));
+        lo = tabled ? table[g] : clamped(g);
+        hi = max(lo, tabled ? table[g + 1] : clamped(g + 1));
     };
     auto group_items = [&](int g) {
         int lo = 0, hi = 0;
@@ -550,34 +568,54 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_block_kernel(Fp8GemmArgs p)
     };
     const int run = (G + 63) / 64;
     int mine = 0;
-    for (int i = 0; i < run; ++i) mine += group_items(t.lane * run + i);
-    const int upto = wave_scan(mine, t.lane);
+    for (int i = 0; i < run; ++i) mine += group_items(lane * run + i);
+    const int upto = wave_scan(mine, lane);
     const long long Q = __builtin_amdgcn_readlane(upto, 63);
-    const int xcd = blockIdx.x & 7;
-    const int hi_item = (int)(Q * (xcd + 1) / 8);
-    for (int q = (int)(Q * xcd / 8) + (int)(blockIdx.x >> 3); q < hi_item; q += gridDim.x >> 3) {
+    const int xcd = blockIdx.x & 7, step = gridDim.x >> 3;
+    const int end = (int)(Q * (xcd + 1) / 8);
+    auto find = [&](int q, Tile& t) {
         // the first lane whose sum passes q, then the same within its run
         const int r = __builtin_ctzll(__builtin_amdgcn_ballot_w64(upto > q));
         int local = q - __builtin_amdgcn_readlane(upto - mine, r);
-        const int items = t.lane < run ? group_items(r * run + t.lane) : 0;
-        const int in_run = wave_scan(items, t.lane);
+        const int items = lane < run ? group_items(r * run + lane) : 0;
+        const int in_run = wave_scan(items, lane);
         const int l = __builtin_ctzll(__builtin_amdgcn_ballot_w64(in_run > local));
         local -= __builtin_amdgcn_readlane(in_run - items, l);
         t.g = r * run + l;
         int r0, r1;
         group_rows(t.g, r0, r1);
+        r0 = __builtin_amdgcn_readfirstlane(r0);
+        r1 = __builtin_amdgcn_readfirstlane(r1);
         const int n = r1 - r0, mt = row_tiles(n);
         const int per = ((n + mt - 1) / mt + 31) & ~31;
         t.n0 = local / mt * TN;
         t.row0 = r0 + local % mt * per;
         t.valid = min(per, r1 - t.row0);
+    };
+    // bytes that this thread's chunk of K's last block reaches past K
+    const int past = max(0, (S - 1) * BK + 16 * ((tid & 7) ^ swz(tid >> 3)) + 16 - p.K);
+    int q = (int)(Q * xcd / 8) + (int)(blockIdx.x >> 3);
+    if (q >= end) return;
+    Tile t;
+    find(q, t);
+    {
+        Fetch<EPI> f;
+        f.set(p, t);
+        f.first_stages(S, past);
+    }
+    for (;;) {
+        const bool more = q + step < end;
+        Tile next = t;
+        if (more) find(q + step, next);
         switch ((t.valid + 31) >> 5) {
-            case 1: run_tile<EPI, 1>(p, t, smem); break;
-            case 2: run_tile<EPI, 2>(p, t, smem); break;
-            case 3: run_tile<EPI, 3>(p, t, smem); break;
-            default: run_tile<EPI, 4>(p, t, smem); break;
+            case 1: run_tile<EPI, 1>(p, t, next, more, past, smem); break;
+            case 2: run_tile<EPI, 2>(p, t, next, more, past, smem); break;
+            case 3: run_tile<EPI, 3>(p, t, next, more, past, smem); break;
+            default: run_tile<EPI, 4>(p, t, next, more, past, smem); break;
         }
-        __syncthreads();                             // the ring is free again
+        if (!more) break;
+        t = next;
+        q += step;
     }
 }
 
