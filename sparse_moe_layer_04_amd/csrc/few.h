@@ -28,12 +28,10 @@ struct FewArgs {
     float* w;                      // [T, k]
     uint16_t* hs;                  // [T, Fs] bf16
     uint16_t* h;                   // [T k, F] bf16, by pair
-    float* part;                   // [T k + T, d] expert outputs by pair, shared ones
     int32_t* expert;               // distinct experts
     int32_t* start;                // [+ 1]
     int32_t* pairs;
     int32_t* n_expert;
-    uint32_t* count;               // [d / 16] experts done of an output chunk
 };
 
 hipError_t launch_few(bool fp8, const FewArgs& p, hipStream_t stream);

@@ -7,15 +7,12 @@
 // shared expert's matrices is tens of microseconds, so launches and
 // dependent round trips count as much as the bandwidth.
 //
-// One kind of work item serves every product of the layer: 16 weight rows
-// times the rows' tokens.  The 8 waves of a workgroup split K in pieces of
-// 128 bytes (wave w takes pieces w, w + 8, ..., so the workgroup reads 1 KB
-// of each row at a time); a wave's load instruction covers 64 bytes of 16
-// rows, which is the operand layout of the 16 x 16 x 32 matrix instruction
-// (any order of K will do, the same for weights and activations): the
-// weights go from memory to the operand registers and are multiplied by up
-// to 16 tokens at once.  The waves' 16 x 16 partial sums meet in LDS and are
-// added in wave order.
+// One kind of work serves every product of the layer: a strip of 16 weight
+// rows times the rows' tokens.  A wave's load instruction covers 64 bytes of
+// 16 rows, which is the operand layout of the 16 x 16 x 32 matrix instruction
+// (any order of K will do, the same for weights and activations): the weights
+// go from memory to the operand registers, eight pieces of 128 bytes a row
+// ahead, and are multiplied by up to 16 tokens at once.
 //
 // 8-bit weights are decoded to bf16 (exact); a piece is one block of K, its
 // sum is multiplied by the block's scale.
@@ -31,22 +28,6 @@ constexpr int kTiles = MOE_FEW_MAX_T / 16; // column tiles of 16 tokens
 constexpr int kMaxPairs = MOE_FEW_MAX_T * MOE_MAX_K;
 static_assert(kMaxPairs <= kThreads, "one thread a (token, slot) pair");
 
-// Values that other workgroups of the same launch read: stored and loaded at
-// device scope (past the XCD's own L2, which is not coherent with the other
-// seven), a store complete for every XCD once the wave's store counter says
-// so.  A device-wide fence instead would write the whole L2 back at every
-// item (133 us instead of 12 for the down products of one token).
-__device__ __forceinline__ void put_shared(float* p, float v) {
-    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ float get_shared(const float* p) {
-    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-// this wave's stores have completed
-__device__ __forceinline__ void stores_done() {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-}
-
 struct Lane {
     int tid, lane, wave, r16, grp;         // r16 = lane % 16, grp = lane / 16
 };
@@ -61,90 +42,141 @@ __device__ __forceinline__ Lane this_lane() {
     return l;
 }
 
-// acc[c] += this wave's share of W[16 rows] x^T for column tile c < ct.
-// wrow: this lane's weight row (row r16 of the item); srow: its block scales
-// (8-bit weights); x[c]: the activations of column r16 of tile c, NULL where
-// the tile has no such column.
+// The products of a strip: acc[c] += W[16 rows] x^T for column tiles c < ct,
+// over the pieces first, first + step, ... of K.
+// wrow: this lane's weight row (row r16 of the strip); srow: its block scales
+// (8-bit weights); x[c]: the activations of column r16 of tile c (a tile's
+// columns past its last token may be anything: no output of theirs is used).
 template <bool FP8>
-__device__ __forceinline__ void strip(const uint8_t* __restrict__ wrow,
-                                      const float* __restrict__ srow, int K,
-                                      const uint16_t* const (&x)[kTiles], int ct, const Lane& l,
-                                      f32x4 (&acc)[kTiles]) {
-    constexpr int UK = FP8 ? 128 : 64;     // K a piece (128 bytes of a row)
-    constexpr int UB = 4;                  // pieces in flight a wave
-    constexpr int XL = FP8 ? 4 : 2;        // 16-byte activation loads a piece
-    const int nu = (K + UK - 1) / UK;
-    for (int u0 = l.wave; u0 < nu; u0 += 8 * UB) {
-        u32x4 w[UB][2];
-        float sc[UB];
+struct Strip {
+    static constexpr int UK = FP8 ? 128 : 64;  // K a piece (128 bytes of a row)
+    static constexpr int R = 8;                // weight pieces in flight a wave
+    static constexpr int RX = 4;               // activation pieces
+    static constexpr int XL = FP8 ? 4 : 2;     // 16-byte activation loads a piece
+
+    const uint8_t* wrow;
+    const float* srow;
+    int K, grp;
+    u32x4 w[R][2];
+    float sc[R];
+    u32x4 xv[RX][XL];
+
+    // piece u; the second half of the last one may lie past K, a multiple of
+    // 64: zeros (8-bit)
+    __device__ __forceinline__ void load_w(int u, u32x4 (&v)[2], float& s) const {
+        const uint8_t* q = wrow + (size_t)u * 128 + 16 * grp;
+        v[0] = *(const u32x4*)q;
+        if constexpr (FP8) {
+            const bool in = u * UK + 64 < K;
+            v[1] = *(const u32x4*)(in ? q + 64 : q);
+            s = srow[u];
+        } else {
+            v[1] = *(const u32x4*)(q + 64);
+        }
+    }
+    __device__ __forceinline__ void load_x(const uint16_t* x, int u, u32x4 (&v)[XL]) const {
+        const uint16_t* q = x + (size_t)u * UK;
+        if constexpr (FP8) {
+            v[0] = *(const u32x4*)(q + 16 * grp);
+            v[1] = *(const u32x4*)(q + 16 * grp + 8);
+            const uint16_t* h = u * UK + 64 < K ? q + 64 : q;
+            v[2] = *(const u32x4*)(h + 16 * grp);
+            v[3] = *(const u32x4*)(h + 16 * grp + 8);
+        } else {
+            v[0] = *(const u32x4*)(q + 8 * grp);
+            v[1] = *(const u32x4*)(q + 32 + 8 * grp);
+        }
+    }
+    __device__ __forceinline__ void multiply(int u, const u32x4 (&wv)[2], float s,
+                                             const u32x4 (&x)[XL], f32x4& acc) const {
+        if constexpr (FP8) {
+            f32x4 part = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < UB; ++i) {
-            const int u = u0 + 8 * i;
-            w[i][0] = w[i][1] = u32x4{0u, 0u, 0u, 0u};
-            sc[i] = 0.0f;
-            if (u < nu) {
-                w[i][0] = *(const u32x4*)(wrow + (size_t)u * 128 + 16 * l.grp);
-                if (!FP8 || u * UK + 64 < K)   // (K is a multiple of 64)
-                    w[i][1] = *(const u32x4*)(wrow + (size_t)u * 128 + 64 + 16 * l.grp);
-                if constexpr (FP8) sc[i] = srow[u];
+            for (int q = 0; q < 2; ++q)
+                part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    fp8x8_to_bf16x8(u32x2{wv[0][2 * q], wv[0][2 * q + 1]}, 1.0f),
+                    __builtin_bit_cast(bf16x8, x[q]), part, 0, 0, 0);
+            if (u * UK + 64 < K) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        fp8x8_to_bf16x8(u32x2{wv[1][2 * q], wv[1][2 * q + 1]}, 1.0f),
+                        __builtin_bit_cast(bf16x8, x[2 + q]), part, 0, 0, 0);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(part[e], s, acc[e]);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    __builtin_bit_cast(bf16x8, wv[q]), __builtin_bit_cast(bf16x8, x[q]), acc, 0, 0,
+                    0);
+        }
+    }
+    // pieces first + step * i of K
+    __device__ __forceinline__ void run(const uint16_t* const (&x)[kTiles], int ct, int first,
+                                        int step, f32x4 (&acc)[kTiles]) {
+        const int nu = (K + UK - 1) / UK;
+        const int n = first < nu ? (nu - first + step - 1) / step : 0;
+        if (ct == 1)
+            run_one(x[0], n, first, step, acc[0]);
+        else
+            run_tiles(x, ct, n, first, step, acc);
+    }
+    // one column tile: weights R pieces ahead, activations RX
+    __device__ __forceinline__ void run_one(const uint16_t* x, int n, int first, int step,
+                                            f32x4& acc) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (i < n) load_w(first + step * i, w[i], sc[i]);
+#pragma unroll
+        for (int i = 0; i < RX; ++i)
+            if (i < n) load_x(x, first + step * i, xv[i]);
+        int i0 = 0;
+        for (; i0 + 2 * R <= n; i0 += R) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                multiply(first + step * (i0 + i), w[i], sc[i], xv[i % RX], acc);
+                load_w(first + step * (i0 + i + R), w[i], sc[i]);
+                load_x(x, first + step * (i0 + i + RX), xv[i % RX]);
             }
         }
+        for (; i0 < n; i0 += R) {
 #pragma unroll
-        for (int c = 0; c < kTiles; ++c) {
-            if (c >= ct) break;
-            u32x4 xv[UB][XL];
-#pragma unroll
-            for (int i = 0; i < UB; ++i) {
-                const int u = u0 + 8 * i;
-#pragma unroll
-                for (int q = 0; q < XL; ++q) xv[i][q] = u32x4{0u, 0u, 0u, 0u};
-                if (u < nu && x[c]) {
-                    const uint16_t* xp = x[c] + (size_t)u * UK;
-                    if constexpr (FP8) {
-                        xv[i][0] = *(const u32x4*)(xp + 16 * l.grp);
-                        xv[i][1] = *(const u32x4*)(xp + 16 * l.grp + 8);
-                        if (u * UK + 64 < K) {
-                            xv[i][2] = *(const u32x4*)(xp + 64 + 16 * l.grp);
-                            xv[i][3] = *(const u32x4*)(xp + 64 + 16 * l.grp + 8);
-                        }
-                    } else {
-                        xv[i][0] = *(const u32x4*)(xp + 8 * l.grp);
-                        xv[i][1] = *(const u32x4*)(xp + 32 + 8 * l.grp);
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < UB; ++i) {
-                if (u0 + 8 * i >= nu) continue;
-                if constexpr (FP8) {
-                    f32x4 part = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const u32x4 v = w[i][q >> 1];
-                        const bf16x8 wv =
-                            fp8x8_to_bf16x8(u32x2{v[2 * (q & 1)], v[2 * (q & 1) + 1]}, 1.0f);
-                        part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            wv, __builtin_bit_cast(bf16x8, xv[i][q]), part, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[c][e] = __builtin_fmaf(part[e], sc[i], acc[c][e]);
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            __builtin_bit_cast(bf16x8, w[i][q]),
-                            __builtin_bit_cast(bf16x8, xv[i][q]), acc[c], 0, 0, 0);
-                }
+            for (int i = 0; i < R; ++i) {
+                const int k = i0 + i;
+                if (k < n) multiply(first + step * k, w[i], sc[i], xv[i % RX], acc);
+                if (k + R < n) load_w(first + step * (k + R), w[i], sc[i]);
+                if (k + RX < n) load_x(x, first + step * (k + RX), xv[i % RX]);
             }
         }
     }
-}
+    // more tokens: each piece against all tiles, the next piece's weights ahead
+    __device__ __forceinline__ void run_tiles(const uint16_t* const (&x)[kTiles], int ct, int n,
+                                              int first, int step, f32x4 (&acc)[kTiles]) {
+        if (n == 0) return;
+        load_w(first, w[0], sc[0]);
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            const int u = first + step * i;
+            load_w(first + step * min(i + 1, n - 1), w[1], sc[1]);
+#pragma unroll
+            for (int c = 0; c < kTiles; ++c)
+                if (c < ct) load_x(x[c], u, xv[c]);
+#pragma unroll
+            for (int c = 0; c < kTiles; ++c)
+                if (c < ct) multiply(u, w[0], sc[0], xv[c], acc[c]);
+            w[0][0] = w[1][0];
+            w[0][1] = w[1][1];
+            sc[0] = sc[1];
+        }
+    }
+};
+static_assert(Strip<true>::RX >= kTiles && Strip<false>::RX >= kTiles, "a register set a tile");
 
-// red: [8 waves][ct][16 rows][16 columns].  The row a lane's scale belongs to
-// is the row of its weights, but lane l's outputs are rows 4 (l / 16) + e, so
-// 8-bit callers pass the scales of the output rows' block (the same for every
-// output row of a lane).
+// A strip whose K is split over the 8 waves: their partial sums meet in LDS,
+// red [8 waves][ct][16 rows][16 columns], and are added in wave order.  Lane l
+// holds rows 4 (l / 16) + e of column l % 16.
 __device__ __forceinline__ void put_partials(float* red, const f32x4 (&acc)[kTiles], int ct,
                                              const Lane& l) {
 #pragma unroll
@@ -168,45 +200,44 @@ __device__ __forceinline__ void zero_acc(f32x4 (&acc)[kTiles]) {
     for (int c = 0; c < kTiles; ++c) acc[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 }
 
-// the 16 rows of a gate/up item: gate rows of features f0 .. f0 + 7, then the
-// up rows of the same features
+// the 16 rows of a gate/up strip: gate rows of features f0 .. f0 + 7, then the
+// up rows of the same features.  (A lane's scales are those of its outputs,
+// rows 4 (l / 16) + e, not of the row it loads.)
 template <bool FP8>
-__device__ __forceinline__ void gate_up_strip(const void* gate, const void* up, const float* sg,
-                                              const float* su, size_t mat, int f0, int F, int d,
-                                              const uint16_t* const (&x)[kTiles], int ct,
-                                              const Lane& l, f32x4 (&acc)[kTiles]) {
-    constexpr size_t B = FP8 ? 1 : 2;
+__device__ __forceinline__ void set_gate_up(Strip<FP8>& s, const void* gate, const void* up,
+                                            const float* sg, const float* su, size_t mat, int f0,
+                                            int F, int d, const Lane& l) {
     const size_t row = (mat * F + f0 + (l.r16 & 7)) * (size_t)d;
-    const uint8_t* wrow = (const uint8_t*)(l.r16 < 8 ? gate : up) + row * B;
-    const float* srow = nullptr;
+    s.wrow = (const uint8_t*)(l.r16 < 8 ? gate : up) + row * (FP8 ? 1 : 2);
+    s.K = d;
+    s.grp = l.grp;
     if constexpr (FP8) {
         const int nbf = (F + 127) / 128, nbd = (d + 127) / 128;
-        srow = (l.grp < 2 ? sg : su) + (mat * nbf + f0 / 128) * (size_t)nbd;
+        s.srow = (l.grp < 2 ? sg : su) + (mat * nbf + f0 / 128) * (size_t)nbd;
     }
-    strip<FP8>(wrow, srow, d, x, ct, l, acc);
 }
 
 // ------------------------------------------------ router and shared expert --
 // Items: 16 experts' router rows, then 8 features of the shared expert: none
-// depends on the routing.  Workgroup 0 clears the counters of the last kernel.
+// depends on the routing.  Few strips: each is split over a workgroup's waves.
 template <bool FP8>
-__global__ __launch_bounds__(kThreads, 2) void few_router_kernel(FewArgs p) {
+__global__ __launch_bounds__(kThreads) void few_router_kernel(FewArgs p) {
     extern __shared__ __align__(16) float red[];
     const Lane l = this_lane();
     const int ct = (p.T + 15) / 16;
     const int nr = (p.E + 15) / 16;
-    if (blockIdx.x == 0)
-        for (int i = l.tid; i < p.d / 16; i += kThreads) p.count[i] = 0u;
     const uint16_t* x[kTiles];
 #pragma unroll
-    for (int c = 0; c < kTiles; ++c)
-        x[c] = 16 * c + l.r16 < p.T ? p.x + (size_t)(16 * c + l.r16) * p.d : nullptr;
+    for (int c = 0; c < kTiles; ++c) x[c] = p.x + (size_t)min(16 * c + l.r16, p.T - 1) * p.d;
     f32x4 acc[kTiles];
     zero_acc(acc);
     const int item = blockIdx.x;
     if (item < nr) {
-        const int e = min(16 * item + l.r16, p.E - 1);
-        strip<false>((const uint8_t*)(p.w_g + (size_t)e * p.d), nullptr, p.d, x, ct, l, acc);
+        Strip<false> st;
+        st.wrow = (const uint8_t*)(p.w_g + (size_t)min(16 * item + l.r16, p.E - 1) * p.d);
+        st.K = p.d;
+        st.grp = l.grp;
+        st.run(x, ct, l.wave, 8, acc);
         put_partials(red, acc, ct, l);
         __syncthreads();
         for (int i = l.tid; i < 256 * ct; i += kThreads) {
@@ -219,8 +250,9 @@ __global__ __launch_bounds__(kThreads, 2) void few_router_kernel(FewArgs p) {
         }
     } else {
         const int f0 = 8 * (item - nr);
-        gate_up_strip<FP8>(p.s_gate, p.s_up, p.s_gate_scale, p.s_up_scale, 0, f0, p.Fs, p.d, x,
-                           ct, l, acc);
+        Strip<FP8> st;
+        set_gate_up(st, p.s_gate, p.s_up, p.s_gate_scale, p.s_up_scale, 0, f0, p.Fs, p.d, l);
+        st.run(x, ct, l.wave, 8, acc);
         put_partials(red, acc, ct, l);
         __syncthreads();
         for (int i = l.tid; i < 128 * ct; i += kThreads) {
@@ -345,30 +377,26 @@ __device__ __forceinline__ void build_table(const FewArgs& p, const Lane& l, Tab
 }
 
 // ------------------------------------------------------- routed gate and up --
-// Items: (expert, 8 features), every token of the expert at once.
+// One wave a strip: (expert, 8 features), every token of the expert at once
+// (16 columns; more in further column tiles).
 template <bool FP8>
-__global__ __launch_bounds__(kThreads, 2) void few_gate_up_kernel(FewArgs p) {
-    extern __shared__ __align__(16) float red_all[];
+__global__ __launch_bounds__(kThreads) void few_gate_up_kernel(FewArgs p) {
     __shared__ Table tb;
     const Lane l = this_lane();
     build_table(p, l, tb);
-    const int n = tb.n;
+    const int n = tb.n, P = p.T * p.k;
     if (blockIdx.x == 0) {
         // the table, for the last kernel
-        for (int i = l.tid; i < kMaxPairs; i += kThreads) {
-            if (i < n) p.expert[i] = tb.expert[i];
-            if (i <= n) p.start[i] = tb.start[i];
-            if (i < tb.start[n]) p.pairs[i] = tb.pairs[i];
+        for (int i = l.tid; i < P; i += kThreads) {
+            p.expert[i] = tb.expert[i];
+            p.pairs[i] = tb.pairs[i];
         }
-        if (l.tid == 0) {
-            p.start[n] = tb.start[n];
-            *p.n_expert = n;
-        }
+        for (int i = l.tid; i <= n; i += kThreads) p.start[i] = tb.start[i];
+        if (l.tid == 0) *p.n_expert = n;
     }
     const int per = p.F / 8;
-    const int buf = 8 * ((p.T * p.k + 15) / 16 < kTiles ? (p.T * p.k + 15) / 16 : kTiles) * 256;
-    int parity = 0;
-    for (int it = blockIdx.x; it < n * per; it += gridDim.x) {
+    // strips dealt to the workgroups first, so that few strips use every CU
+    for (int it = l.wave * gridDim.x + blockIdx.x; it < n * per; it += 8 * gridDim.x) {
         const int u = it / per, f0 = (it - u * per) * 8;
         const int e = tb.expert[u], s = tb.start[u], m_all = tb.start[u + 1] - s;
         // (repeated ids of a hash table can give an expert more rows than
@@ -376,161 +404,135 @@ __global__ __launch_bounds__(kThreads, 2) void few_gate_up_kernel(FewArgs p) {
         for (int m0 = 0; m0 < m_all; m0 += MOE_FEW_MAX_T) {
             const int m = min(m_all - m0, MOE_FEW_MAX_T), ct = (m + 15) / 16;
             const uint16_t* x[kTiles];
+            int pair[kTiles];
 #pragma unroll
-            for (int c = 0; c < kTiles; ++c)
-                x[c] = 16 * c + l.r16 < m
-                           ? p.x + (size_t)(tb.pairs[s + m0 + 16 * c + l.r16] / p.k) * p.d
-                           : nullptr;
+            for (int c = 0; c < kTiles; ++c) {
+                pair[c] = tb.pairs[s + m0 + min(16 * c + l.r16, m - 1)];
+                x[c] = p.x + (size_t)(pair[c] / p.k) * p.d;
+            }
             f32x4 acc[kTiles];
             zero_acc(acc);
-            gate_up_strip<FP8>(p.w_gate, p.w_up, p.w_gate_scale, p.w_up_scale, e, f0, p.F, p.d, x,
-                               ct, l, acc);
-            float* red = red_all + parity * buf;
-            parity ^= 1;
-            put_partials(red, acc, ct, l);
-            __syncthreads();
-            for (int i = l.tid; i < 128 * ct; i += kThreads) {
-                const int f = i & 7, r = i >> 3;
-                if (r < m) {
-                    const float g = sum_partials(red, ct, r >> 4, f, r & 15);
-                    const float up = sum_partials(red, ct, r >> 4, f + 8, r & 15);
-                    p.h[(size_t)tb.pairs[s + m0 + r] * p.F + f0 + f] =
-                        f32_to_bf16(clamped_swiglu(g, up, p.clamp_limit, p.clamp_mode));
+            Strip<FP8> st;
+            set_gate_up(st, p.w_gate, p.w_up, p.w_gate_scale, p.w_up_scale, e, f0, p.F, p.d, l);
+            st.run(x, ct, 0, 1, acc);
+            // lanes 0-31 hold the gate sums of features 4 grp + e, lanes 32-63
+            // the up sums of the same ones
+#pragma unroll
+            for (int c = 0; c < kTiles; ++c) {
+                if (c >= ct) break;
+                uint32_t h[2];
+#pragma unroll
+                for (int e2 = 0; e2 < 2; ++e2) {
+                    float v[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float mine = acc[c][2 * e2 + i];
+                        v[i] = clamped_swiglu(mine, __shfl_xor(mine, 32, 64), p.clamp_limit,
+                                              p.clamp_mode);
+                    }
+                    h[e2] = bf16_pack2(v[0], v[1]);
                 }
+                if (l.grp < 2 && 16 * c + l.r16 < m)
+                    *(u32x2*)(p.h + (size_t)pair[c] * p.F + f0 + 4 * l.grp) = u32x2{h[0], h[1]};
             }
         }
     }
 }
 
 // --------------------------------------------------------- down and combine --
-// y[t, o] = shared + sum_j w_j y_j, j in slot order, for 16 outputs o
-__device__ __forceinline__ void combine_chunk(const FewArgs& p, int chunk, int tid) {
-    const int P = p.T * p.k;
-    for (int i = tid; i < p.T * 16; i += kThreads) {
-        const int t = i >> 4;
-        const size_t o = (size_t)chunk * 16 + (i & 15);
-        float e[MOE_MAX_K];
-#pragma unroll
-        for (int j = 0; j < MOE_MAX_K; ++j)
-            e[j] = j < p.k && p.ids[t * p.k + j] >= 0
-                       ? get_shared(&p.part[(size_t)(t * p.k + j) * p.d + o]) : 0.0f;
-        float v = p.Fs > 0 ? get_shared(&p.part[(size_t)(P + t) * p.d + o]) : 0.0f;
-#pragma unroll
-        for (int j = 0; j < MOE_MAX_K; ++j)
-            if (j < p.k && p.ids[t * p.k + j] >= 0) v = __builtin_fmaf(p.w[t * p.k + j], e[j], v);
-        if (p.out_dtype == MOE_OUT_F32)
-            ((float*)p.y)[(size_t)t * p.d + o] = v;
-        else
-            ((uint16_t*)p.y)[(size_t)t * p.d + o] = f32_to_bf16(v);
-    }
-}
-
-// Items: (expert or the shared one, 16 outputs).  The workgroup that finishes
-// an output chunk's last expert adds the experts up: which one that is does
-// not change the order of the sum.
+// One workgroup 16 outputs, of every expert in turn: its waves take the
+// experts (and the shared one) as strips, whose outputs stay in LDS by (token,
+// slot) pair until all are there and are then added in slot order, shared
+// expert first.  Nothing crosses workgroups, and a token's sum does not depend
+// on the batch it is in.
 template <bool FP8>
-__global__ __launch_bounds__(kThreads, 2) void few_down_kernel(FewArgs p) {
-    extern __shared__ __align__(16) float red_all[];
-    __shared__ int last_sh[2];
+__global__ __launch_bounds__(kThreads) void few_down_kernel(FewArgs p) {
+    extern __shared__ __align__(16) float out[];     // [P + T][16]
+    __shared__ int expert[kMaxPairs], start[kMaxPairs + 1], pairs[kMaxPairs];
+    __shared__ int ids[kMaxPairs], n_sh;
+    __shared__ float wt[kMaxPairs];
     const Lane l = this_lane();
-    const int n = *p.n_expert, sh = p.Fs > 0 ? 1 : 0;
-    const int per = p.d / 16;
-    const int nct = (p.T * p.k + 15) / 16;
-    const int buf = 8 * (nct < kTiles ? nct : kTiles) * 256;
-    if (n + sh == 0) {                     // nothing adds to y
-        for (int c = blockIdx.x; c < per; c += gridDim.x) combine_chunk(p, c, l.tid);
-        return;
+    const int P = p.T * p.k, sh = p.Fs > 0 ? 1 : 0;
+    // (one round trip: entries past the number of experts are not used)
+    if (l.tid < P) {
+        expert[l.tid] = p.expert[l.tid];
+        start[l.tid] = p.start[l.tid];
+        pairs[l.tid] = p.pairs[l.tid];
+        ids[l.tid] = p.ids[l.tid];
+        wt[l.tid] = p.w[l.tid];
     }
-    int parity = 0;
-    for (int it = blockIdx.x; it < (n + sh) * per; it += gridDim.x) {
-        const int u = it / per, chunk = it - u * per;
-        const bool shared = u == n;
-        const int s = shared ? 0 : p.start[u];
-        const int m_all = shared ? p.T : p.start[u + 1] - s;
-        const int K = shared ? p.Fs : p.F;
-        const size_t mat = shared ? 0 : (size_t)p.expert[u];
-        const size_t row = (mat * p.d + 16 * chunk + l.r16) * (size_t)K;
-        const uint8_t* wrow =
-            (const uint8_t*)(shared ? p.s_down : p.w_down) + row * (FP8 ? 1 : 2);
-        const float* srow = nullptr;
-        if constexpr (FP8) {
-            const int nbd = (p.d + 127) / 128, nbk = (K + 127) / 128;
-            srow = (shared ? p.s_down_scale : p.w_down_scale) +
-                   (mat * nbd + chunk / 8) * (size_t)nbk;
-        }
-        for (int m0 = 0; m0 < m_all; m0 += MOE_FEW_MAX_T) {
-            const int m = min(m_all - m0, MOE_FEW_MAX_T), ct = (m + 15) / 16;
-            const uint16_t* x[kTiles];
+    if (l.tid == 0) {
+        start[P] = p.start[P];
+        n_sh = *p.n_expert;
+    }
+    __syncthreads();
+    const int n = n_sh;
+    for (int chunk = blockIdx.x; chunk < p.d / 16; chunk += gridDim.x) {
+        for (int u = l.wave; u < n + sh; u += 8) {
+            const bool shared = u >= n;
+            const int s = shared ? 0 : start[u];
+            const int m_all = shared ? p.T : start[u + 1] - s;
+            const int K = shared ? p.Fs : p.F;
+            const size_t mat = shared ? 0 : (size_t)expert[u];
+            Strip<FP8> st;
+            st.wrow = (const uint8_t*)(shared ? p.s_down : p.w_down) +
+                      (mat * p.d + 16 * chunk + l.r16) * (size_t)K * (FP8 ? 1 : 2);
+            st.K = K;
+            st.grp = l.grp;
+            if constexpr (FP8) {
+                const int nbd = (p.d + 127) / 128, nbk = (K + 127) / 128;
+                st.srow = (shared ? p.s_down_scale : p.w_down_scale) +
+                          (mat * nbd + chunk / 8) * (size_t)nbk;
+            }
+            for (int m0 = 0; m0 < m_all; m0 += MOE_FEW_MAX_T) {
+                const int m = min(m_all - m0, MOE_FEW_MAX_T), ct = (m + 15) / 16;
+                const uint16_t* x[kTiles];
+                int slot[kTiles];
 #pragma unroll
-            for (int c = 0; c < kTiles; ++c) {
-                const int r = m0 + 16 * c + l.r16;
-                x[c] = r - m0 >= m ? nullptr
-                       : shared    ? p.hs + (size_t)r * K
-                                   : p.h + (size_t)p.pairs[s + r] * K;
-            }
-            f32x4 acc[kTiles];
-            zero_acc(acc);
-            strip<FP8>(wrow, srow, K, x, ct, l, acc);
-            float* red = red_all + parity * buf;
-            parity ^= 1;
-            put_partials(red, acc, ct, l);
-            __syncthreads();
-            for (int i = l.tid; i < 256 * ct; i += kThreads) {
-                const int o = i & 15, r = i >> 4;
-                if (r < m) {
-                    const size_t slot =
-                        shared ? (size_t)p.T * p.k + r : (size_t)p.pairs[s + m0 + r];
-                    put_shared(&p.part[slot * p.d + 16 * chunk + o],
-                               sum_partials(red, ct, r >> 4, o, r & 15));
+                for (int c = 0; c < kTiles; ++c) {
+                    const int r = m0 + min(16 * c + l.r16, m - 1);
+                    slot[c] = shared ? P + r : pairs[s + r];
+                    x[c] = shared ? p.hs + (size_t)r * K : p.h + (size_t)slot[c] * K;
                 }
+                f32x4 acc[kTiles];
+                zero_acc(acc);
+                st.run(x, ct, 0, 1, acc);
+#pragma unroll
+                for (int c = 0; c < kTiles; ++c)
+                    if (c < ct && 16 * c + l.r16 < m)
+                        *(f32x4*)(out + slot[c] * 16 + 4 * l.grp) = acc[c];
             }
         }
-        stores_done();                     // the partial outputs, before the count
         __syncthreads();
-        int* last = &last_sh[parity];
-        if (l.tid == 0)
-            *last = __hip_atomic_fetch_add(&p.count[chunk], 1u, __ATOMIC_RELAXED,
-                                           __HIP_MEMORY_SCOPE_AGENT) == (unsigned)(n + sh - 1);
+        for (int i = l.tid; i < p.T * 16; i += kThreads) {
+            const int t = i >> 4, o = i & 15;
+            float v = sh ? out[(P + t) * 16 + o] : 0.0f;
+            for (int j = 0; j < p.k; ++j)
+                if (ids[t * p.k + j] >= 0)
+                    v = __builtin_fmaf(wt[t * p.k + j], out[(t * p.k + j) * 16 + o], v);
+            const size_t at = (size_t)t * p.d + 16 * chunk + o;
+            if (p.out_dtype == MOE_OUT_F32)
+                ((float*)p.y)[at] = v;
+            else
+                ((uint16_t*)p.y)[at] = f32_to_bf16(v);
+        }
         __syncthreads();
-        if (*last) combine_chunk(p, chunk, l.tid);
     }
-}
-
-// (up to 64 tokens need more dynamic LDS than the default limit)
-template <bool FP8>
-hipError_t set_up() {
-    static DeviceSetup setup;
-    long long a = 0, b = 0;
-    return device_setup(setup, a, b, [](int, long long&, long long&) {
-        hipError_t e = hipSuccess;
-        for (const void* fn : {(const void*)few_gate_up_kernel<FP8>,
-                               (const void*)few_down_kernel<FP8>})
-            if (e == hipSuccess)
-                e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                        2 * kTiles * 8 * 256 * (int)sizeof(float));
-        return e;
-    });
 }
 
 template <bool FP8>
 hipError_t launch(const FewArgs& p, hipStream_t stream) {
-    hipError_t e = set_up<FP8>();
-    if (e != hipSuccess) return e;
-    const int nt_tok = (p.T + 15) / 16;
-    const int nt_pair = (p.T * p.k + 15) / 16 < kTiles ? (p.T * p.k + 15) / 16 : kTiles;
-    const size_t wave_tile = 8 * 256 * sizeof(float);
+    const size_t red = (size_t)((p.T + 15) / 16) * 8 * 256 * sizeof(float);
     const int grid1 = (p.E + 15) / 16 + (p.Fs > 0 ? p.Fs / 8 : 0);
-    hipLaunchKernelGGL(few_router_kernel<FP8>, dim3(grid1), dim3(kThreads), nt_tok * wave_tile,
-                       stream, p);
+    hipLaunchKernelGGL(few_router_kernel<FP8>, dim3(grid1), dim3(kThreads), red, stream, p);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int cus = device_cu_count();
+    hipLaunchKernelGGL(few_gate_up_kernel<FP8>, dim3(cus), dim3(kThreads), 0, stream, p);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int grid = 2 * device_cu_count();
-    hipLaunchKernelGGL(few_gate_up_kernel<FP8>, dim3(grid), dim3(kThreads),
-                       2 * nt_pair * wave_tile, stream, p);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(few_down_kernel<FP8>, dim3(grid), dim3(kThreads), 2 * nt_pair * wave_tile,
-                       stream, p);
+    hipLaunchKernelGGL(few_down_kernel<FP8>, dim3(p.d / 16 < cus ? p.d / 16 : cus),
+                       dim3(kThreads), (size_t)(p.T * p.k + p.T) * 16 * sizeof(float), stream, p);
     return hipGetLastError();
 }
 
