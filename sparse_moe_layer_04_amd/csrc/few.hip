@@ -43,11 +43,11 @@ __device__ __forceinline__ Lane this_lane() {
 }
 
 // The products of a strip: acc[c] += W[16 rows] x^T for column tiles c < ct,
-// over the pieces first, first + step, ... of K.
+// over the pieces first, first + STEP, ... of K.
 // wrow: this lane's weight row (row r16 of the strip); srow: its block scales
-// (8-bit weights); x[c]: the activations of column r16 of tile c (a tile's
+// (8-bit weights); row(c): the activations of column r16 of tile c (a tile's
 // columns past its last token may be anything: no output of theirs is used).
-template <bool FP8>
+template <bool FP8, int STEP>
 struct Strip {
     static constexpr int UK = FP8 ? 128 : 64;  // K a piece (128 bytes of a row)
     static constexpr int R = 8;                // weight pieces in flight a wave
@@ -57,135 +57,180 @@ struct Strip {
     const uint8_t* wrow;
     const float* srow;
     int K, grp;
-    u32x4 w[R][2];
-    float sc[R];
-    u32x4 xv[RX][XL];
 
-    // piece u; the second half of the last one may lie past K, a multiple of
-    // 64: zeros (8-bit)
-    __device__ __forceinline__ void load_w(int u, u32x4 (&v)[2], float& s) const {
-        const uint8_t* q = wrow + (size_t)u * 128 + 16 * grp;
+    static __device__ __forceinline__ void load_w(const uint8_t* q, u32x4 (&v)[2]) {
+        v[0] = *(const u32x4*)q;
+        v[1] = *(const u32x4*)(q + 64);
+    }
+    static __device__ __forceinline__ void load_x(const uint16_t* q, u32x4 (&v)[XL]) {
         v[0] = *(const u32x4*)q;
         if constexpr (FP8) {
-            const bool in = u * UK + 64 < K;
-            v[1] = *(const u32x4*)(in ? q + 64 : q);
-            s = srow[u];
+            v[1] = *(const u32x4*)(q + 8);
+            v[2] = *(const u32x4*)(q + 64);
+            v[3] = *(const u32x4*)(q + 72);
         } else {
-            v[1] = *(const u32x4*)(q + 64);
+            v[1] = *(const u32x4*)(q + 32);
         }
     }
-    __device__ __forceinline__ void load_x(const uint16_t* x, int u, u32x4 (&v)[XL]) const {
-        const uint16_t* q = x + (size_t)u * UK;
+    // half h of a piece
+    static __device__ __forceinline__ void multiply_half(int h, const u32x4& wv,
+                                                         const u32x4 (&x)[XL], f32x4& acc) {
         if constexpr (FP8) {
-            v[0] = *(const u32x4*)(q + 16 * grp);
-            v[1] = *(const u32x4*)(q + 16 * grp + 8);
-            const uint16_t* h = u * UK + 64 < K ? q + 64 : q;
-            v[2] = *(const u32x4*)(h + 16 * grp);
-            v[3] = *(const u32x4*)(h + 16 * grp + 8);
-        } else {
-            v[0] = *(const u32x4*)(q + 8 * grp);
-            v[1] = *(const u32x4*)(q + 32 + 8 * grp);
-        }
-    }
-    __device__ __forceinline__ void multiply(int u, const u32x4 (&wv)[2], float s,
-                                             const u32x4 (&x)[XL], f32x4& acc) const {
-        if constexpr (FP8) {
-            f32x4 part = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-                part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    fp8x8_to_bf16x8(u32x2{wv[0][2 * q], wv[0][2 * q + 1]}, 1.0f),
-                    __builtin_bit_cast(bf16x8, x[q]), part, 0, 0, 0);
-            if (u * UK + 64 < K) {
-#pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        fp8x8_to_bf16x8(u32x2{wv[1][2 * q], wv[1][2 * q + 1]}, 1.0f),
-                        __builtin_bit_cast(bf16x8, x[2 + q]), part, 0, 0, 0);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(part[e], s, acc[e]);
-        } else {
 #pragma unroll
             for (int q = 0; q < 2; ++q)
                 acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    __builtin_bit_cast(bf16x8, wv[q]), __builtin_bit_cast(bf16x8, x[q]), acc, 0, 0,
-                    0);
+                    fp8x8_to_bf16x8(u32x2{wv[2 * q], wv[2 * q + 1]}, 1.0f),
+                    __builtin_bit_cast(bf16x8, x[2 * h + q]), acc, 0, 0, 0);
+        } else {
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, wv),
+                                                          __builtin_bit_cast(bf16x8, x[h]), acc, 0,
+                                                          0, 0);
         }
     }
-    // pieces first + step * i of K
-    __device__ __forceinline__ void run(const uint16_t* const (&x)[kTiles], int ct, int first,
-                                        int step, f32x4 (&acc)[kTiles]) {
-        const int nu = (K + UK - 1) / UK;
-        const int n = first < nu ? (nu - first + step - 1) / step : 0;
-        if (ct == 1)
-            run_one(x[0], n, first, step, acc[0]);
-        else
-            run_tiles(x, ct, n, first, step, acc);
+    static __device__ __forceinline__ void multiply(const u32x4 (&wv)[2], float s,
+                                                    const u32x4 (&x)[XL], f32x4& acc) {
+        if constexpr (FP8) {
+            f32x4 part = {0.0f, 0.0f, 0.0f, 0.0f};
+            multiply_half(0, wv[0], x, part);
+            multiply_half(1, wv[1], x, part);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(part[e], s, acc[e]);
+        } else {
+            multiply_half(0, wv[0], x, acc);
+            multiply_half(1, wv[1], x, acc);
+        }
+    }
+    // whole pieces of this wave, and whether it has the half piece that a K of
+    // an odd number of 64s ends in (8-bit)
+    __device__ __forceinline__ int pieces(int first) const {
+        const int nu = K / UK;
+        return first < nu ? (nu - first + STEP - 1) / STEP : 0;
+    }
+    __device__ __forceinline__ bool has_half(int first) const {
+        return FP8 && K % UK && K / UK % STEP == first % STEP;
+    }
+    __device__ __forceinline__ void half_piece(const uint16_t* x, f32x4& acc) const {
+        const int u = K / UK;
+        const u32x4 wv = *(const u32x4*)(wrow + (size_t)u * 128 + 16 * grp);
+        u32x4 v[XL];
+        const uint16_t* q = x + (size_t)u * UK + 16 * grp;
+        v[0] = *(const u32x4*)q;
+        v[1] = *(const u32x4*)(q + 8);
+        f32x4 part = {0.0f, 0.0f, 0.0f, 0.0f};
+        multiply_half(0, wv, v, part);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(part[e], srow[u], acc[e]);
     }
     // one column tile: weights R pieces ahead, activations RX
-    __device__ __forceinline__ void run_one(const uint16_t* x, int n, int first, int step,
-                                            f32x4& acc) {
+    __device__ __forceinline__ f32x4 run_one(const uint16_t* x, int first) const {
+        constexpr int WB = STEP * 128, XB = STEP * UK;   // weight bytes, activations a piece
+        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        const int n = pieces(first);
+        u32x4 w[R][2], xv[RX][XL];
+        float sc[R] = {};
+        const uint8_t* wq = wrow + (size_t)first * 128 + 16 * grp;
+        const uint16_t* xq = x + (size_t)first * UK + (FP8 ? 16 : 8) * grp;
+        const float* sq = FP8 ? srow + first : nullptr;
 #pragma unroll
         for (int i = 0; i < R; ++i)
-            if (i < n) load_w(first + step * i, w[i], sc[i]);
+            if (i < n) {
+                load_w(wq + i * WB, w[i]);
+                if constexpr (FP8) sc[i] = sq[i * STEP];
+            }
 #pragma unroll
         for (int i = 0; i < RX; ++i)
-            if (i < n) load_x(x, first + step * i, xv[i]);
-        int i0 = 0;
-        for (; i0 + 2 * R <= n; i0 += R) {
+            if (i < n) load_x(xq + i * XB, xv[i]);
+        int left = n;
+        for (; left >= 2 * R; left -= R) {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                multiply(first + step * (i0 + i), w[i], sc[i], xv[i % RX], acc);
-                load_w(first + step * (i0 + i + R), w[i], sc[i]);
-                load_x(x, first + step * (i0 + i + RX), xv[i % RX]);
+                multiply(w[i], sc[i], xv[i % RX], acc);
+                load_w(wq + (i + R) * WB, w[i]);
+                if constexpr (FP8) sc[i] = sq[(i + R) * STEP];
+                load_x(xq + (i + RX) * XB, xv[i % RX]);
             }
+            wq += R * WB;
+            xq += R * XB;
+            if constexpr (FP8) sq += R * STEP;
         }
-        for (; i0 < n; i0 += R) {
+#pragma unroll 1
+        for (; left > 0; left -= R) {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const int k = i0 + i;
-                if (k < n) multiply(first + step * k, w[i], sc[i], xv[i % RX], acc);
-                if (k + R < n) load_w(first + step * (k + R), w[i], sc[i]);
-                if (k + RX < n) load_x(x, first + step * (k + RX), xv[i % RX]);
+                if (i < left) multiply(w[i], sc[i], xv[i % RX], acc);
+                if (i + R < left) {
+                    load_w(wq + (i + R) * WB, w[i]);
+                    if constexpr (FP8) sc[i] = sq[(i + R) * STEP];
+                }
+                if (i + RX < left) load_x(xq + (i + RX) * XB, xv[i % RX]);
             }
+            wq += R * WB;
+            xq += R * XB;
+            if constexpr (FP8) sq += R * STEP;
         }
+        if (has_half(first)) half_piece(x, acc);
+        return acc;
     }
     // more tokens: each piece against all tiles, the next piece's weights ahead
-    __device__ __forceinline__ void run_tiles(const uint16_t* const (&x)[kTiles], int ct, int n,
-                                              int first, int step, f32x4 (&acc)[kTiles]) {
-        if (n == 0) return;
-        load_w(first, w[0], sc[0]);
+    template <class Row>
+    __device__ __forceinline__ void run_tiles(const Row& row, int ct, int first,
+                                              f32x4 (&acc)[kTiles]) const {
+        const int n = pieces(first);
+        const uint16_t* x[kTiles];
+#pragma unroll
+        for (int c = 0; c < kTiles; ++c) {
+            x[c] = row(c < ct ? c : 0);
+            acc[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        const uint8_t* wq = wrow + (size_t)first * 128 + 16 * grp;
+        int at = first * UK + (FP8 ? 16 : 8) * grp;
+        u32x4 w[2];
+        if (n > 0) load_w(wq, w);
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
-            const int u = first + step * i;
-            load_w(first + step * min(i + 1, n - 1), w[1], sc[1]);
+            u32x4 w2[2], xv[kTiles][XL];
+            const float s = FP8 ? srow[first + STEP * i] : 0.0f;
+            wq += i + 1 < n ? STEP * 128 : 0;
+            load_w(wq, w2);
 #pragma unroll
             for (int c = 0; c < kTiles; ++c)
-                if (c < ct) load_x(x[c], u, xv[c]);
+                if (c < ct) load_x(x[c] + at, xv[c]);
 #pragma unroll
             for (int c = 0; c < kTiles; ++c)
-                if (c < ct) multiply(u, w[0], sc[0], xv[c], acc[c]);
-            w[0][0] = w[1][0];
-            w[0][1] = w[1][1];
-            sc[0] = sc[1];
+                if (c < ct) multiply(w, s, xv[c], acc[c]);
+            w[0] = w2[0];
+            w[1] = w2[1];
+            at += STEP * UK;
+        }
+        if (has_half(first)) {
+#pragma unroll
+            for (int c = 0; c < kTiles; ++c)
+                if (c < ct) half_piece(x[c], acc[c]);
         }
     }
+    // done(c, sums): called for every tile c < ct
+    template <class Row, class Done>
+    __device__ __forceinline__ void run(const Row& row, int ct, int first, const Done& done) const {
+        if (ct == 1) {
+            done(0, run_one(row(0), first));
+            return;
+        }
+        f32x4 acc[kTiles];
+        run_tiles(row, ct, first, acc);
+#pragma unroll
+        for (int c = 0; c < kTiles; ++c)
+            if (c < ct) done(c, acc[c]);
+    }
 };
-static_assert(Strip<true>::RX >= kTiles && Strip<false>::RX >= kTiles, "a register set a tile");
 
 // A strip whose K is split over the 8 waves: their partial sums meet in LDS,
 // red [8 waves][ct][16 rows][16 columns], and are added in wave order.  Lane l
 // holds rows 4 (l / 16) + e of column l % 16.
-__device__ __forceinline__ void put_partials(float* red, const f32x4 (&acc)[kTiles], int ct,
+__device__ __forceinline__ void put_partials(float* red, const f32x4& acc, int c, int ct,
                                              const Lane& l) {
 #pragma unroll
-    for (int c = 0; c < kTiles; ++c) {
-        if (c >= ct) break;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            red[((l.wave * ct + c) * 16 + 4 * l.grp + e) * 16 + l.r16] = acc[c][e];
-    }
+    for (int e = 0; e < 4; ++e)
+        red[((l.wave * ct + c) * 16 + 4 * l.grp + e) * 16 + l.r16] = acc[e];
 }
 
 __device__ __forceinline__ float sum_partials(const float* red, int ct, int c, int row, int col) {
@@ -195,16 +240,11 @@ __device__ __forceinline__ float sum_partials(const float* red, int ct, int c, i
     return s;
 }
 
-__device__ __forceinline__ void zero_acc(f32x4 (&acc)[kTiles]) {
-#pragma unroll
-    for (int c = 0; c < kTiles; ++c) acc[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-}
-
 // the 16 rows of a gate/up strip: gate rows of features f0 .. f0 + 7, then the
 // up rows of the same features.  (A lane's scales are those of its outputs,
 // rows 4 (l / 16) + e, not of the row it loads.)
-template <bool FP8>
-__device__ __forceinline__ void set_gate_up(Strip<FP8>& s, const void* gate, const void* up,
+template <bool FP8, int STEP>
+__device__ __forceinline__ void set_gate_up(Strip<FP8, STEP>& s, const void* gate, const void* up,
                                             const float* sg, const float* su, size_t mat, int f0,
                                             int F, int d, const Lane& l) {
     const size_t row = (mat * F + f0 + (l.r16 & 7)) * (size_t)d;
@@ -226,19 +266,15 @@ __global__ __launch_bounds__(kThreads) void few_router_kernel(FewArgs p) {
     const Lane l = this_lane();
     const int ct = (p.T + 15) / 16;
     const int nr = (p.E + 15) / 16;
-    const uint16_t* x[kTiles];
-#pragma unroll
-    for (int c = 0; c < kTiles; ++c) x[c] = p.x + (size_t)min(16 * c + l.r16, p.T - 1) * p.d;
-    f32x4 acc[kTiles];
-    zero_acc(acc);
+    auto row = [&](int c) { return p.x + (size_t)min(16 * c + l.r16, p.T - 1) * p.d; };
+    auto partials = [&](int c, const f32x4& acc) { put_partials(red, acc, c, ct, l); };
     const int item = blockIdx.x;
     if (item < nr) {
-        Strip<false> st;
+        Strip<false, 8> st;
         st.wrow = (const uint8_t*)(p.w_g + (size_t)min(16 * item + l.r16, p.E - 1) * p.d);
         st.K = p.d;
         st.grp = l.grp;
-        st.run(x, ct, l.wave, 8, acc);
-        put_partials(red, acc, ct, l);
+        st.run(row, ct, l.wave, partials);
         __syncthreads();
         for (int i = l.tid; i < 256 * ct; i += kThreads) {
             const int row = i & 15, t = i >> 4, en = 16 * item + row;
@@ -250,10 +286,9 @@ __global__ __launch_bounds__(kThreads) void few_router_kernel(FewArgs p) {
         }
     } else {
         const int f0 = 8 * (item - nr);
-        Strip<FP8> st;
+        Strip<FP8, 8> st;
         set_gate_up(st, p.s_gate, p.s_up, p.s_gate_scale, p.s_up_scale, 0, f0, p.Fs, p.d, l);
-        st.run(x, ct, l.wave, 8, acc);
-        put_partials(red, acc, ct, l);
+        st.run(row, ct, l.wave, partials);
         __syncthreads();
         for (int i = l.tid; i < 128 * ct; i += kThreads) {
             const int f = i & 7, t = i >> 3;
@@ -403,38 +438,22 @@ __global__ __launch_bounds__(kThreads) void few_gate_up_kernel(FewArgs p) {
         // there are tokens: in runs of MOE_FEW_MAX_T)
         for (int m0 = 0; m0 < m_all; m0 += MOE_FEW_MAX_T) {
             const int m = min(m_all - m0, MOE_FEW_MAX_T), ct = (m + 15) / 16;
-            const uint16_t* x[kTiles];
-            int pair[kTiles];
-#pragma unroll
-            for (int c = 0; c < kTiles; ++c) {
-                pair[c] = tb.pairs[s + m0 + min(16 * c + l.r16, m - 1)];
-                x[c] = p.x + (size_t)(pair[c] / p.k) * p.d;
-            }
-            f32x4 acc[kTiles];
-            zero_acc(acc);
-            Strip<FP8> st;
+            auto pair = [&](int c) { return tb.pairs[s + m0 + min(16 * c + l.r16, m - 1)]; };
+            Strip<FP8, 1> st;
             set_gate_up(st, p.w_gate, p.w_up, p.w_gate_scale, p.w_up_scale, e, f0, p.F, p.d, l);
-            st.run(x, ct, 0, 1, acc);
             // lanes 0-31 hold the gate sums of features 4 grp + e, lanes 32-63
             // the up sums of the same ones
+            st.run([&](int c) { return p.x + (size_t)(pair(c) / p.k) * p.d; }, ct, 0,
+                   [&](int c, const f32x4& acc) {
+                       float v[4];
 #pragma unroll
-            for (int c = 0; c < kTiles; ++c) {
-                if (c >= ct) break;
-                uint32_t h[2];
-#pragma unroll
-                for (int e2 = 0; e2 < 2; ++e2) {
-                    float v[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float mine = acc[c][2 * e2 + i];
-                        v[i] = clamped_swiglu(mine, __shfl_xor(mine, 32, 64), p.clamp_limit,
-                                              p.clamp_mode);
-                    }
-                    h[e2] = bf16_pack2(v[0], v[1]);
-                }
-                if (l.grp < 2 && 16 * c + l.r16 < m)
-                    *(u32x2*)(p.h + (size_t)pair[c] * p.F + f0 + 4 * l.grp) = u32x2{h[0], h[1]};
-            }
+                       for (int i = 0; i < 4; ++i)
+                           v[i] = clamped_swiglu(acc[i], __shfl_xor(acc[i], 32, 64),
+                                                 p.clamp_limit, p.clamp_mode);
+                       if (l.grp < 2 && 16 * c + l.r16 < m)
+                           *(u32x2*)(p.h + (size_t)pair(c) * p.F + f0 + 4 * l.grp) =
+                               u32x2{bf16_pack2(v[0], v[1]), bf16_pack2(v[2], v[3])};
+                   });
         }
     }
 }
@@ -474,7 +493,7 @@ __global__ __launch_bounds__(kThreads) void few_down_kernel(FewArgs p) {
             const int m_all = shared ? p.T : start[u + 1] - s;
             const int K = shared ? p.Fs : p.F;
             const size_t mat = shared ? 0 : (size_t)expert[u];
-            Strip<FP8> st;
+            Strip<FP8, 1> st;
             st.wrow = (const uint8_t*)(shared ? p.s_down : p.w_down) +
                       (mat * p.d + 16 * chunk + l.r16) * (size_t)K * (FP8 ? 1 : 2);
             st.K = K;
@@ -486,21 +505,16 @@ __global__ __launch_bounds__(kThreads) void few_down_kernel(FewArgs p) {
             }
             for (int m0 = 0; m0 < m_all; m0 += MOE_FEW_MAX_T) {
                 const int m = min(m_all - m0, MOE_FEW_MAX_T), ct = (m + 15) / 16;
-                const uint16_t* x[kTiles];
-                int slot[kTiles];
-#pragma unroll
-                for (int c = 0; c < kTiles; ++c) {
+                auto slot = [&](int c) {
                     const int r = m0 + min(16 * c + l.r16, m - 1);
-                    slot[c] = shared ? P + r : pairs[s + r];
-                    x[c] = shared ? p.hs + (size_t)r * K : p.h + (size_t)slot[c] * K;
-                }
-                f32x4 acc[kTiles];
-                zero_acc(acc);
-                st.run(x, ct, 0, 1, acc);
-#pragma unroll
-                for (int c = 0; c < kTiles; ++c)
-                    if (c < ct && 16 * c + l.r16 < m)
-                        *(f32x4*)(out + slot[c] * 16 + 4 * l.grp) = acc[c];
+                    return shared ? P + r : pairs[s + r];
+                };
+                st.run([&](int c) { return shared ? p.hs + (size_t)(slot(c) - P) * K
+                                                  : p.h + (size_t)slot(c) * K; },
+                       ct, 0, [&](int c, const f32x4& acc) {
+                           if (16 * c + l.r16 < m)
+                               *(f32x4*)(out + slot(c) * 16 + 4 * l.grp) = acc;
+                       });
             }
         }
         __syncthreads();
