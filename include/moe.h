@@ -74,6 +74,8 @@ extern "C" {
 
 #define MOE_FLAG_BAD_INPUT_ID 1u  /* an input id outside [0, V) */
 #define MOE_FLAG_BAD_EXPERT_ID 2u /* an expert id outside [0, E) */
+#define MOE_FLAG_OVERLAP 4u       /* moe_forward_few: another call used the
+                                     workspace at the same time */
 
 /* Limits: 1 <= k <= 8, k <= E, 1 <= E <= 1024 (route/permute/forward);
  * d, F multiples of 64 (expert FFN, forward); T * k < 2^31; G <= 4096.
@@ -566,7 +568,7 @@ int moe_forward_timed(const moe_cfg* cfg, const moe_weights* w, const uint16_t* 
 
 /* ------------------------------------------------------------------------
  * Whole layer forward for a few tokens (decoding): the layer of moe_forward
- * for T <= MOE_FEW_MAX_T tokens, on weights as checkpoints hold them, in three
+ * for T <= MOE_FEW_MAX_T tokens, on weights as checkpoints hold them, in two
  * kernels without a dispatch permutation.  Arguments, limits and outputs as
  * moe_forward, with
  *   w->packed == 0: bf16 matrices [out, in], or MOE_WEIGHTS_FP8_BLOCK: 8-bit

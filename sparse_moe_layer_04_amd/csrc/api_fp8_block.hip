@@ -158,10 +158,7 @@ size_t few_layout(const moe_cfg* c, char* base, FewArgs& p) {
     p.w = (float*)take(N * 4);
     p.hs = (uint16_t*)take(T * (size_t)(c->F_shared > 0 ? c->F_shared : 0) * 2);
     p.h = (uint16_t*)take(N * c->F * 2);
-    p.expert = (int32_t*)take(N * 4);
-    p.start = (int32_t*)take((N + 1) * 4);
-    p.pairs = (int32_t*)take(N * 4);
-    p.n_expert = (int32_t*)take(4);
+    p.sync = (uint32_t*)take(MOE_FEW_SYNC_BYTES);
     return off;
 }
 

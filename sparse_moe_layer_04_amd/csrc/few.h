@@ -5,6 +5,8 @@
 
 namespace moe {
 
+constexpr int MOE_FEW_SYNC_BYTES = 3 * 8 * 128;
+
 struct FewArgs {
     int T, d, E, k, F, Fs, mode, n_bias, V;
     float scale, clamp_limit;
@@ -28,10 +30,7 @@ struct FewArgs {
     float* w;                      // [T, k]
     uint16_t* hs;                  // [T, Fs] bf16
     uint16_t* h;                   // [T k, F] bf16, by pair
-    int32_t* expert;               // distinct experts
-    int32_t* start;                // [+ 1]
-    int32_t* pairs;
-    int32_t* n_expert;
+    uint32_t* sync;                // tickets and counts, MOE_FEW_SYNC_BYTES
 };
 
 hipError_t launch_few(bool fp8, const FewArgs& p, hipStream_t stream);

@@ -26,6 +26,7 @@ namespace {
 constexpr int kThreads = 512;              // 8 waves
 constexpr int kTiles = MOE_FEW_MAX_T / 16; // column tiles of 16 tokens
 constexpr int kMaxPairs = MOE_FEW_MAX_T * MOE_MAX_K;
+constexpr int kMaxPolls = 1 << 22;
 static_assert(kMaxPairs <= kThreads, "one thread a (token, slot) pair");
 
 struct Lane {
@@ -50,7 +51,7 @@ __device__ __forceinline__ Lane this_lane() {
 template <bool FP8, int STEP>
 struct Strip {
     static constexpr int UK = FP8 ? 128 : 64;  // K a piece (128 bytes of a row)
-    static constexpr int R = 8;                // weight pieces in flight a wave
+    static constexpr int R = STEP == 1 ? 8 : 4;  // weight pieces in flight a wave
     static constexpr int RX = 4;               // activation pieces
     static constexpr int XL = FP8 ? 4 : 2;     // 16-byte activation loads a piece
 
@@ -121,8 +122,11 @@ struct Strip {
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(part[e], srow[u], acc[e]);
     }
-    // one column tile: weights R pieces ahead, activations RX
-    __device__ __forceinline__ f32x4 run_one(const uint16_t* x, int first) const {
+    // one column tile: weights R pieces ahead, activations RX; ready() returns
+    // when the activations may be read
+    template <class Ready>
+    __device__ __forceinline__ f32x4 run_one(const uint16_t* x, int first,
+                                             const Ready& ready) const {
         constexpr int WB = STEP * 128, XB = STEP * UK;   // weight bytes, activations a piece
         f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
         const int n = pieces(first);
@@ -137,6 +141,7 @@ struct Strip {
                 load_w(wq + i * WB, w[i]);
                 if constexpr (FP8) sc[i] = sq[i * STEP];
             }
+        ready();
 #pragma unroll
         for (int i = 0; i < RX; ++i)
             if (i < n) load_x(xq + i * XB, xv[i]);
@@ -209,12 +214,14 @@ struct Strip {
         }
     }
     // done(c, sums): called for every tile c < ct
-    template <class Row, class Done>
-    __device__ __forceinline__ void run(const Row& row, int ct, int first, const Done& done) const {
+    template <class Row, class Ready, class Done>
+    __device__ __forceinline__ void run(const Row& row, int ct, int first, const Ready& ready,
+                                        const Done& done) const {
         if (ct == 1) {
-            done(0, run_one(row(0), first));
+            done(0, run_one(row(0), first, ready));
             return;
         }
+        ready();
         f32x4 acc[kTiles];
         run_tiles(row, ct, first, acc);
 #pragma unroll
@@ -269,12 +276,15 @@ __global__ __launch_bounds__(kThreads) void few_router_kernel(FewArgs p) {
     auto row = [&](int c) { return p.x + (size_t)min(16 * c + l.r16, p.T - 1) * p.d; };
     auto partials = [&](int c, const f32x4& acc) { put_partials(red, acc, c, ct, l); };
     const int item = blockIdx.x;
+    // the next kernel's counters
+    if (item == 0)
+        for (int i = l.tid; i < MOE_FEW_SYNC_BYTES / 4; i += kThreads) p.sync[i] = 0u;
     if (item < nr) {
         Strip<false, 8> st;
         st.wrow = (const uint8_t*)(p.w_g + (size_t)min(16 * item + l.r16, p.E - 1) * p.d);
         st.K = p.d;
         st.grp = l.grp;
-        st.run(row, ct, l.wave, partials);
+        st.run(row, ct, l.wave, [] {}, partials);
         __syncthreads();
         for (int i = l.tid; i < 256 * ct; i += kThreads) {
             const int row = i & 15, t = i >> 4, en = 16 * item + row;
@@ -288,7 +298,7 @@ __global__ __launch_bounds__(kThreads) void few_router_kernel(FewArgs p) {
         const int f0 = 8 * (item - nr);
         Strip<FP8, 8> st;
         set_gate_up(st, p.s_gate, p.s_up, p.s_gate_scale, p.s_up_scale, 0, f0, p.Fs, p.d, l);
-        st.run(row, ct, l.wave, partials);
+        st.run(row, ct, l.wave, [] {}, partials);
         __syncthreads();
         for (int i = l.tid; i < 128 * ct; i += kThreads) {
             const int f = i & 7, t = i >> 3;
@@ -411,88 +421,164 @@ __device__ __forceinline__ void build_table(const FewArgs& p, const Lane& l, Tab
     __syncthreads();
 }
 
-// ------------------------------------------------------- routed gate and up --
-// One wave a strip: (expert, 8 features), every token of the expert at once
-// (16 columns; more in further column tiles).
-template <bool FP8>
-__global__ __launch_bounds__(kThreads) void few_gate_up_kernel(FewArgs p) {
-    __shared__ Table tb;
-    const Lane l = this_lane();
-    build_table(p, l, tb);
-    const int n = tb.n, P = p.T * p.k;
-    if (blockIdx.x == 0) {
-        // the table, for the last kernel
-        for (int i = l.tid; i < P; i += kThreads) {
-            p.expert[i] = tb.expert[i];
-            p.pairs[i] = tb.pairs[i];
-        }
-        for (int i = l.tid; i <= n; i += kThreads) p.start[i] = tb.start[i];
-        if (l.tid == 0) *p.n_expert = n;
-    }
-    const int per = p.F / 8;
-    // strips dealt to the workgroups first, so that few strips use every CU
-    for (int it = l.wave * gridDim.x + blockIdx.x; it < n * per; it += 8 * gridDim.x) {
-        const int u = it / per, f0 = (it - u * per) * 8;
-        const int e = tb.expert[u], s = tb.start[u], m_all = tb.start[u + 1] - s;
-        // (repeated ids of a hash table can give an expert more rows than
-        // there are tokens: in runs of MOE_FEW_MAX_T)
-        for (int m0 = 0; m0 < m_all; m0 += MOE_FEW_MAX_T) {
-            const int m = min(m_all - m0, MOE_FEW_MAX_T), ct = (m + 15) / 16;
-            auto pair = [&](int c) { return tb.pairs[s + m0 + min(16 * c + l.r16, m - 1)]; };
-            Strip<FP8, 1> st;
-            set_gate_up(st, p.w_gate, p.w_up, p.w_gate_scale, p.w_up_scale, e, f0, p.F, p.d, l);
-            // lanes 0-31 hold the gate sums of features 4 grp + e, lanes 32-63
-            // the up sums of the same ones
-            st.run([&](int c) { return p.x + (size_t)(pair(c) / p.k) * p.d; }, ct, 0,
-                   [&](int c, const f32x4& acc) {
-                       float v[4];
-#pragma unroll
-                       for (int i = 0; i < 4; ++i)
-                           v[i] = clamped_swiglu(acc[i], __shfl_xor(acc[i], 32, 64),
-                                                 p.clamp_limit, p.clamp_mode);
-                       if (l.grp < 2 && 16 * c + l.r16 < m)
-                           *(u32x2*)(p.h + (size_t)pair(c) * p.F + f0 + 4 * l.grp) =
-                               u32x2{bf16_pack2(v[0], v[1]), bf16_pack2(v[2], v[3])};
-                   });
-        }
-    }
+// ------------------------------------------------------ the routed experts --
+// Gate and up, down and combine in one launch.  Workgroups take work by
+// tickets: gridDim.x shares of the gate/up strips first, then the chunks of 16
+// outputs.  A chunk needs every share, and a workgroup turns to the chunks
+// only once all shares have been taken, by workgroups that are running: who
+// waits, waits for work that is going on, however many workgroups the device
+// holds at once.  Each of 8 slots (blockIdx % 8, an XCD's workgroups) has its
+// own share of the tickets and counts, a line apart: on one counter 256
+// workgroups queue for 16 us.
+//
+// Gate/up: one wave a strip (expert, 8 features), every token of the expert at
+// once (16 columns; more in further column tiles).
+// Down: the waves of a workgroup take the experts (and the shared one) of its
+// 16 outputs; what they find stays in LDS by (token, slot) pair until all are
+// there and is then added in slot order, shared expert first, so that a
+// token's sum does not depend on the batch it is in.  The first weights of a
+// chunk are on their way while its waves wait for the shares.
+//
+// h crosses the XCDs, whose L2s are not coherent: it is stored at device scope
+// (a fence would write a whole L2 back), counted once the stores have
+// completed, and read after an acquire fence behind the count.
+constexpr int kSlots = 8;
+__device__ __forceinline__ uint32_t* sync_word(const FewArgs& p, int kind, int slot) {
+    return p.sync + (kind * kSlots + slot) * 32;
+}
+enum SyncKind : int { kShares = 0, kChunks = 1, kDone = 2 };
+constexpr int kSyncWords = 3 * kSlots * 32;
+static_assert(kSyncWords * 4 == MOE_FEW_SYNC_BYTES, "workspace of the counters");
+__device__ __forceinline__ unsigned take(uint32_t* counter) {
+    return __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ unsigned look(const uint32_t* counter) {
+    return __hip_atomic_load(counter, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// --------------------------------------------------------- down and combine --
-// One workgroup 16 outputs, of every expert in turn: its waves take the
-// experts (and the shared one) as strips, whose outputs stay in LDS by (token,
-// slot) pair until all are there and are then added in slot order, shared
-// expert first.  Nothing crosses workgroups, and a token's sum does not depend
-// on the batch it is in.
 template <bool FP8>
-__global__ __launch_bounds__(kThreads) void few_down_kernel(FewArgs p) {
+__global__ __launch_bounds__(kThreads) void few_experts_kernel(FewArgs p) {
     extern __shared__ __align__(16) float out[];     // [P + T][16]
-    __shared__ int expert[kMaxPairs], start[kMaxPairs + 1], pairs[kMaxPairs];
-    __shared__ int ids[kMaxPairs], n_sh;
-    __shared__ float wt[kMaxPairs];
+    __shared__ Table tb;
+    __shared__ int share_sh, chunk_sh;
+    __shared__ unsigned open_sh;
     const Lane l = this_lane();
-    const int P = p.T * p.k, sh = p.Fs > 0 ? 1 : 0;
-    // (one round trip: entries past the number of experts are not used)
-    if (l.tid < P) {
-        expert[l.tid] = p.expert[l.tid];
-        start[l.tid] = p.start[l.tid];
-        pairs[l.tid] = p.pairs[l.tid];
-        ids[l.tid] = p.ids[l.tid];
-        wt[l.tid] = p.w[l.tid];
-    }
+    const int slot_of = blockIdx.x % kSlots;
+    const int shares = gridDim.x, per_slot = shares / kSlots;   // (whole)
+    // thread 0's tickets in hand: a share and, taken ahead, a chunk
+    unsigned share_t = 0, chunk_t = 0;
     if (l.tid == 0) {
-        start[P] = p.start[P];
-        n_sh = *p.n_expert;
+        share_t = take(sync_word(p, kShares, slot_of));
+        chunk_t = take(sync_word(p, kChunks, slot_of));
+        open_sh = 0u;
     }
-    __syncthreads();
-    const int n = n_sh;
-    for (int chunk = blockIdx.x; chunk < p.d / 16; chunk += gridDim.x) {
+    bool opened = false;                             // the shares are done
+    build_table(p, l, tb);
+    const int n = tb.n, P = p.T * p.k, sh = p.Fs > 0 ? 1 : 0;
+    const int per = p.F / 8, strips = n * per, chunks = p.d / 16;
+    bool more_shares = true;
+    for (;;) {
+        if (more_shares && l.wave == 0) {
+            // the slot's next share, or one that another slot has left
+            int share = (int)share_t < per_slot ? slot_of + kSlots * (int)share_t : -1;
+            share = __builtin_amdgcn_readfirstlane(share);
+            while (share < 0) {
+                const unsigned taken =
+                    l.lane < kSlots ? look(sync_word(p, kShares, l.lane)) : ~0u;
+                const uint64_t left = __builtin_amdgcn_ballot_w64((int)min(taken, 0x7fffffffu) <
+                                                                  per_slot);
+                if (!left) break;
+                const int from = __builtin_ctzll(left);
+                unsigned got = 0;
+                if (l.lane == 0) got = take(sync_word(p, kShares, from));
+                got = (unsigned)__builtin_amdgcn_readfirstlane((int)got);
+                if ((int)got < per_slot) share = from + kSlots * (int)got;
+            }
+            if (l.lane == 0) share_sh = share;
+        }
+        if (l.tid == 0) chunk_sh = slot_of + kSlots * (int)min(chunk_t, 1u << 24);
+        __syncthreads();
+        const int share = more_shares ? share_sh : -1, chunk = chunk_sh;
+        more_shares = share >= 0;
+        if (more_shares) {
+            if (l.tid == 0) share_t = take(sync_word(p, kShares, slot_of));
+            // (strips dealt to the shares first, so that few strips use every
+            // CU; finer shares or strips taken one by one balance the CUs
+            // better but end no earlier: memory's rate decides)
+            for (int it = l.wave * shares + share; it < strips; it += 8 * shares) {
+                const int u = it / per, f0 = (it - u * per) * 8;
+                const int e = tb.expert[u], s = tb.start[u], m_all = tb.start[u + 1] - s;
+                // (repeated ids of a hash table can give an expert more rows
+                // than there are tokens: in runs of MOE_FEW_MAX_T)
+                for (int m0 = 0; m0 < m_all; m0 += MOE_FEW_MAX_T) {
+                    const int m = min(m_all - m0, MOE_FEW_MAX_T), ct = (m + 15) / 16;
+                    auto pair = [&](int c) {
+                        return tb.pairs[s + m0 + min(16 * c + l.r16, m - 1)];
+                    };
+                    Strip<FP8, 1> st;
+                    set_gate_up(st, p.w_gate, p.w_up, p.w_gate_scale, p.w_up_scale, e, f0, p.F,
+                                p.d, l);
+                    // lanes 0-31 hold the gate sums of features 4 grp + i,
+                    // lanes 32-63 the up sums of the same ones
+                    st.run([&](int c) { return p.x + (size_t)(pair(c) / p.k) * p.d; }, ct, 0,
+                           [] {}, [&](int c, const f32x4& acc) {
+                               float v[4];
+#pragma unroll
+                               for (int i = 0; i < 4; ++i)
+                                   v[i] = clamped_swiglu(acc[i], __shfl_xor(acc[i], 32, 64),
+                                                         p.clamp_limit, p.clamp_mode);
+                               const uint64_t h = (uint64_t)bf16_pack2(v[0], v[1]) |
+                                                  (uint64_t)bf16_pack2(v[2], v[3]) << 32;
+                               if (l.grp < 2 && 16 * c + l.r16 < m)
+                                   __hip_atomic_store(
+                                       (uint64_t*)(p.h + (size_t)pair(c) * p.F + f0 + 4 * l.grp),
+                                       h, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                           });
+                }
+            }
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wave's stores are there
+            __syncthreads();
+            if (l.tid == 0) take(sync_word(p, kDone, share % kSlots));
+            continue;
+        }
+        if (chunk >= chunks) return;
+        if (l.tid == 0) chunk_t = take(sync_word(p, kChunks, slot_of));
+        // the last wave watches the count for all (through LDS: a wave's own
+        // load would queue behind its weights)
+        auto ready = [&] {
+            if (opened) return;
+            auto is_open = [&] {
+                return __hip_atomic_load(&open_sh, __ATOMIC_RELAXED,
+                                         __HIP_MEMORY_SCOPE_WORKGROUP) != 0u;
+            };
+            if (l.wave == 7 && !is_open()) {
+                // (the limit, seconds, ends the wait when another call has
+                // cleared the counts of this call's workspace meanwhile)
+                int polls = 0;
+                while (__builtin_amdgcn_ballot_w64(
+                           l.lane < kSlots &&
+                           look(sync_word(p, kDone, l.lane)) != (unsigned)per_slot) &&
+                       ++polls < kMaxPolls)
+                    __builtin_amdgcn_s_sleep(1);
+                if (polls == kMaxPolls && l.lane == 0 && p.flags)
+                    atomicOr(p.flags, MOE_FLAG_OVERLAP);
+                // (for the whole workgroup: its waves share the caches that
+                // this invalidates)
+                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                __hip_atomic_store(&open_sh, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+            }
+            while (!is_open()) __builtin_amdgcn_s_sleep(1);
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+            opened = true;
+        };
+        if (l.wave == 7) ready();
         for (int u = l.wave; u < n + sh; u += 8) {
             const bool shared = u >= n;
-            const int s = shared ? 0 : start[u];
-            const int m_all = shared ? p.T : start[u + 1] - s;
+            const int s = shared ? 0 : tb.start[u];
+            const int m_all = shared ? p.T : tb.start[u + 1] - s;
             const int K = shared ? p.Fs : p.F;
-            const size_t mat = shared ? 0 : (size_t)expert[u];
+            const size_t mat = shared ? 0 : (size_t)tb.expert[u];
             Strip<FP8, 1> st;
             st.wrow = (const uint8_t*)(shared ? p.s_down : p.w_down) +
                       (mat * p.d + 16 * chunk + l.r16) * (size_t)K * (FP8 ? 1 : 2);
@@ -507,11 +593,11 @@ __global__ __launch_bounds__(kThreads) void few_down_kernel(FewArgs p) {
                 const int m = min(m_all - m0, MOE_FEW_MAX_T), ct = (m + 15) / 16;
                 auto slot = [&](int c) {
                     const int r = m0 + min(16 * c + l.r16, m - 1);
-                    return shared ? P + r : pairs[s + r];
+                    return shared ? P + r : tb.pairs[s + r];
                 };
                 st.run([&](int c) { return shared ? p.hs + (size_t)(slot(c) - P) * K
                                                   : p.h + (size_t)slot(c) * K; },
-                       ct, 0, [&](int c, const f32x4& acc) {
+                       ct, 0, ready, [&](int c, const f32x4& acc) {
                            if (16 * c + l.r16 < m)
                                *(f32x4*)(out + slot(c) * 16 + 4 * l.grp) = acc;
                        });
@@ -522,15 +608,14 @@ __global__ __launch_bounds__(kThreads) void few_down_kernel(FewArgs p) {
             const int t = i >> 4, o = i & 15;
             float v = sh ? out[(P + t) * 16 + o] : 0.0f;
             for (int j = 0; j < p.k; ++j)
-                if (ids[t * p.k + j] >= 0)
-                    v = __builtin_fmaf(wt[t * p.k + j], out[(t * p.k + j) * 16 + o], v);
+                if (tb.ids[t * p.k + j] >= 0)
+                    v = __builtin_fmaf(tb.w[t * p.k + j], out[(t * p.k + j) * 16 + o], v);
             const size_t at = (size_t)t * p.d + 16 * chunk + o;
             if (p.out_dtype == MOE_OUT_F32)
                 ((float*)p.y)[at] = v;
             else
                 ((uint16_t*)p.y)[at] = f32_to_bf16(v);
         }
-        __syncthreads();
     }
 }
 
@@ -541,12 +626,8 @@ hipError_t launch(const FewArgs& p, hipStream_t stream) {
     hipLaunchKernelGGL(few_router_kernel<FP8>, dim3(grid1), dim3(kThreads), red, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int cus = device_cu_count();
-    hipLaunchKernelGGL(few_gate_up_kernel<FP8>, dim3(cus), dim3(kThreads), 0, stream, p);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(few_down_kernel<FP8>, dim3(p.d / 16 < cus ? p.d / 16 : cus),
-                       dim3(kThreads), (size_t)(p.T * p.k + p.T) * 16 * sizeof(float), stream, p);
+    hipLaunchKernelGGL(few_experts_kernel<FP8>, dim3((device_cu_count() + 7) & ~7), dim3(kThreads),
+                       (size_t)(p.T * p.k + p.T) * 16 * sizeof(float), stream, p);
     return hipGetLastError();
 }
 
