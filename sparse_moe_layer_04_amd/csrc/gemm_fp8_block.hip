@@ -38,18 +38,17 @@
 namespace moe {
 namespace {
 
-constexpr int BM = 128;                    // rows a tile, at most
+constexpr int BM = 160;                    // rows a tile, at most
 constexpr int kSplitM = 128;               // rows a tile of a larger group
 constexpr int BN = 256;                    // weight rows a tile
 constexpr int BK = 128;                    // K a stage: one block
 constexpr int kThreads = 512;
 constexpr int kSlotW = BN * BK;
-constexpr int kSlotS = kSlotW + BM * BK;   // the stage's scales: the rows' (3 x 64
-constexpr int kSlot = kSlotS + 1024;       // words), then two of the weights
+constexpr int kSlotS = kSlotW + BM * BK;   // the stage's scales: BM rows', then two
+constexpr int kSlot = kSlotS + 768;        // of the weights
 constexpr int kRing = 3 * kSlot;
-constexpr int kRowMax = 8 * BM * 4;        // SwiGLU: the waves' row maxima
-constexpr int kTable = 2048;               // offsets kept in LDS
-constexpr int kLds = kRing + kRowMax + kTable * 4;
+constexpr int kMaxX = 8 * BM;              // SwiGLU: the waves' row exponents, a byte each
+constexpr int kLds = kRing + kMaxX;
 static_assert(kLds <= 160 * 1024 && kSlot % 128 == 0, "three slots of LDS");
 
 // Copies from memory into LDS that pass no register: lane l's 16 (4) bytes go
@@ -112,12 +111,12 @@ struct Tile {
 // the tile's or the matrix's end lie past them and fetch nothing).  A wave's
 // copy fills 8 LDS rows of 128 bytes; the place of a chunk in its row is
 // swizzled, so the lanes fetch swizzled chunks.
-constexpr int kCopies = 7;                 // copies a wave and stage: 4 W, 2 A, scales
+constexpr int kCopies = 8;                 // copies a wave and stage: 4 W, 3 A, scales
 constexpr int kEarly = 3;                  // of them, issued in the stage before
 template <int EPI>
 struct Fetch {
     u32x4 wsrc, asrc;
-    int wo[4], ao[2];
+    int wo[4], ao[3];
     const float* sp;
 
     __device__ __forceinline__ void set(const Fp8GemmArgs& p, const Tile& t) {
@@ -137,18 +136,19 @@ struct Fetch {
             const int R = lr + 64 * q;
             wo[q] = (SW ? 16 * (R >> 5) + (R & 15) : R) * K + 16 * c;
         }
+        // (the last 32 rows twice, the same bytes to the same place, so that
+        // every wave issues the same number of copies)
 #pragma unroll
-        for (int q = 0; q < 2; ++q) ao[q] = (lr + 64 * q) * K + 16 * c;
-        // scales: waves 0 to 2 fetch the rows', the others (the same ones) the
-        // weights' of the tile's two 128-blocks of rows, or of gate and up
-        const int nb0 = t.n0 / 128;
-        if (wave < 3) {
-            sp = p.as + (size_t)(t.row0 + min(64 * wave + lane, t.valid - 1)) * S;
-        } else if constexpr (SW) {
-            sp = (lane & 1 ? p.s2 : p.s1) + ((size_t)t.g * nbn + nb0) * S;
-        } else {
-            sp = p.s1 + ((size_t)t.g * nbn + min(nb0 + (lane & 1), nbn - 1)) * S;
-        }
+        for (int q = 0; q < 3; ++q) ao[q] = ((q == 2 ? lr & 31 : lr) + 64 * q) * K + 16 * c;
+        // scales, words of the slot: the rows', at BM those of the tile's two
+        // 128-blocks of weight rows, or of gate and up (waves 2 to 7 the same)
+        const int word = 64 * min(wave, 2) + lane, nb0 = t.n0 / 128;
+        if (word < BM)
+            sp = p.as + (size_t)(t.row0 + min(word, t.valid - 1)) * S;
+        else if constexpr (SW)
+            sp = (word & 1 ? p.s2 : p.s1) + ((size_t)t.g * nbn + nb0) * S;
+        else
+            sp = p.s1 + ((size_t)t.g * nbn + min(nb0 + (word & 1), nbn - 1)) * S;
     }
 
     // Copy q (of kCopies) of stage j into the slot at LDS byte `at`.  Stage 0
@@ -163,11 +163,11 @@ struct Fetch {
         const int back = j == 0 ? past : 0, out = j < S ? 0 : (int)0x80000000;
         if (q < 4)
             copy16(wsrc, (wo[q] - back) | out, b * BK, at + q * 64 * BK + wave * 1024);
-        else if (q < 6)
+        else if (q < 7)
             copy16(asrc, (ao[q - 4] - back) | out, b * BK,
-                   at + kSlotW + (q - 4) * 64 * BK + wave * 1024);
+                   at + kSlotW + (q - 4) * 64 * BK + (q == 6 ? wave & 3 : wave) * 1024);
         else
-            copy4(sp + b, at + kSlotS + min(wave, 3) * 256);
+            copy4(sp + b, at + kSlotS + min(wave, 2) * 256);
     }
     template <int Q0, int Q1>
     __device__ __forceinline__ void copies(int j, int S, int past, int at) const {
@@ -181,6 +181,115 @@ struct Fetch {
         copies<0, kEarly>(2, S, past, 2 * kSlot);
     }
 };
+
+// f(integral_constant<int, I>()) for I in [I0, I1)
+template <int I0, int I1, class F>
+__device__ __forceinline__ void static_for(const F& f) {
+    if constexpr (I0 < I1) {
+        f(std::integral_constant<int, I0>());
+        static_for<I0 + 1, I1>(f);
+    }
+}
+
+// The stages of a tile of five blocks of rows (its registers do not hold two
+// sets of operands): the same steps, taken a product at a time, the operands
+// of a product made ready during the one before, those of W once a step.
+template <int EPI, class Turn, class Scales, class ReadS, class Add>
+__device__ __forceinline__ void run_five(const Fetch<EPI>& f, unsigned char* ring, int rdw, int rda,
+                                         int S, int past, const Turn& turn, const Scales& scales,
+                                         const ReadS& read_s, const Add& add_part,
+                                         f32x16 (&part)[5][1]) {
+    constexpr int MI = 5;
+    f32x16 zero;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) zero[e] = 0.0f;
+    int slot = 0;
+    auto read = [&](int at, int q, int i) {
+        return *(const u32x4*)(ring + (at ^ (q << 5)) + i * 32 * BK);
+    };
+    if constexpr (EPI != FP8_OUT_BF16) {
+        // product L = 5 h + i: step h (16 of K), block i.  ra[i] holds 32 of K,
+        // read again as soon as its second half is decoded
+        u32x4 rw[2], ra[MI];
+        bf16x8 w[2], a[2];
+        auto half = [](const u32x4& v, int h) {
+            return h ? fp8x8_to_bf16x8(u32x2{v[2], v[3]}, 1.0f)
+                     : fp8x8_to_bf16x8(u32x2{v[0], v[1]}, 1.0f);
+        };
+        rw[0] = read(rdw, 0, 0);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) ra[i] = read(rda, 0, i);
+        w[0] = half(rw[0], 0);
+        a[0] = half(ra[0], 0);
+        for (int j = 0; j < S; ++j) {
+            const int next = slot == 2 * kSlot ? 0 : slot + kSlot;
+            const int last = next == 2 * kSlot ? 0 : next + kSlot;
+            scales();                               // of block j - 1
+            read_s(slot);
+            static_for<0, 8 * MI>([&](auto index) {
+                constexpr int L = decltype(index)::value, h = L / MI, i = L % MI;
+                constexpr int L2 = (L + 1) % (8 * MI), h2 = L2 / MI, i2 = L2 % MI;
+                if constexpr (L == 6 * MI - 1) turn();
+                if constexpr (i == 0 && h < 5)
+                    f.template copies<kEarly + h, kEarly + h + 1>(j + 2, S, past, last);
+                if constexpr (i == 1 && h >= 6)
+                    f.template copies<h - 6, h == 7 ? kEarly : 1>(j + 3, S, past, slot);
+                // W of the next 32 of K
+                if constexpr (i == 0 && h % 2 == 0)
+                    rw[h / 2 + 1 & 1] = h == 6 ? read(rdw + next, 0, 0) : read(rdw + slot, h / 2 + 1, 0);
+                // the next product's operands
+                a[L2 & 1] = half(ra[i2], h2 & 1);
+                if constexpr (i2 == 0) w[h2 & 1] = half(rw[h2 / 2 & 1], h2 & 1);
+                if constexpr (h2 & 1)
+                    ra[i2] = h2 == 7 ? read(rda + next, 0, i2) : read(rda + slot, h2 / 2 + 1, i2);
+                if constexpr (h == 0) add_part(i, 0);
+                part[i][0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    w[h & 1], a[L & 1], h == 0 ? zero : part[i][0], 0, 0, 0);
+                if constexpr (i == MI - 1) __builtin_amdgcn_sched_barrier(0);
+            });
+            slot = next;
+        }
+    } else {
+        // product L = 5 s + i: half s of the block, rows' operands two ahead
+        u32x4 rw[2][2], ra[2][2];
+        auto read2 = [&](u32x4 (&r)[2], int at, int s, int i) {
+            r[0] = read(at, 2 * s, i);
+            r[1] = read(at, 2 * s + 1, i);
+        };
+        auto cat = [](const u32x4 (&r)[2]) {
+            return v8i{(int)r[0][0], (int)r[0][1], (int)r[0][2], (int)r[0][3],
+                       (int)r[1][0], (int)r[1][1], (int)r[1][2], (int)r[1][3]};
+        };
+        read2(rw[0], rdw, 0, 0);
+        read2(ra[0], rda, 0, 0);
+        read2(ra[1], rda, 0, 1);
+        for (int j = 0; j < S; ++j) {
+            const int next = slot == 2 * kSlot ? 0 : slot + kSlot;
+            const int last = next == 2 * kSlot ? 0 : next + kSlot;
+            scales();                               // of block j - 1
+            read_s(slot);
+            read2(rw[1], rdw + slot, 1, 0);
+            static_for<0, 2 * MI>([&](auto index) {
+                constexpr int L = decltype(index)::value, s = L / MI, i = L % MI;
+                constexpr int L2 = (L + 2) % (2 * MI);
+                if constexpr (s == 0) add_part(i, 0);
+                part[i][0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    cat(rw[s]), cat(ra[L & 1]), s == 0 ? zero : part[i][0], 0, 0, 0, 127, 0, 127);
+                if constexpr (L < kCopies - kEarly)
+                    f.template copies<kEarly + L, kEarly + L + 1>(j + 2, S, past, last);
+                if constexpr (L == 2 * MI - 3) {
+                    turn();
+                    read2(rw[0], rdw + next, 0, 0);
+                }
+                read2(ra[L & 1], rda + (L2 < 2 ? next : slot), L2 / MI, L2 % MI);
+                if constexpr (L >= 2 * MI - 3)
+                    f.template copies<L - (2 * MI - 3), L - (2 * MI - 3) + 1>(j + 3, S, past, slot);
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            slot = next;
+        }
+    }
+}
 
 // One tile, whose first three stages are on their way into the ring; sends the
 // next tile's (if there are more) off before this one's results are written.
@@ -210,7 +319,7 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t, co
     const int rdw = wn * NJ * 32 * BK + rd0;
     const int rda = kSlotW + wm * MI * 32 * BK + rd0;
     const int rds = kSlotS + (wm * MI * 32 + l32) * 4;
-    const int rdsw = kSlotS + 768 + (SW ? 0 : wn * NJ * 32 / 128) * 4;
+    const int rdsw = kSlotS + BM * 4 + (SW ? 0 : wn * NJ * 32 / 128) * 4;
     float sa[MI] = {}, sw1 = 0.0f, sw2 = 0.0f;
     auto read_s = [&](int slot) {
 #pragma unroll
@@ -265,20 +374,24 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t, co
     if (past) {
         const u32x4 z = {0u, 0u, 0u, 0u};
 #pragma unroll
-        for (int q = 0; q < (BN + BM) / 64; ++q) *(u32x4*)(ring + q * 64 * BK + tid * 16) = z;
+        for (int q = 0; q < (BN + BM + 63) / 64; ++q)
+            *(u32x4*)(ring + q * 64 * BK + (q == (BN + BM) / 64 ? tid & 255 : tid) * 16) = z;
     }
     __syncthreads();
     // The middle of stage j: stage j + 1's block has landed and every wave has
     // read stage j's, whose slot takes stage j + 3's.  The copies are spread
-    // over the steps, one at a time (7 at once hold every wave until the memory
-    // pipeline has taken 48 KB): the first after this barrier, the rest in the
+    // over the steps, one at a time (all at once hold every wave until the
+    // memory pipeline has taken 48 KB): the first after this barrier, the rest in the
     // next stage's steps before its own.
     auto turn = [&]() {
         wait_vm<kCopies>();
         __syncthreads();
     };
 
-    if constexpr (EXACT) {
+    using std::integral_constant;
+    if constexpr (MB == 5) {
+        run_five<EPI>(f, ring, rdw, rda, S, past, turn, scales, read_s, add_part, part);
+    } else if constexpr (EXACT) {
         u32x4 rw[2][NJ], ra[2][MI];        // 32 of K: the codes of two steps
         bf16x8 w[2][NJ], a[2][MI];         // operands of a step
         auto read = [&](int slot, int q, auto set) {
@@ -311,7 +424,6 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t, co
                         w[h & 1][n], a[h & 1][i], h == 0 ? zero : part[i][n], 0, 0, 0);
                 }
         };
-        using std::integral_constant;
         auto step = [&](auto st) {
             constexpr int h = decltype(st)::value;
             decode(integral_constant<int, (h + 1) & 7>());
@@ -347,6 +459,7 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t, co
             read(slot, 3, H1());
             f.template copies<6, 7>(j + 2, S, past, last);
             step(integral_constant<int, 3>());
+            f.template copies<7, 8>(j + 2, S, past, last);
             step(integral_constant<int, 4>());
             turn();
             read(next, 0, H0());                    // (past the end: not used)
@@ -410,13 +523,14 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t, co
             read_s(slot);
             read(slot, B1());
             multiply(B0(), [&](auto q) {
-                f.template copies<3 + decltype(q)::value, 4 + decltype(q)::value>(j + 2, S, past, last);
+                constexpr int c = kEarly + decltype(q)::value;
+                f.template copies<c, c == 6 ? kCopies : c + 1>(j + 2, S, past, last);
             });
             turn();
             read(next, B0());                       // (past the end: not used)
             multiply(B1(), [&](auto q) {
-                if constexpr (decltype(q)::value < kEarly)
-                    f.template copies<decltype(q)::value, decltype(q)::value + 1>(j + 3, S, past, slot);
+                constexpr int c = decltype(q)::value;
+                if constexpr (c < kEarly) f.template copies<c, c + 1>(j + 3, S, past, slot);
             });
             slot = next;
         }
@@ -472,10 +586,11 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t, co
                 }
         }
     } else {
-        // h = SwiGLU in fp32, quantised along the tile's 128 features: the
-        // row maximum over this lane's features, its half-wave partner's and
-        // the other waves'
-        float* rm = (float*)(ring + kRing);           // [WN][BM]
+        // h = SwiGLU in fp32, quantised along the tile's 128 features.  The
+        // exponent of a row's scale is the largest of its parts' exponents:
+        // this lane's and its half-wave partner's features, the other waves'
+        // (a byte each; the lowest where a part is all zeros)
+        int8_t* xs = (int8_t*)(ring + kRing);         // [WN][BM]
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
             float m = 0.0f;
@@ -491,17 +606,18 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t, co
                 }
             }
             m = fmaxf(m, __shfl_xor(m, 32, 64));
-            if (half == 0) rm[wn * BM + (wm * MI + i) * 32 + l32] = m;
+            if (half == 0)
+                xs[wn * BM + (wm * MI + i) * 32 + l32] = m > 0.0f ? block_exponent(m) : -128;
         }
         __syncthreads();
         const int nbf = (N + 127) / 128;
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
             const int r = (wm * MI + i) * 32 + l32;
-            float m = 0.0f;
+            int X = -128;
 #pragma unroll
-            for (int w = 0; w < WN; ++w) m = fmaxf(m, rm[w * BM + r]);
-            const int X = block_exponent(m);
+            for (int w = 0; w < WN; ++w) X = max(X, (int)xs[w * BM + r]);
+            X = X == -128 ? 0 : X;
             const float inv = pow2(-X);
             uint8_t* o = (uint8_t*)p.out + (size_t)(t.row0 + r) * N + t.n0;
 #pragma unroll
@@ -516,6 +632,17 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t, co
                 p.out_scale[(size_t)(t.row0 + r) * nbf + t.n0 / 128] = pow2(X);
         }
     }
+}
+
+// *p for a wave-uniform p
+__device__ __forceinline__ int scalar_load(const int32_t* p) {
+    const uint64_t a = (uint64_t)(uintptr_t)p;
+    const uint64_t u = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a) |
+                       (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32))
+                           << 32;
+    int v;
+    asm volatile("s_load_dword %0, %1, 0x0\n\ts_waitcnt lgkmcnt(0)" : "=s"(v) : "s"(u));
+    return v;
 }
 
 // Inclusive sum over the wave's lanes
@@ -549,22 +676,10 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_block_kernel(Fp8GemmArgs p)
     const int tid = threadIdx.x, lane = tid & 63;
     const int G = p.G, rows = p.rows, S = (p.K + BK - 1) / BK;
     const int NT = (p.N + TN - 1) / TN;
-    // the groups' offsets, clamped into [0, rows], in LDS where they fit (a
-    // load from memory would wait for the copies before it)
-    int* table = (int*)(smem + kRing + kRowMax);
-    const bool tabled = G < kTable;
-    auto clamped = [&](int g) { return min(max(p.offsets[g], 0), rows); };
-    if (tabled)
-        for (int g = tid; g <= G; g += kThreads) table[g] = clamped(g);
-    __syncthreads();
-    auto group_rows = [&](int g, int& lo, int& hi) {
-        lo = tabled ? table[g] : clamped(g);
-        hi = max(lo, tabled ? table[g + 1] : clamped(g + 1));
-    };
+    auto clamped = [&](int v) { return min(max(v, 0), rows); };
     auto group_items = [&](int g) {
-        int lo = 0, hi = 0;
-        if (g < G) group_rows(g, lo, hi);
-        return NT * row_tiles(hi - lo);
+        if (g >= G) return 0;
+        return NT * row_tiles(clamped(p.offsets[g + 1]) - clamped(p.offsets[g]));
     };
     const int run = (G + 63) / 64;
     int mine = 0;
@@ -574,23 +689,25 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_block_kernel(Fp8GemmArgs p)
     const int xcd = blockIdx.x & 7, step = gridDim.x >> 3;
     const int end = (int)(Q * (xcd + 1) / 8);
     auto find = [&](int q, Tile& t) {
-        // the first lane whose sum passes q, then the same within its run
+        // the first lane whose sum passes q, then the groups of its run in
+        // turn (scalar loads: a vector load would wait for the copies that are
+        // on their way)
         const int r = __builtin_ctzll(__builtin_amdgcn_ballot_w64(upto > q));
         int local = q - __builtin_amdgcn_readlane(upto - mine, r);
-        const int items = lane < run ? group_items(r * run + lane) : 0;
-        const int in_run = wave_scan(items, lane);
-        const int l = __builtin_ctzll(__builtin_amdgcn_ballot_w64(in_run > local));
-        local -= __builtin_amdgcn_readlane(in_run - items, l);
-        t.g = r * run + l;
-        int r0, r1;
-        group_rows(t.g, r0, r1);
-        r0 = __builtin_amdgcn_readfirstlane(r0);
-        r1 = __builtin_amdgcn_readfirstlane(r1);
-        const int n = r1 - r0, mt = row_tiles(n);
+        t.g = r * run;
+        int r0 = clamped(scalar_load(p.offsets + t.g)), n, mt;
+        for (;; ++t.g) {                             // (ends: the run holds item q)
+            const int r1 = clamped(scalar_load(p.offsets + t.g + 1));
+            n = max(r1 - r0, 0);
+            mt = row_tiles(n);
+            if (local < NT * mt || t.g + 1 >= G) break;
+            local -= NT * mt;
+            r0 = r1;
+        }
         const int per = ((n + mt - 1) / mt + 31) & ~31;
         t.n0 = local / mt * TN;
         t.row0 = r0 + local % mt * per;
-        t.valid = min(per, r1 - t.row0);
+        t.valid = min(per, r0 + n - t.row0);
     };
     // bytes that this thread's chunk of K's last block reaches past K
     const int past = max(0, (S - 1) * BK + 16 * ((tid & 7) ^ swz(tid >> 3)) + 16 - p.K);
@@ -611,7 +728,8 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_block_kernel(Fp8GemmArgs p)
             case 1: run_tile<EPI, 1>(p, t, next, more, past, smem); break;
             case 2: run_tile<EPI, 2>(p, t, next, more, past, smem); break;
             case 3: run_tile<EPI, 3>(p, t, next, more, past, smem); break;
-            default: run_tile<EPI, 4>(p, t, next, more, past, smem); break;
+            case 4: run_tile<EPI, 4>(p, t, next, more, past, smem); break;
+            default: run_tile<EPI, 5>(p, t, next, more, past, smem); break;
         }
         if (!more) break;
         t = next;
