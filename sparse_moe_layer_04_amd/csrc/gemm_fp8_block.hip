@@ -58,6 +58,7 @@ static_assert(kLds <= 160 * 1024 && kSlot % 128 == 0, "three slots of LDS");
 // compiler does not count these copies: wait_vm does.
 __device__ __forceinline__ void copy16(u32x4 rsrc, int voffset, int soffset, int lds) {
     const int at = __builtin_amdgcn_readfirstlane(lds);
+    soffset = __builtin_amdgcn_readfirstlane(soffset);
     int saved;
     asm volatile(
         "s_mov_b32 %0, m0\n\t"
@@ -111,7 +112,8 @@ struct Tile {
 // the tile's or the matrix's end lie past them and fetch nothing).  A wave's
 // copy fills 8 LDS rows of 128 bytes; the place of a chunk in its row is
 // swizzled, so the lanes fetch swizzled chunks.
-constexpr int kCopies = 8;                 // copies a wave and stage: 4 W, 3 A, scales
+// copies a wave and stage: 4 of W, one for each 64 rows of A, the scales
+constexpr int row_copies(int blocks) { return (blocks + 1) / 2; }
 constexpr int kEarly = 3;                  // of them, issued in the stage before
 template <int EPI>
 struct Fetch {
@@ -151,34 +153,41 @@ struct Fetch {
             sp = p.s1 + ((size_t)t.g * nbn + min(nb0 + (word & 1), nbn - 1)) * S;
     }
 
-    // Copy q (of kCopies) of stage j into the slot at LDS byte `at`.  Stage 0
+    // Copy q (of 4 + NA + 1) of stage j into the slot at LDS byte `at`.  Stage 0
     // takes K's last block, the short one if any, stage j block j - 1.  (Every
     // stage issues its copies: past the last stage with offsets past the
     // resources.)  `past`: the bytes that this thread's chunk reaches past K in
     // the last block; it fetches the row's last chunk instead, which is
     // overwritten by zeros when it has landed.
+    template <int NA>
     __device__ __forceinline__ void copy(int q, int j, int S, int past, int at) const {
         const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
         const int b = j == 0 ? S - 1 : min(j, S) - 1;
         const int back = j == 0 ? past : 0, out = j < S ? 0 : (int)0x80000000;
         if (q < 4)
             copy16(wsrc, (wo[q] - back) | out, b * BK, at + q * 64 * BK + wave * 1024);
-        else if (q < 7)
+        else if (q < 4 + NA)
             copy16(asrc, (ao[q - 4] - back) | out, b * BK,
                    at + kSlotW + (q - 4) * 64 * BK + (q == 6 ? wave & 3 : wave) * 1024);
         else
             copy4(sp + b, at + kSlotS + min(wave, 2) * 256);
     }
-    template <int Q0, int Q1>
+    template <int NA, int Q0, int Q1>
     __device__ __forceinline__ void copies(int j, int S, int past, int at) const {
 #pragma unroll
-        for (int q = Q0; q < Q1; ++q) copy(q, j, S, past, at);
+        for (int q = Q0; q < Q1 && q < 4 + NA + 1; ++q) copy<NA>(q, j, S, past, at);
     }
-    // what is on its way when a tile begins
-    __device__ __forceinline__ void first_stages(int S, int past) const {
-        copies<0, kCopies>(0, S, past, 0);
-        copies<0, kCopies>(1, S, past, kSlot);
-        copies<0, kEarly>(2, S, past, 2 * kSlot);
+    // what is on its way when a tile (of NA row copies) begins
+    template <int NA>
+    __device__ __forceinline__ void first(int S, int past) const {
+        copies<NA, 0, 8>(0, S, past, 0);
+        copies<NA, 0, 8>(1, S, past, kSlot);
+        copies<NA, 0, kEarly>(2, S, past, 2 * kSlot);
+    }
+    __device__ __forceinline__ void first_stages(int valid, int S, int past) const {
+        if (valid <= 64) first<1>(S, past);
+        else if (valid <= 128) first<2>(S, past);
+        else first<3>(S, past);
     }
 };
 
@@ -231,9 +240,9 @@ __device__ __forceinline__ void run_five(const Fetch<EPI>& f, unsigned char* rin
                 constexpr int L2 = (L + 1) % (8 * MI), h2 = L2 / MI, i2 = L2 % MI;
                 if constexpr (L == 6 * MI - 1) turn();
                 if constexpr (i == 0 && h < 5)
-                    f.template copies<kEarly + h, kEarly + h + 1>(j + 2, S, past, last);
+                    f.template copies<3, kEarly + h, kEarly + h + 1>(j + 2, S, past, last);
                 if constexpr (i == 1 && h >= 6)
-                    f.template copies<h - 6, h == 7 ? kEarly : 1>(j + 3, S, past, slot);
+                    f.template copies<3, h - 6, h == 7 ? kEarly : 1>(j + 3, S, past, slot);
                 // W of the next 32 of K
                 if constexpr (i == 0 && h % 2 == 0)
                     rw[h / 2 + 1 & 1] = h == 6 ? read(rdw + next, 0, 0) : read(rdw + slot, h / 2 + 1, 0);
@@ -275,15 +284,15 @@ __device__ __forceinline__ void run_five(const Fetch<EPI>& f, unsigned char* rin
                 if constexpr (s == 0) add_part(i, 0);
                 part[i][0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
                     cat(rw[s]), cat(ra[L & 1]), s == 0 ? zero : part[i][0], 0, 0, 0, 127, 0, 127);
-                if constexpr (L < kCopies - kEarly)
-                    f.template copies<kEarly + L, kEarly + L + 1>(j + 2, S, past, last);
+                if constexpr (kEarly + L < 8)
+                    f.template copies<3, kEarly + L, kEarly + L + 1>(j + 2, S, past, last);
                 if constexpr (L == 2 * MI - 3) {
                     turn();
                     read2(rw[0], rdw + next, 0, 0);
                 }
                 read2(ra[L & 1], rda + (L2 < 2 ? next : slot), L2 / MI, L2 % MI);
                 if constexpr (L >= 2 * MI - 3)
-                    f.template copies<L - (2 * MI - 3), L - (2 * MI - 3) + 1>(j + 3, S, past, slot);
+                    f.template copies<3, L - (2 * MI - 3), L - (2 * MI - 3) + 1>(j + 3, S, past, slot);
                 __builtin_amdgcn_sched_barrier(0);
             });
             slot = next;
@@ -309,6 +318,7 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t, co
     constexpr int WM = MB == 4 ? 2 : 1, WN = 8 / WM, MI = MB / WM, NJ = 8 / WN;
     constexpr bool SW = EPI == FP8_SWIGLU;
     constexpr bool EXACT = EPI != FP8_OUT_BF16;
+    constexpr int NA = row_copies(MB), kCopies = 4 + NA + 1;
     const int wm = wave / WN, wn = wave % WN;
     const int K = p.K, N = p.N;
     const int S = (K + BK - 1) / BK;
@@ -449,26 +459,26 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t, co
             const int last = next == 2 * kSlot ? 0 : next + kSlot;
             scales();                               // of block j - 1
             read_s(slot);
-            f.template copies<3, 4>(j + 2, S, past, last);
+            f.template copies<NA, 3, 4>(j + 2, S, past, last);
             step(H0());
             read(slot, 2, H0());
-            f.template copies<4, 5>(j + 2, S, past, last);
+            f.template copies<NA, 4, 5>(j + 2, S, past, last);
             step(H1());
-            f.template copies<5, 6>(j + 2, S, past, last);
+            f.template copies<NA, 5, 6>(j + 2, S, past, last);
             step(integral_constant<int, 2>());
             read(slot, 3, H1());
-            f.template copies<6, 7>(j + 2, S, past, last);
+            f.template copies<NA, 6, 7>(j + 2, S, past, last);
             step(integral_constant<int, 3>());
-            f.template copies<7, 8>(j + 2, S, past, last);
+            f.template copies<NA, 7, 8>(j + 2, S, past, last);
             step(integral_constant<int, 4>());
             turn();
             read(next, 0, H0());                    // (past the end: not used)
-            f.template copies<0, 1>(j + 3, S, past, slot);
+            f.template copies<NA, 0, 1>(j + 3, S, past, slot);
             step(integral_constant<int, 5>());
-            f.template copies<1, 2>(j + 3, S, past, slot);
+            f.template copies<NA, 1, 2>(j + 3, S, past, slot);
             step(integral_constant<int, 6>());
             read(next, 1, H1());
-            f.template copies<2, 3>(j + 3, S, past, slot);
+            f.template copies<NA, 2, 3>(j + 3, S, past, slot);
             step(integral_constant<int, 7>());
             slot = next;
         }
@@ -524,13 +534,13 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t, co
             read(slot, B1());
             multiply(B0(), [&](auto q) {
                 constexpr int c = kEarly + decltype(q)::value;
-                f.template copies<c, c == 6 ? kCopies : c + 1>(j + 2, S, past, last);
+                f.template copies<NA, c, c == 6 ? kCopies : c + 1>(j + 2, S, past, last);
             });
             turn();
             read(next, B0());                       // (past the end: not used)
             multiply(B1(), [&](auto q) {
                 constexpr int c = decltype(q)::value;
-                if constexpr (c < kEarly) f.template copies<c, c + 1>(j + 3, S, past, slot);
+                if constexpr (c < kEarly) f.template copies<NA, c, c + 1>(j + 3, S, past, slot);
             });
             slot = next;
         }
@@ -539,7 +549,7 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t, co
     if (more) {
         Fetch<EPI> nf;
         nf.set(p, next_t);
-        nf.first_stages(S, past);
+        nf.first_stages(next_t.valid, S, past);
     }
     scales();
 #pragma unroll
@@ -718,7 +728,7 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_block_kernel(Fp8GemmArgs p)
     {
         Fetch<EPI> f;
         f.set(p, t);
-        f.first_stages(S, past);
+        f.first_stages(t.valid, S, past);
     }
     for (;;) {
         const bool more = q + step < end;
