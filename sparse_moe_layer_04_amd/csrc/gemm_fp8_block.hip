@@ -665,10 +665,15 @@ __device__ __forceinline__ int wave_scan(int x, int lane) {
     return x;
 }
 
-// Row tiles of a group of n rows: one up to BM rows (a second one would fetch
-// the group's weights again), else of up to kSplitM rows each.
-__device__ __forceinline__ int row_tiles(int n) {
-    return n <= BM ? n > 0 : (n + kSplitM - 1) / kSplitM;
+// Row tiles of a group of n rows.  A tile has up to `blocks` blocks of 32
+// rows.  With 5, the most, a group of up to 160 rows is one tile (a second one
+// would fetch the group's weights again), a larger one has tiles of up to
+// kSplitM rows.  1 to 3 are for few tiles (n < 2^15).
+constexpr int kTallest = BM / 32;
+__device__ __forceinline__ int row_tiles(int n, int blocks) {
+    const int c = (n + 31) >> 5;
+    if (blocks == kTallest) return c <= kTallest ? c > 0 : (c + kSplitM / 32 - 1) / (kSplitM / 32);
+    return blocks == 1 ? c : blocks == 2 ? (c + 1) >> 1 : (c + 2) * 21846 >> 16;  // (c + 2) / 3
 }
 
 // Persistent grid, one workgroup a CU.  Items are (group, n-tile, m-tile), the
@@ -687,14 +692,29 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_block_kernel(Fp8GemmArgs p)
     const int G = p.G, rows = p.rows, S = (p.K + BK - 1) / BK;
     const int NT = (p.N + TN - 1) / TN;
     auto clamped = [&](int v) { return min(max(v, 0), rows); };
-    auto group_items = [&](int g) {
-        if (g >= G) return 0;
-        return NT * row_tiles(clamped(p.offsets[g + 1]) - clamped(p.offsets[g]));
-    };
     const int run = (G + 63) / 64;
-    int mine = 0;
-    for (int i = 0; i < run; ++i) mine += group_items(lane * run + i);
-    const int upto = wave_scan(mine, lane);
+    auto tiles_of_my_run = [&](int blocks) {
+        int sum = 0;
+        for (int i = 0; i < run; ++i) {
+            const int g = lane * run + i;
+            if (g < G)
+                sum += row_tiles(max(clamped(p.offsets[g + 1]) - clamped(p.offsets[g]), 0), blocks);
+        }
+        return NT * sum;
+    };
+    int blocks = kTallest, mine = tiles_of_my_run(blocks), upto = wave_scan(mine, lane);
+    // few tiles: the lowest of which every one still has a CU of its own
+    if ((long long)rows * NT <= 96ll * gridDim.x &&
+        __builtin_amdgcn_readlane(upto, 63) < (int)gridDim.x) {
+        for (int b = 1; b <= 3; ++b) {
+            const int lower = tiles_of_my_run(b), sum = wave_scan(lower, lane);
+            if (__builtin_amdgcn_readlane(sum, 63) > (int)gridDim.x) continue;
+            blocks = b;
+            mine = lower;
+            upto = sum;
+            break;
+        }
+    }
     const long long Q = __builtin_amdgcn_readlane(upto, 63);
     const int xcd = blockIdx.x & 7, step = gridDim.x >> 3;
     const int end = (int)(Q * (xcd + 1) / 8);
@@ -709,7 +729,7 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_block_kernel(Fp8GemmArgs p)
         for (;; ++t.g) {                             // (ends: the run holds item q)
             const int r1 = clamped(scalar_load(p.offsets + t.g + 1));
             n = max(r1 - r0, 0);
-            mt = row_tiles(n);
+            mt = row_tiles(n, blocks);
             if (local < NT * mt || t.g + 1 >= G) break;
             local -= NT * mt;
             r0 = r1;

@@ -217,6 +217,20 @@ def test_grouped_gemm(counts, K, N, out):
     assert torch.equal(again[:offs[-1]], got[:offs[-1]])
 
 
+# Row tiles are as low as leaves every one a CU of its own.  With 10 weight
+# tiles the first list fits 256 CUs at 32 rows a tile, the second at 64, the
+# third at 96 and the last at none: there are tiles of every number of 32-row
+# blocks, and groups of one tile and of several.
+HEIGHTS = [[32] * 25, [64] * 17 + [33], [96] * 17 + [65, 1],
+           [1, 32, 33, 64, 65, 96, 97, 128, 129, 160, 161, 0, 256, 257, 300, 321] * 2]
+
+
+@pytest.mark.parametrize("out", [ops.OUT_F32, ops.OUT_BF16])
+@pytest.mark.parametrize("counts", HEIGHTS)
+def test_grouped_gemm_tile_heights(counts, out):
+    test_grouped_gemm(counts, 272, 2320, out)
+
+
 def test_grouped_gemm_codes_as_float8():
     a, sa, od, offs, w, sw = operands(2, [9, 40], 256, 128, 5)
     f8 = torch.float8_e4m3fn
@@ -336,6 +350,11 @@ def test_expert_ffn(counts, d, F, mode, lim, out):
         differ += int((got != codes)[same & ((got | codes) != 0x80)].sum())
         total += got.size
     assert differ <= max(2, 4e-3 * total), (differ, total)
+
+
+@pytest.mark.parametrize("counts", HEIGHTS)
+def test_expert_ffn_tile_heights(counts):
+    test_expert_ffn(counts, 144, 1168, 0, 10.0, ops.OUT_BF16)
 
 
 def test_expert_ffn_rows_outside_groups_untouched():
