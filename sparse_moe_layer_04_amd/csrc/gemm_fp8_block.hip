@@ -21,16 +21,31 @@
 // the loss, and of the second the codes of small values would move by
 // several steps (E4M3 goes down to 2^-18 of a block's largest value).
 //
-// Tile: up to 128 rows x 256 weight rows (SwiGLU: 128 features, gate and up
-// rows interleaved by 16 so that a wave holds both of a feature), 8 waves,
-// one 128-wide block of K a stage.  Both operands go through a 3-slot LDS
-// ring as codes (48 KB a stage): a wave's 64 lanes load 8 rows x 128 bytes
-// (whole lines of the row-major operands) into registers a stage before they
-// go to LDS, which is two stages before they are multiplied, so that the
-// operand reads can run one step ahead of the matrix products all the way
-// through; one barrier a stage.
-// LDS row r holds its 16-byte chunk c at c ^ ((r >> 1) & 7), so that the
-// lanes of an operand read (32 rows, one chunk index) spread over the banks.
+// Tile: up to 160 rows x 256 weight rows (SwiGLU: 128 features, gate and up
+// rows interleaved by 16 so that a wave holds both of a feature), 8 waves of
+// 64 x 64 or (rows of the tile) x 32 outputs in registers, one 128-wide block
+// of K a stage.  256 weight rows, since each CU moves the codes of both
+// operands once a tile: at 128 x 256 that is 85 products a byte.  160 rows,
+// since the weights of a group of 129 to 160 rows are otherwise fetched twice
+// (384 groups of 128 rows on average x 4096 x 2048, tiles of up to 128 rows
+// against 160: 1193 and 1036 us with fp32, 839 and 736 with bf16 output).
+//
+// Both operands go to LDS as codes, by copies that pass no register, through
+// a ring of 3 slots of 52.75 KB: a block's copies are issued two stages before
+// they are multiplied, so that operand reads run ahead of the matrix products
+// across the end of a stage; one barrier a stage.  (Through registers, a block
+// less in flight: 384 groups x 128 rows x 4096 x 2048 with bf16 output took
+// 1117 us, with the copies 853.)  A wave's copy covers 8 rows x 128 bytes (whole lines of the row-major operands); LDS row r holds its
+// 16-byte chunk c at c ^ ((r >> 1) & 7), so that the lanes of an operand read
+// (32 rows, one chunk index) spread over the banks.
+//
+// Bound and measured, 1 group x 8192 rows x 4096 x 2048: the matrix cores, at
+// 1038 TFLOP/s with fp32 output (bf16 cores) and 1748 with bf16 output (8-bit
+// cores; where a large library product of the same types reaches 1395 and
+// 2684): the vector units decode and scale beside them, and the clock drops
+// under both.  384 groups x 128 rows x 4096 x 2048: 3.2 GB of weights, 736 us
+// with bf16 output (memory, 4.9 TB/s), 1036 with fp32 (cores and memory in
+// turn).  Ten rows a group: memory, 5.5 TB/s.
 #include <type_traits>
 
 #include "fp8_block.h"
@@ -668,7 +683,10 @@ __device__ __forceinline__ int wave_scan(int x, int lane) {
 // Row tiles of a group of n rows.  A tile has up to `blocks` blocks of 32
 // rows.  With 5, the most, a group of up to 160 rows is one tile (a second one
 // would fetch the group's weights again), a larger one has tiles of up to
-// kSplitM rows.  1 to 3 are for few tiles (n < 2^15).
+// kSplitM rows.  1 to 3 are for few tiles (n < 2^15), where CUs would have
+// none: lower ones use more CUs, and the weights they share come from the L2.
+// 16 groups x 160 rows x 4096 x 256: 64 us with one tile a group, 27 with five
+// (fp32 output; bf16 35 and 18).
 constexpr int kTallest = BM / 32;
 __device__ __forceinline__ int row_tiles(int n, int blocks) {
     const int c = (n + 31) >> 5;
