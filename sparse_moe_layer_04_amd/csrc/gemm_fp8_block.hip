@@ -35,15 +35,18 @@
 // they are multiplied, so that operand reads run ahead of the matrix products
 // across the end of a stage; one barrier a stage.  (Through registers, a block
 // less in flight: 384 groups x 128 rows x 4096 x 2048 with bf16 output took
-// 1117 us, with the copies 853.)  A wave's copy covers 8 rows x 128 bytes (whole lines of the row-major operands); LDS row r holds its
-// 16-byte chunk c at c ^ ((r >> 1) & 7), so that the lanes of an operand read
-// (32 rows, one chunk index) spread over the banks.
+// 1117 us, with the copies 853.)  A wave's copy covers 8 rows x 128 bytes
+// (whole lines of the row-major operands); LDS row r holds its 16-byte chunk c
+// at c ^ ((r >> 1) & 7), so that the lanes of an operand read (32 rows, one
+// chunk index) spread over the banks.
 //
 // Bound and measured, 1 group x 8192 rows x 4096 x 2048: the matrix cores, at
-// 1038 TFLOP/s with fp32 output (bf16 cores) and 1748 with bf16 output (8-bit
-// cores; where a large library product of the same types reaches 1395 and
-// 2684): the vector units decode and scale beside them, and the clock drops
-// under both.  384 groups x 128 rows x 4096 x 2048: 3.2 GB of weights, 736 us
+// 1100 to 1136 TFLOP/s with fp32 output (bf16 cores) and 1780 to 1895 with
+// bf16 output (8-bit cores; where a large library product of the same types
+// reaches 1395 and 2684).  With neither decoding nor scaling the same loop
+// reaches 1379 (100 us; decoding adds 16, scaling 5 to 10) and, without the
+// scaling, 2160 (64 us; scaling adds 9): the vector units run beside the
+// matrix cores, and the clock drops under both.  384 groups x 128 rows x 4096 x 2048: 3.2 GB of weights, 736 us
 // with bf16 output (memory, 4.9 TB/s), 1036 with fp32 (cores and memory in
 // turn).  Ten rows a group: memory, 5.5 TB/s.
 #include <type_traits>
@@ -54,7 +57,6 @@ namespace moe {
 namespace {
 
 constexpr int BM = 160;                    // rows a tile, at most
-constexpr int kSplitM = 128;               // rows a tile of a larger group
 constexpr int BN = 256;                    // weight rows a tile
 constexpr int BK = 128;                    // K a stage: one block
 constexpr int kThreads = 512;
@@ -680,26 +682,31 @@ __device__ __forceinline__ int wave_scan(int x, int lane) {
     return x;
 }
 
-// Row tiles of a group of n rows.  A tile has up to `blocks` blocks of 32
-// rows.  With 5, the most, a group of up to 160 rows is one tile (a second one
-// would fetch the group's weights again), a larger one has tiles of up to
-// kSplitM rows.  1 to 3 are for few tiles (n < 2^15), where CUs would have
+// Row tiles of a group of n rows, tiles of up to `blocks` blocks of 32 rows.
+// 4 and 5 are the usual ones: a group of up to 160 rows is one tile (a second
+// one would fetch the group's weights again), a larger one has tiles of up to
+// 128 or 160 rows.  1 to 3 are for few tiles (n < 2^15), where CUs would have
 // none: lower ones use more CUs, and the weights they share come from the L2.
 // 16 groups x 160 rows x 4096 x 256: 64 us with one tile a group, 27 with five
 // (fp32 output; bf16 35 and 18).
 constexpr int kTallest = BM / 32;
 __device__ __forceinline__ int row_tiles(int n, int blocks) {
     const int c = (n + 31) >> 5;
-    if (blocks == kTallest) return c <= kTallest ? c > 0 : (c + kSplitM / 32 - 1) / (kSplitM / 32);
+    if (blocks >= 4) return c <= kTallest ? c > 0 : blocks == 4 ? (c + 3) >> 2 : (c + 4) / 5;
     return blocks == 1 ? c : blocks == 2 ? (c + 1) >> 1 : (c + 2) * 21846 >> 16;  // (c + 2) / 3
 }
 
-// Persistent grid, one workgroup a CU.  Items are (group, n-tile, m-tile), the
-// 8 XCDs take contiguous ranges, so that the m-tiles of a weight tile and the
-// n-tiles of a group's rows meet in one XCD's L2; a group's rows split evenly
-// over its m-tiles.  The group of an item comes from a two-level sum that
+// Persistent grid, one workgroup a CU.  Items are (group, band of kBand
+// m-tiles, n-tile, m-tile), the 8 XCDs take contiguous ranges, so that the
+// m-tiles of a weight tile and the n-tiles of a group's rows meet in one XCD's
+// L2: the 32 items that its CUs work on are 8 m-tiles x 4 n-tiles, the shape
+// that needs the fewest rows of both.  (1 group x 8192 rows x 4096 x 2048 with
+// a column of all m-tiles an XCD: 78 us with bf16, 130 with fp32 output; in
+// bands of 8 72 and 121, of 16 73 and 126.)  A group's rows split evenly over
+// its m-tiles.  The group of an item comes from a two-level sum that
 // every wave keeps in registers: lane l holds the items before run l of
 // ceil(G / 64) groups, and looks into the run that holds the item.
+constexpr int kBand = 8;
 static_assert(MOE_MAX_GROUPS <= 64 * 64, "one lane a run, one lane a group of a run");
 
 template <int EPI>
@@ -711,21 +718,45 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_block_kernel(Fp8GemmArgs p)
     const int NT = (p.N + TN - 1) / TN;
     auto clamped = [&](int v) { return min(max(v, 0), rows); };
     const int run = (G + 63) / 64;
-    auto tiles_of_my_run = [&](int blocks) {
-        int sum = 0;
+    // the tiles of this lane's run, NT * (x: of up to b1 blocks, y: of b2)
+    auto tiles_of_my_run = [&](int b1, int b2) {
+        int2 sum = {0, 0};
         for (int i = 0; i < run; ++i) {
             const int g = lane * run + i;
-            if (g < G)
-                sum += row_tiles(max(clamped(p.offsets[g + 1]) - clamped(p.offsets[g]), 0), blocks);
+            if (g < G) {
+                const int n = max(clamped(p.offsets[g + 1]) - clamped(p.offsets[g]), 0);
+                sum.x += row_tiles(n, b1);
+                sum.y += row_tiles(n, b2);
+            }
         }
-        return NT * sum;
+        return int2{NT * sum.x, NT * sum.y};
     };
-    int blocks = kTallest, mine = tiles_of_my_run(blocks), upto = wave_scan(mine, lane);
+    const int2 usual = tiles_of_my_run(4, kTallest);
+    int blocks = 4, mine = usual.x, upto = wave_scan(mine, lane);
+    // Tiles of 160 rows where they save CUs a fifth of their rounds and more
+    // (such a tile takes 1.18 to 1.26 times one of 128 with bf16, 1.24 to 1.30
+    // with fp32 output).  64 groups of 126 to 3500 rows x 2048 x 1024, three
+    // rounds for four: 91 us to 80 with bf16, 136 to 127 with fp32 output; 1
+    // group x 20480 rows x 4096 x 4096, eight for ten: 360 to 364 us (not
+    // taken).
+    auto rounds = [&](int tiles) {
+        const int cus = (int)gridDim.x;
+        return (int)(((long long)tiles + cus - 1) / cus);
+    };
+    const int first = rounds(__builtin_amdgcn_readlane(upto, 63));
+    if (first > 1 && __builtin_amdgcn_ballot_w64(usual.x != usual.y)) {
+        const int sum = wave_scan(usual.y, lane);
+        if (rounds(__builtin_amdgcn_readlane(sum, 63)) * 5ll < first * 4ll) {
+            blocks = kTallest;
+            mine = usual.y;
+            upto = sum;
+        }
+    }
     // few tiles: the lowest of which every one still has a CU of its own
     if ((long long)rows * NT <= 96ll * gridDim.x &&
         __builtin_amdgcn_readlane(upto, 63) < (int)gridDim.x) {
         for (int b = 1; b <= 3; ++b) {
-            const int lower = tiles_of_my_run(b), sum = wave_scan(lower, lane);
+            const int lower = tiles_of_my_run(b, b).x, sum = wave_scan(lower, lane);
             if (__builtin_amdgcn_readlane(sum, 63) > (int)gridDim.x) continue;
             blocks = b;
             mine = lower;
@@ -753,8 +784,10 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_block_kernel(Fp8GemmArgs p)
             r0 = r1;
         }
         const int per = ((n + mt - 1) / mt + 31) & ~31;
-        t.n0 = local / mt * TN;
-        t.row0 = r0 + local % mt * per;
+        const int band = local / (kBand * NT) * kBand, high = min(kBand, mt - band);
+        local -= band * NT;
+        t.n0 = local / high * TN;
+        t.row0 = r0 + (band + local % high) * per;
         t.valid = min(per, r0 + n - t.row0);
     };
     // bytes that this thread's chunk of K's last block reaches past K

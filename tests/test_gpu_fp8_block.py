@@ -231,6 +231,15 @@ def test_grouped_gemm_tile_heights(counts, out):
     test_grouped_gemm(counts, 272, 2320, out)
 
 
+# Groups of more than one band of 8 row tiles (the last one lower), several
+# tiles a CU.  With 10 weight tiles on 256 CUs the first list takes tiles of
+# 160 rows (three rounds for four), the second, of no fewer rounds, of 128.
+@pytest.mark.parametrize("out", [ops.OUT_F32, ops.OUT_BF16])
+@pytest.mark.parametrize("counts", [[12123], [1100, 0, 3001, 160, 161], [2049, 5, 8000]])
+def test_grouped_gemm_bands(counts, out):
+    test_grouped_gemm(counts, 144, 2320, out)
+
+
 def test_grouped_gemm_codes_as_float8():
     a, sa, od, offs, w, sw = operands(2, [9, 40], 256, 128, 5)
     f8 = torch.float8_e4m3fn
@@ -355,6 +364,10 @@ def test_expert_ffn(counts, d, F, mode, lim, out):
 @pytest.mark.parametrize("counts", HEIGHTS)
 def test_expert_ffn_tile_heights(counts):
     test_expert_ffn(counts, 144, 1168, 0, 10.0, ops.OUT_BF16)
+
+
+def test_expert_ffn_bands():
+    test_expert_ffn([1100, 161, 6001], 144, 1168, 0, 10.0, ops.OUT_BF16)
 
 
 def test_expert_ffn_rows_outside_groups_untouched():
