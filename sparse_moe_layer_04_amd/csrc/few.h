@@ -5,7 +5,10 @@
 
 namespace moe {
 
-constexpr int MOE_FEW_SYNC_BYTES = 3 * 8 * 128;
+// workgroups of the experts' kernel, at most; its counters (two kinds, 8 of
+// each, a line apart) and flags (a word a workgroup's share)
+constexpr int MOE_FEW_MAX_SHARES = 1024;
+constexpr int MOE_FEW_SYNC_BYTES = 2 * 8 * 128 + 4 * MOE_FEW_MAX_SHARES;
 
 struct FewArgs {
     int T, d, E, k, F, Fs, mode, n_bias, V;
@@ -30,7 +33,7 @@ struct FewArgs {
     float* w;                      // [T, k]
     uint16_t* hs;                  // [T, Fs] bf16
     uint16_t* h;                   // [T k, F] bf16, by pair
-    uint32_t* sync;                // tickets and counts, MOE_FEW_SYNC_BYTES
+    uint32_t* sync;                // tickets and flags, MOE_FEW_SYNC_BYTES
 };
 
 hipError_t launch_few(bool fp8, const FewArgs& p, hipStream_t stream);

@@ -12,8 +12,11 @@
 // 8-bit: 0.85 ms (3.9 GB, 4.6 TB/s: of an expert with several tokens the
 // weights' columns are multiplied once, but every strip reads its tokens'
 // activations again).  Of one token's 33 us the first kernel takes 5, the
-// second 26: 4 until its workgroups have the experts' table, 11 for the gate
-// and up products, 4 until all know that they are done and 7 for the rest.
+// second 26: 3 until its workgroups have the experts' table, 12 for the gate
+// and up products, 4 until all know that they are done and 7 for the rest; 2
+// lie between the kernels.  (Sixteen pieces of the weights in flight for
+// eight, or x and h staged in LDS: no faster.  What is asked for earlier in
+// the wait makes the wait longer.)
 //
 // One kind of work serves every product of the layer: a strip of 16 weight
 // rows times the rows' tokens.  A wave's load instruction covers 64 bytes of
@@ -275,6 +278,9 @@ __device__ __forceinline__ void set_gate_up(Strip<FP8, STEP>& s, const void* gat
 // ------------------------------------------------ router and shared expert --
 // Items: 16 experts' router rows, then 8 features of the shared expert: none
 // depends on the routing.  Few strips: each is split over a workgroup's waves.
+// (384 experts, d 4096, Fs 2048, 8-bit weights: 24 + 256 items on 256 CUs take
+// 10 us.  The router's rows dealt out to the 256 others, two apiece, take 9,
+// and one token of the layer 57.8 us for 58.4; two workgroups a CU, 10.)
 template <bool FP8>
 __global__ __launch_bounds__(kThreads) void few_router_kernel(FewArgs p) {
     extern __shared__ __align__(16) float red[];
@@ -284,7 +290,7 @@ __global__ __launch_bounds__(kThreads) void few_router_kernel(FewArgs p) {
     auto row = [&](int c) { return p.x + (size_t)min(16 * c + l.r16, p.T - 1) * p.d; };
     auto partials = [&](int c, const f32x4& acc) { put_partials(red, acc, c, ct, l); };
     const int item = blockIdx.x;
-    // the next kernel's counters
+    // the next kernel's counters and flags
     if (item == 0)
         for (int i = l.tid; i < MOE_FEW_SYNC_BYTES / 4; i += kThreads) p.sync[i] = 0u;
     if (item < nr) {
@@ -436,8 +442,8 @@ __device__ __forceinline__ void build_table(const FewArgs& p, const Lane& l, Tab
 // only once all shares have been taken, by workgroups that are running: who
 // waits, waits for work that is going on, however many workgroups the device
 // holds at once.  Each of 8 slots (blockIdx % 8, an XCD's workgroups) has its
-// own share of the tickets and counts, a line apart: on one counter 256
-// workgroups queue for 16 us.
+// own share of the tickets, a line apart: on one counter 256 workgroups queue
+// for 16 us.
 //
 // Gate/up: one wave a strip (expert, 8 features), every token of the expert at
 // once (16 columns; more in further column tiles).
@@ -448,20 +454,37 @@ __device__ __forceinline__ void build_table(const FewArgs& p, const Lane& l, Tab
 // chunk are on their way while its waves wait for the shares.
 //
 // h crosses the XCDs, whose L2s are not coherent: it is stored at device scope
-// (a fence would write a whole L2 back), counted once the stores have
-// completed, and read after an acquire fence behind the count.
+// (a fence would write a whole L2 back), its share's flag set once the stores
+// have completed, and read after an acquire fence behind the flags.
 constexpr int kSlots = 8;
 __device__ __forceinline__ uint32_t* sync_word(const FewArgs& p, int kind, int slot) {
     return p.sync + (kind * kSlots + slot) * 32;
 }
-enum SyncKind : int { kShares = 0, kChunks = 1, kDone = 2 };
-constexpr int kSyncWords = 3 * kSlots * 32;
-static_assert(kSyncWords * 4 == MOE_FEW_SYNC_BYTES, "workspace of the counters");
+enum SyncKind : int { kShares = 0, kChunks = 1 };
+constexpr int kCounterWords = 2 * kSlots * 32;
+static_assert((kCounterWords + MOE_FEW_MAX_SHARES) * 4 == MOE_FEW_SYNC_BYTES,
+              "workspace of the counters and flags");
+// a word a share: 1 when its h is in memory (a flag each, since additions to
+// one counter wait for each other, 60 ns apiece)
+__device__ __forceinline__ uint32_t* done_flags(const FewArgs& p) { return p.sync + kCounterWords; }
 __device__ __forceinline__ unsigned take(uint32_t* counter) {
     return __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 __device__ __forceinline__ unsigned look(const uint32_t* counter) {
     return __hip_atomic_load(counter, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// one wave: whether all shares (an even number) are done
+__device__ __forceinline__ bool all_done(const FewArgs& p, int shares, int lane) {
+    const uint64_t* two = (const uint64_t*)done_flags(p);
+    bool open = false;
+    for (int i = lane; 2 * i < shares; i += 128) {
+        const int j = min(i + 64, shares / 2 - 1);
+        const uint64_t a = __hip_atomic_load(two + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const uint64_t b = __hip_atomic_load(two + j, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        open |= (a & b) != 0x100000001ull;
+    }
+    return !__builtin_amdgcn_ballot_w64(open);
 }
 
 template <bool FP8>
@@ -473,9 +496,12 @@ __global__ __launch_bounds__(kThreads) void few_experts_kernel(FewArgs p) {
     const Lane l = this_lane();
     const int slot_of = blockIdx.x % kSlots;
     const int shares = gridDim.x, per_slot = shares / kSlots;   // (whole)
-    // thread 0's tickets in hand: a share and, taken ahead, a chunk
-    unsigned share_t = 0, chunk_t = 0;
-    if (l.tid == 0) {
+    // The last wave takes the tickets (its first thread: a share and, ahead, a
+    // chunk): the first ones route, and what a wave loads comes back behind
+    // the tickets that it has asked for before, 2 us for 32 of one counter.
+    const bool clerk = l.wave == kThreads / 64 - 1;
+    unsigned share_t = 0, chunk_t = 0, taken = 0u;
+    if (clerk && l.lane == 0) {
         share_t = take(sync_word(p, kShares, slot_of));
         chunk_t = take(sync_word(p, kChunks, slot_of));
         open_sh = 0u;
@@ -486,30 +512,33 @@ __global__ __launch_bounds__(kThreads) void few_experts_kernel(FewArgs p) {
     const int per = p.F / 8, strips = n * per, chunks = p.d / 16;
     bool more_shares = true;
     for (;;) {
-        if (more_shares && l.wave == 0) {
-            // the slot's next share, or one that another slot has left
+        if (more_shares && clerk) {
+            // the slot's next share, or one that another slot has left (lane l
+            // holds how many of slot l's were taken when it last looked)
             int share = (int)share_t < per_slot ? slot_of + kSlots * (int)share_t : -1;
             share = __builtin_amdgcn_readfirstlane(share);
             while (share < 0) {
-                const unsigned taken =
-                    l.lane < kSlots ? look(sync_word(p, kShares, l.lane)) : ~0u;
-                const uint64_t left = __builtin_amdgcn_ballot_w64((int)min(taken, 0x7fffffffu) <
-                                                                  per_slot);
+                const uint64_t left = __builtin_amdgcn_ballot_w64(l.lane < kSlots &&
+                                                                  taken < (unsigned)per_slot);
                 if (!left) break;
                 const int from = __builtin_ctzll(left);
                 unsigned got = 0;
                 if (l.lane == 0) got = take(sync_word(p, kShares, from));
                 got = (unsigned)__builtin_amdgcn_readfirstlane((int)got);
                 if ((int)got < per_slot) share = from + kSlots * (int)got;
+                else if (l.lane < kSlots) taken = look(sync_word(p, kShares, l.lane));
             }
             if (l.lane == 0) share_sh = share;
         }
-        if (l.tid == 0) chunk_sh = slot_of + kSlots * (int)min(chunk_t, 1u << 24);
+        if (clerk && l.lane == 0) chunk_sh = slot_of + kSlots * (int)min(chunk_t, 1u << 24);
         __syncthreads();
         const int share = more_shares ? share_sh : -1, chunk = chunk_sh;
         more_shares = share >= 0;
         if (more_shares) {
-            if (l.tid == 0) share_t = take(sync_word(p, kShares, slot_of));
+            if (clerk) {
+                if (l.lane == 0) share_t = take(sync_word(p, kShares, slot_of));
+                if (l.lane < kSlots) taken = look(sync_word(p, kShares, l.lane));
+            }
             // (strips dealt to the shares first, so that few strips use every
             // CU; finer shares or strips taken one by one balance the CUs
             // better but end no earlier: memory's rate decides)
@@ -546,27 +575,26 @@ __global__ __launch_bounds__(kThreads) void few_experts_kernel(FewArgs p) {
             }
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wave's stores are there
             __syncthreads();
-            if (l.tid == 0) take(sync_word(p, kDone, share % kSlots));
+            if (l.tid == 0)
+                __hip_atomic_store(done_flags(p) + share, 1u, __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
             continue;
         }
         if (chunk >= chunks) return;
-        if (l.tid == 0) chunk_t = take(sync_word(p, kChunks, slot_of));
-        // the last wave watches the count for all (through LDS: a wave's own
-        // load would queue behind its weights)
+        if (clerk && l.lane == 0) chunk_t = take(sync_word(p, kChunks, slot_of));
+        // the clerk watches the flags for all (through LDS: a wave's own load
+        // would queue behind its weights)
         auto ready = [&] {
             if (opened) return;
             auto is_open = [&] {
                 return __hip_atomic_load(&open_sh, __ATOMIC_RELAXED,
                                          __HIP_MEMORY_SCOPE_WORKGROUP) != 0u;
             };
-            if (l.wave == 7 && !is_open()) {
+            if (clerk && !is_open()) {
                 // (the limit, seconds, ends the wait when another call has
-                // cleared the counts of this call's workspace meanwhile)
+                // cleared the flags of this call's workspace meanwhile)
                 int polls = 0;
-                while (__builtin_amdgcn_ballot_w64(
-                           l.lane < kSlots &&
-                           look(sync_word(p, kDone, l.lane)) != (unsigned)per_slot) &&
-                       ++polls < kMaxPolls)
+                while (!all_done(p, shares, l.lane) && ++polls < kMaxPolls)
                     __builtin_amdgcn_s_sleep(1);
                 if (polls == kMaxPolls && l.lane == 0 && p.flags)
                     atomicOr(p.flags, MOE_FLAG_OVERLAP);
@@ -580,7 +608,7 @@ __global__ __launch_bounds__(kThreads) void few_experts_kernel(FewArgs p) {
             __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
             opened = true;
         };
-        if (l.wave == 7) ready();
+        if (clerk) ready();
         for (int u = l.wave; u < n + sh; u += 8) {
             const bool shared = u >= n;
             const int s = shared ? 0 : tb.start[u];
@@ -634,7 +662,8 @@ hipError_t launch(const FewArgs& p, hipStream_t stream) {
     hipLaunchKernelGGL(few_router_kernel<FP8>, dim3(grid1), dim3(kThreads), red, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(few_experts_kernel<FP8>, dim3((device_cu_count() + 7) & ~7), dim3(kThreads),
+    const int shares = min((device_cu_count() + 7) & ~7, MOE_FEW_MAX_SHARES);
+    hipLaunchKernelGGL(few_experts_kernel<FP8>, dim3(shares), dim3(kThreads),
                        (size_t)(p.T * p.k + p.T) * 16 * sizeof(float), stream, p);
     return hipGetLastError();
 }

@@ -128,6 +128,17 @@ def test_topk(T, d, E, k, F, Fs, fp8):
     check(*make(T, d, E, k, F, Fs, fp8, T + d + E))
 
 
+# router and shared expert in more workgroups than 256 CUs hold at once, in as
+# many, and a last router strip of few experts
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T,d,E,k,F,Fs", [
+    (1, 64, 240, 2, 64, 2048), (1, 1216, 384, 6, 64, 2048), (16, 128, 511, 3, 64, 2048),
+    (33, 192, 1000, 2, 64, 2048), (64, 64, 1024, 8, 64, 1984), (17, 128, 17, 2, 64, 2048),
+    (64, 128, 200, 2, 64, 2112)])
+def test_router_beside_the_shared_expert(T, d, E, k, F, Fs, fp8):
+    check(*make(T, d, E, k, F, Fs, fp8, T + d + E))
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("kw", [
     dict(n_bias=1), dict(n_bias=2), dict(n_bias=2, offset=True), dict(mode=ops.MODE_HASH),
