@@ -23,6 +23,15 @@
 namespace moe {
 namespace {
 
+// A launch's x extent holds fewer than 2^32 threads, which are 2^24 workgroups
+// of 256: beyond kGridX workgroups there are rows of them.
+constexpr unsigned kGridX = 1u << 20;
+dim3 grid_of(unsigned n) {
+    const unsigned x = n < kGridX ? n : kGridX;
+    return dim3(x, (n + x - 1) / x);
+}
+__device__ __forceinline__ unsigned workgroup() { return blockIdx.y * gridDim.x + blockIdx.x; }
+
 // values of one 16-byte load: 8 bf16 or 4 fp32
 template <bool F32>
 struct Ld {
@@ -70,7 +79,9 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const void* __restrict_
                                                          unsigned nblocks, int K, int nb) {
     constexpr int V = Ld<F32>::V, L = Ld<F32>::L, PB = 256 / L;
     const int li = threadIdx.x % L;
-    const unsigned first = blockIdx.x * (unsigned)(PB * kU) + threadIdx.x / L;
+    // (past the last block: a workgroup of the last row of them has none)
+    const unsigned first = min(workgroup(), (nblocks - 1) / (PB * kU) + 1) * (unsigned)(PB * kU) +
+                           threadIdx.x / L;
     u32x4 w[kU];
     size_t at[kU];
     bool live[kU];
@@ -101,10 +112,12 @@ template <bool F32>
 __global__ __launch_bounds__(256) void quant_matrix_kernel(const void* __restrict__ a,
                                                            uint8_t* __restrict__ codes,
                                                            float* __restrict__ scales, int N,
-                                                           int K, int nbn, int nbk) {
+                                                           int K, int nbn, int nbk,
+                                                           unsigned nblocks) {
     constexpr int V = Ld<F32>::V, L = Ld<F32>::L, PR = 256 / L, NP = 128 / PR;
     __shared__ float part[4];
-    const unsigned blk = blockIdx.x;
+    const unsigned blk = workgroup();
+    if (blk >= nblocks) return;
     const unsigned kb = blk % (unsigned)nbk, rest = blk / (unsigned)nbk;
     const unsigned rb = rest % (unsigned)nbn, g = rest / (unsigned)nbn;
     const int c = (int)kb * 128 + (threadIdx.x % L) * V;
@@ -144,7 +157,7 @@ hipError_t launch_quant_rows_fp8_block(const void* a, int in_dtype, long long ro
     const unsigned nblocks = (unsigned)(rows * nb);
     if (nblocks == 0) return hipSuccess;
     const unsigned per = (in_dtype == MOE_IN_F32 ? 8u : 16u) * kU;
-    const dim3 grid((nblocks + per - 1) / per);
+    const dim3 grid = grid_of((nblocks + per - 1) / per);
     if (in_dtype == MOE_IN_F32)
         hipLaunchKernelGGL(quant_rows_kernel<true>, grid, dim3(256), 0, stream, a, codes, scales,
                            nblocks, K, nb);
@@ -157,13 +170,14 @@ hipError_t launch_quant_rows_fp8_block(const void* a, int in_dtype, long long ro
 hipError_t launch_quant_matrix_fp8_block(const void* w, int in_dtype, int G, int N, int K,
                                          uint8_t* codes, float* scales, hipStream_t stream) {
     const int nbn = (N + 127) / 128, nbk = (K + 127) / 128;
-    const dim3 grid((unsigned)((long long)G * nbn * nbk));
+    const unsigned nblocks = (unsigned)((long long)G * nbn * nbk);
+    const dim3 grid = grid_of(nblocks);
     if (in_dtype == MOE_IN_F32)
         hipLaunchKernelGGL(quant_matrix_kernel<true>, grid, dim3(256), 0, stream, w, codes, scales,
-                           N, K, nbn, nbk);
+                           N, K, nbn, nbk, nblocks);
     else
         hipLaunchKernelGGL(quant_matrix_kernel<false>, grid, dim3(256), 0, stream, w, codes,
-                           scales, N, K, nbn, nbk);
+                           scales, N, K, nbn, nbk, nblocks);
     return hipGetLastError();
 }
 

@@ -173,6 +173,21 @@ def test_quantize_matrix(G, N, K, dtype):
         assert torch.equal(c2, codes[0]) and torch.equal(s2, scales[0])
 
 
+def test_quantize_more_matrices_than_one_grid_row():
+    """2^24 blocks and more: over several rows of workgroups."""
+    G = (1 << 24) + 5
+    g = gen(3)
+    w = torch.randint(-200, 200, (G, 1, 16), generator=g, device=DEV).bfloat16()
+    codes, scales = ops.quantize_weights_fp8_block(w)
+    m = w.abs().amax(2).float()                    # (at most 200: below 448 * 2^X, X <= -1)
+    X = torch.ceil(torch.log2(m.clamp(min=1).double() / 448))
+    want = torch.where(m > 0, torch.exp2(X), torch.ones_like(X)).float()
+    assert torch.equal(scales.view(-1), want.view(-1))
+    for lo in range(0, G, 1 << 22):
+        v = w[lo:lo + (1 << 22)].float() / want[lo:lo + (1 << 22), :, None]
+        assert torch.equal(codes[lo:lo + (1 << 22)], v.to(torch.float8_e4m3fn).view(torch.uint8))
+
+
 def test_quantize_nothing():
     codes, scales = ops.quantize_fp8_block(torch.empty((0, 256), device=DEV))
     assert codes.shape == (0, 256) and scales.shape == (0, 2)
