@@ -569,7 +569,7 @@ int moe_forward_timed(const moe_cfg* cfg, const moe_weights* w, const uint16_t* 
 /* ------------------------------------------------------------------------
  * Whole layer forward for a few tokens (decoding): the layer of moe_forward
  * for T <= MOE_FEW_MAX_T tokens, on weights as checkpoints hold them, in two
- * kernels without a dispatch permutation.  Arguments, limits and outputs as
+ * or three kernels without a dispatch permutation.  Arguments, limits and outputs as
  * moe_forward, with
  *   w->packed == 0: bf16 matrices [out, in], or MOE_WEIGHTS_FP8_BLOCK: 8-bit
  *   codes with fp32 scales of 128 x 128 blocks (moe_weights); activations

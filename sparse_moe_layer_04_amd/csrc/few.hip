@@ -6,13 +6,13 @@
 // part in a few products; at one token the read of six experts' and the
 // shared expert's matrices is tens of microseconds, so launches and
 // dependent round trips count as much as the bandwidth.  Measured: one token,
-// 64 experts of 2048 x 1024, bf16, six and the shared one used: 33 us (88 MB,
-// 2.7 TB/s); 384 experts of 4096 x 2048, 8-bit: 58 us (178 MB, 3.1 TB/s);
+// 64 experts of 2048 x 1024, bf16, six and the shared one used: 34 us (88 MB,
+// 2.6 TB/s); 384 experts of 4096 x 2048, 8-bit: 58 us (178 MB, 3.1 TB/s);
 // eight tokens of those, bf16: 0.40 ms (2.4 GB, 6 TB/s); 33 tokens of them,
-// 8-bit: 0.85 ms (3.9 GB, 4.6 TB/s: of an expert with several tokens the
+// 8-bit: 0.80 ms (3.9 GB, 4.9 TB/s: of an expert with several tokens the
 // weights' columns are multiplied once, but every strip reads its tokens'
-// activations again).  Of one token's 33 us the first kernel takes 5, the
-// second 26: 3 until its workgroups have the experts' table, 12 for the gate
+// activations again).  Of one token's 34 us the first kernel takes 4, the
+// second 27: 3 until its workgroups have the experts' table, 12 for the gate
 // and up products, 4 until all know that they are done and 7 for the rest; 2
 // lie between the kernels.  (Sixteen pieces of the weights in flight for
 // eight, or x and h staged in LDS: no faster.  What is asked for earlier in
@@ -334,7 +334,7 @@ struct Table {
     int expert[kMaxPairs];       // distinct experts, in order of first use
     int start[kMaxPairs + 1];    // their first entries in pairs
     int pairs[kMaxPairs];        // pair indexes t k + j, grouped by expert
-    int first[kMaxPairs];        // (by pair) start of the expert it is the first of
+    int lead[MOE_MAX_E];         // (by expert) its first pair, then its first entry
     int scan[8];
     int n;                       // distinct experts
 };
@@ -346,73 +346,168 @@ __device__ __forceinline__ void topk_token(const FewArgs& p, int t, int lane, in
                          id, w);
 }
 
-// one wave: the k experts and weights of token t in lanes j < k (the scores,
-// ties, sums and refusals of moe_route); returns the flag bits
-__device__ __forceinline__ uint32_t route_token(const FewArgs& p, int t, int lane, int& id,
-                                                float& w) {
-    if (p.mode == MOE_MODE_TOPK) {
-        if (p.E <= 64) topk_token<1>(p, t, lane, id, w);
-        else if (p.E <= 256) topk_token<4>(p, t, lane, id, w);
-        else if (p.E <= 384) topk_token<6>(p, t, lane, id, w);
-        else topk_token<MOE_MAX_E / 64>(p, t, lane, id, w);
-        return 0u;
-    }
-    const int tok = p.input_ids[t];
-    id = -1;
-    w = 0.0f;
-    if (tok < 0 || tok >= p.V) return MOE_FLAG_BAD_INPUT_ID;
-    if (lane < p.k) id = p.tid2eid[(size_t)tok * p.k + lane];
-    if (__builtin_amdgcn_ballot_w64(lane < p.k && (id < 0 || id >= p.E))) {
-        id = -1;
-        return MOE_FLAG_BAD_EXPERT_ID;
-    }
-    const float g = lane < p.k ? score_fn(p.logits[(size_t)t * p.E + id]) : 0.0f;
-    float sum = lane_read(g, 0);
-    for (int j = 1; j < p.k; ++j) sum = sum + lane_read(g, j);
-    w = (g / sum) * p.scale;
-    return 0u;
+// one wave: the k experts and weights of token t in lanes j < k (top-k)
+__device__ __forceinline__ void route_token(const FewArgs& p, int t, int lane, int& id, float& w) {
+    if (p.E <= 64) topk_token<1>(p, t, lane, id, w);
+    else if (p.E <= 256) topk_token<4>(p, t, lane, id, w);
+    else if (p.E <= 384) topk_token<6>(p, t, lane, id, w);
+    else topk_token<MOE_MAX_E / 64>(p, t, lane, id, w);
 }
 
-// every workgroup routes the batch for itself (the logits are in the caches);
-// workgroup 0 writes ids and weights out
-__device__ __forceinline__ void build_table(const FewArgs& p, const Lane& l, Table& tb) {
-    for (int t = l.wave; t < p.T; t += 8) {
-        int id;
-        float w;
-        const uint32_t bad = route_token(p, t, l.lane, id, w);
-        if (l.lane < p.k) {
-            tb.ids[t * p.k + l.lane] = id;
-            tb.w[t * p.k + l.lane] = w;
-            if (blockIdx.x == 0) {
-                p.ids[t * p.k + l.lane] = id;
-                p.w[t * p.k + l.lane] = w;
-            }
-        }
-        if (bad && l.lane == 0 && blockIdx.x == 0 && p.flags) atomicOr(p.flags, bad);
+// A token takes a wave 2 (up to 64 experts) to 3 us (384), whatever the other
+// waves do.  Up to two a wave each workgroup of the experts' kernel routes the
+// batch for itself; more get a wave each in a kernel of their own, which costs
+// 5 us with its launch.  (32 tokens, 27 experts: 9 us in each workgroup; 31
+// tokens, 330 experts: 12.)
+constexpr int kOwnTokens = 16;
+__host__ __device__ __forceinline__ bool routed_before(const FewArgs& p) {
+    return p.mode == MOE_MODE_TOPK && p.T > kOwnTokens;
+}
+__global__ __launch_bounds__(64) void few_route_kernel(FewArgs p) {
+    const int t = blockIdx.x, lane = threadIdx.x;
+    int id;
+    float w;
+    route_token(p, t, lane, id, w);
+    if (lane < p.k) {
+        p.ids[t * p.k + lane] = id;
+        p.w[t * p.k + lane] = w;
     }
-    __syncthreads();
+}
+
+// ids and weights of the batch into tb (the scores, ties, sums and refusals of
+// moe_route); workgroup 0 writes them out
+__device__ __forceinline__ void route_batch(const FewArgs& p, const Lane& l, Table& tb) {
     const int P = p.T * p.k, me = l.tid;
-    int id = -1, rank = 0, count = 0, lead = me;
-    if (me < P) {
-        id = tb.ids[me];
-        for (int q = 0; q < P; ++q) {
-            const bool same = tb.ids[q] == id;
-            count += same;
-            if (same && q < me) {
-                if (rank == 0) lead = q;
-                ++rank;
+    if (p.mode == MOE_MODE_HASH) {
+        // a thread a pair
+        int id = -1;
+        float g = 0.0f;
+        if (me < P) {
+            const int t = me / p.k, j = me - t * p.k, tok = p.input_ids[t];
+            const bool known = tok >= 0 && tok < p.V;
+            if (known) id = p.tid2eid[(size_t)tok * p.k + j];
+            if (known && (id < 0 || id >= p.E)) id = -2;
+            if (id >= 0) g = score_fn(p.logits[(size_t)t * p.E + id]);
+            tb.ids[me] = id;
+            tb.w[me] = g;
+        }
+        __syncthreads();
+        float w = 0.0f;
+        if (me < P) {
+            const int first = me / p.k * p.k;
+            float sum = 0.0f;
+            int worst = 0;
+            for (int j = 0; j < p.k; ++j) {
+                sum = j ? sum + tb.w[first + j] : tb.w[first];
+                worst = min(worst, tb.ids[first + j]);
+            }
+            w = worst < 0 ? 0.0f : (g / sum) * p.scale;
+            id = worst < 0 ? -1 : id;
+            if (blockIdx.x == 0) {
+                p.ids[me] = id;
+                p.w[me] = w;
+                if (worst < 0 && me == first && p.flags)
+                    atomicOr(p.flags, worst == -2 ? MOE_FLAG_BAD_EXPERT_ID : MOE_FLAG_BAD_INPUT_ID);
+            }
+        }
+        __syncthreads();
+        if (me < P) {
+            tb.ids[me] = id;
+            tb.w[me] = w;
+        }
+    } else if (routed_before(p)) {
+        if (me < P) {
+            tb.ids[me] = p.ids[me];
+            tb.w[me] = p.w[me];
+        }
+    } else {
+        for (int t = l.wave; t < p.T; t += 8) {
+            int id;
+            float w;
+            route_token(p, t, l.lane, id, w);
+            if (l.lane < p.k) {
+                tb.ids[t * p.k + l.lane] = id;
+                tb.w[t * p.k + l.lane] = w;
+                if (blockIdx.x == 0) {
+                    p.ids[t * p.k + l.lane] = id;
+                    p.w[t * p.k + l.lane] = w;
+                }
             }
         }
     }
-    const bool lead_here = me < P && id >= 0 && rank == 0;
-    // inclusive scan of (1, rows) over the leading pairs
-    int x = lead_here ? (1 << 16) | count : 0;
-    const int mine = x;
+}
+
+__device__ __forceinline__ int wave_scan(int x, int lane) {   // inclusive
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
         const int y = __shfl_up(x, off, 64);
-        if (l.lane >= off) x += y;
+        if (lane >= off) x += y;
     }
+    return x;
+}
+
+// The table of up to 64 pairs, by one wave: ballots of the ids' bits give each
+// pair the set of its expert's pairs.  (One token of the 64-expert layer takes
+// 1 us less than with the masks in LDS and their barriers.)
+__device__ __forceinline__ void build_small(int P, int lane, Table& tb) {
+    static_assert(MOE_MAX_E <= 1 << 10, "bits of an id");
+    const int id = lane < P ? tb.ids[lane] : -1;
+    uint64_t same = __builtin_amdgcn_ballot_w64(id >= 0);
+#pragma unroll
+    for (int bit = 0; bit < 10; ++bit) {
+        const uint64_t ones = __builtin_amdgcn_ballot_w64(id >> bit & 1);
+        same &= id >> bit & 1 ? ones : ~ones;
+    }
+    if (id < 0) same = 0u;
+    const int rank = __popcll(same & ((1ull << lane) - 1u));
+    const bool lead_here = id >= 0 && rank == 0;
+    // sum of (1, rows) over the leading pairs
+    const int mine = lead_here ? (1 << 16) | __popcll(same) : 0, x = wave_scan(mine, lane);
+    const int ex = x - mine;
+    if (lead_here) {
+        tb.expert[ex >> 16] = id;
+        tb.start[ex >> 16] = ex & 0xffff;
+    }
+    const int first = __shfl(ex, same ? __builtin_ctzll(same) : 0, 64) & 0xffff;
+    if (id >= 0) tb.pairs[first + rank] = lane;
+    if (lane == 63) {
+        tb.n = x >> 16;
+        tb.start[x >> 16] = x & 0xffff;
+    }
+}
+
+// The table of more.  mask: P rows of ceil(P / 32) words of LDS.  The first
+// pair of an expert has a row with a bit for each of the expert's pairs: their
+// number and a pair's place among them are counts of bits.
+__device__ __forceinline__ void build_table(const FewArgs& p, const Lane& l, Table& tb,
+                                            uint32_t* mask) {
+    const int P = p.T * p.k, W = (P + 31) / 32, me = l.tid;
+    if (P > 64) {
+        for (int i = l.tid; i < P * W; i += kThreads) mask[i] = 0u;
+        for (int i = l.tid; i < p.E; i += kThreads) tb.lead[i] = kMaxPairs;
+    }
+    route_batch(p, l, tb);
+    __syncthreads();
+    if (P <= 64) {
+        if (l.wave == 0) build_small(P, l.lane, tb);
+        __syncthreads();
+        return;
+    }
+    const int id = me < P ? tb.ids[me] : -1;
+    if (id >= 0) atomicMin(&tb.lead[id], me);
+    __syncthreads();
+    const int lead = id >= 0 ? tb.lead[id] : 0;
+    if (id >= 0) atomicOr(&mask[lead * W + me / 32], 1u << (me % 32));
+    __syncthreads();
+    int rank = 0, count = 0;
+    if (id >= 0)
+        for (int i = 0; i < W; ++i) {
+            const uint32_t bits = mask[lead * W + i];
+            count += __popc(bits);
+            rank += __popc(i < me / 32 ? bits : i == me / 32 ? bits & ((1u << (me % 32)) - 1u) : 0u);
+        }
+    const bool lead_here = id >= 0 && rank == 0;
+    const int mine = lead_here ? (1 << 16) | count : 0, x = wave_scan(mine, l.lane);
     if (l.lane == 63) tb.scan[l.wave] = x;
     __syncthreads();
     int before = 0, total = 0;
@@ -424,14 +519,14 @@ __device__ __forceinline__ void build_table(const FewArgs& p, const Lane& l, Tab
     if (lead_here) {
         tb.expert[ex >> 16] = id;
         tb.start[ex >> 16] = ex & 0xffff;
-        tb.first[me] = ex & 0xffff;
+        tb.lead[id] = ex & 0xffff;               // (from here on the first entry)
     }
     if (me == 0) {
         tb.n = total >> 16;
         tb.start[total >> 16] = total & 0xffff;
     }
     __syncthreads();
-    if (me < P && id >= 0) tb.pairs[tb.first[lead] + rank] = me;
+    if (id >= 0) tb.pairs[tb.lead[id] + rank] = me;
     __syncthreads();
 }
 
@@ -489,7 +584,8 @@ __device__ __forceinline__ bool all_done(const FewArgs& p, int shares, int lane)
 
 template <bool FP8>
 __global__ __launch_bounds__(kThreads) void few_experts_kernel(FewArgs p) {
-    extern __shared__ __align__(16) float out[];     // [P + T][16]
+    // [P + T][16]; the table's masks before (at most kMaxPairs / 8 = 64 bytes a pair)
+    extern __shared__ __align__(16) float out[];
     __shared__ Table tb;
     __shared__ int share_sh, chunk_sh;
     __shared__ unsigned open_sh;
@@ -507,9 +603,17 @@ __global__ __launch_bounds__(kThreads) void few_experts_kernel(FewArgs p) {
         open_sh = 0u;
     }
     bool opened = false;                             // the shares are done
-    build_table(p, l, tb);
+    build_table(p, l, tb, (uint32_t*)out);
     const int n = tb.n, P = p.T * p.k, sh = p.Fs > 0 ? 1 : 0;
-    const int per = p.F / 8, strips = n * per, chunks = p.d / 16;
+    const int per = p.F / 8, strips = n * per;
+    // Chunks by 16 outputs and, where those are fewer than the workgroups, by
+    // parts of the tokens: a part's experts' weights are read again, from the
+    // caches.  (31 tokens, 330 experts, d 256, 8-bit weights: 16 workgroups of
+    // 111 experts' strips 19 us, 256 of two tokens' 6; 64 tokens, 64 experts,
+    // d 2048: the whole layer 256 us with 128 chunks, 218 with 256.)
+    const int columns = p.d / 16;
+    const int tokens = (p.T + max(shares / columns, 1) - 1) / max(shares / columns, 1);
+    const int chunks = columns * ((p.T + tokens - 1) / tokens);
     bool more_shares = true;
     for (;;) {
         if (more_shares && clerk) {
@@ -609,27 +713,39 @@ __global__ __launch_bounds__(kThreads) void few_experts_kernel(FewArgs p) {
             opened = true;
         };
         if (clerk) ready();
+        const int column = chunk % columns, t0 = chunk / columns * tokens;
+        const int t1 = min(t0 + tokens, p.T);
         for (int u = l.wave; u < n + sh; u += 8) {
             const bool shared = u >= n;
-            const int s = shared ? 0 : tb.start[u];
-            const int m_all = shared ? p.T : tb.start[u + 1] - s;
+            // the part's entries of the expert (they are in the tokens' order)
+            int s = shared ? t0 : tb.start[u], m_all = shared ? t1 - t0 : tb.start[u + 1] - s;
+            if (!shared && tokens < p.T) {
+                int below = 0, inside = 0;
+                for (int i = 0; i < m_all; i += 64) {
+                    const int q = i + l.lane < m_all ? tb.pairs[s + i + l.lane] : kMaxPairs;
+                    below += __popcll(__builtin_amdgcn_ballot_w64(q < t0 * p.k));
+                    inside += __popcll(__builtin_amdgcn_ballot_w64(q >= t0 * p.k && q < t1 * p.k));
+                }
+                s += below;
+                m_all = inside;
+            }
             const int K = shared ? p.Fs : p.F;
             const size_t mat = shared ? 0 : (size_t)tb.expert[u];
             Strip<FP8, 1> st;
             st.wrow = (const uint8_t*)(shared ? p.s_down : p.w_down) +
-                      (mat * p.d + 16 * chunk + l.r16) * (size_t)K * (FP8 ? 1 : 2);
+                      (mat * p.d + 16 * column + l.r16) * (size_t)K * (FP8 ? 1 : 2);
             st.K = K;
             st.grp = l.grp;
             if constexpr (FP8) {
                 const int nbd = (p.d + 127) / 128, nbk = (K + 127) / 128;
                 st.srow = (shared ? p.s_down_scale : p.w_down_scale) +
-                          (mat * nbd + chunk / 8) * (size_t)nbk;
+                          (mat * nbd + column / 8) * (size_t)nbk;
             }
             for (int m0 = 0; m0 < m_all; m0 += MOE_FEW_MAX_T) {
                 const int m = min(m_all - m0, MOE_FEW_MAX_T), ct = (m + 15) / 16;
                 auto slot = [&](int c) {
-                    const int r = m0 + min(16 * c + l.r16, m - 1);
-                    return shared ? P + r : tb.pairs[s + r];
+                    const int r = s + m0 + min(16 * c + l.r16, m - 1);
+                    return shared ? P + r : tb.pairs[r];
                 };
                 st.run([&](int c) { return shared ? p.hs + (size_t)(slot(c) - P) * K
                                                   : p.h + (size_t)slot(c) * K; },
@@ -640,13 +756,13 @@ __global__ __launch_bounds__(kThreads) void few_experts_kernel(FewArgs p) {
             }
         }
         __syncthreads();
-        for (int i = l.tid; i < p.T * 16; i += kThreads) {
-            const int t = i >> 4, o = i & 15;
+        for (int i = l.tid; i < (t1 - t0) * 16; i += kThreads) {
+            const int t = t0 + (i >> 4), o = i & 15;
             float v = sh ? out[(P + t) * 16 + o] : 0.0f;
             for (int j = 0; j < p.k; ++j)
                 if (tb.ids[t * p.k + j] >= 0)
                     v = __builtin_fmaf(tb.w[t * p.k + j], out[(t * p.k + j) * 16 + o], v);
-            const size_t at = (size_t)t * p.d + 16 * chunk + o;
+            const size_t at = (size_t)t * p.d + 16 * column + o;
             if (p.out_dtype == MOE_OUT_F32)
                 ((float*)p.y)[at] = v;
             else
@@ -662,6 +778,11 @@ hipError_t launch(const FewArgs& p, hipStream_t stream) {
     hipLaunchKernelGGL(few_router_kernel<FP8>, dim3(grid1), dim3(kThreads), red, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    if (routed_before(p)) {
+        hipLaunchKernelGGL(few_route_kernel, dim3(p.T), dim3(64), 0, stream, p);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
     const int shares = min((device_cu_count() + 7) & ~7, MOE_FEW_MAX_SHARES);
     hipLaunchKernelGGL(few_experts_kernel<FP8>, dim3(shares), dim3(kThreads),
                        (size_t)(p.T * p.k + p.T) * 16 * sizeof(float), stream, p);

@@ -157,6 +157,41 @@ def test_fewer_tokens_than_the_layer(fp8):
     assert layer.forward_few(x[:0]).shape == (0, 256)
 
 
+# up to and beyond the tokens that a workgroup routes for itself, the pairs
+# that one wave tables, and tokens that a chunk's workgroup takes alone
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T,d,E,k,kw", [
+    (8, 192, 70, 8, {}), (13, 64, 70, 5, dict(n_bias=1)), (16, 128, 300, 4, dict(n_bias=2)),
+    (17, 128, 300, 4, dict(n_bias=2)), (64, 4160, 90, 8, dict(n_bias=1)),
+    (50, 256, 600, 3, dict(out=ops.OUT_BF16)), (21, 128, 40, 3, dict(mode=ops.MODE_HASH)),
+    (22, 128, 40, 3, dict(mode=ops.MODE_HASH)), (64, 64, 1000, 8, dict(mode=ops.MODE_HASH))])
+def test_routing_and_parts(T, d, E, k, kw, fp8):
+    layer, w, x, ids, mod = make(T, d, E, k, 128, 64, fp8, T + d, **kw)
+    whole = check(layer, w, x, ids, mod)
+    for t in (1, T - 1):                             # alone and in the batch: the same bits
+        cut = lambda v: None if v is None else v[:t]  # noqa: E731
+        assert torch.equal(layer.forward_few(x[:t], input_ids=cut(ids), modality=cut(mod)),
+                           whole[:t])
+
+
+def test_hash_bad_ids_among_many():
+    T, k = 60, 4
+    layer, w, x, ids, _ = make(T, 128, 30, k, 64, 64, True, 19, mode=ops.MODE_HASH, V=20)
+    table = layer.weights["tid2eid"]
+    table[3] = torch.tensor([4, 9, 4, 9], dtype=torch.int32)
+    table[5] = torch.tensor([1, 2, 30, 0], dtype=torch.int32)
+    ids[7], ids[40], ids[59], ids[11] = 3, -5, 20, 5
+    bad = (ids < 0) | (ids >= 20) | (ids == 5)
+    got = torch.empty((T, k), dtype=torch.int32, device=DEV)
+    wt = torch.empty((T, k), device=DEV)
+    y = layer.forward_few(x, input_ids=ids, ids=got, w=wt)
+    assert bool((got[bad] == -1).all()) and bool((wt[bad] == 0).all())
+    assert torch.equal(got[~bad], table[ids[~bad].long()])
+    assert ops.read_error_flags(layer.flags) == ops.FLAG_BAD_INPUT_ID | ops.FLAG_BAD_EXPERT_ID
+    ref = plain(layer, w, x, got, wt)
+    assert float((y.to(D) - ref).abs().max()) <= 1e-2 * float(ref.pow(2).mean().sqrt())
+
+
 def test_equal_scores_take_the_lower_experts():
     layer, w, x, _, _ = make(4, 128, 70, 5, 64, 0, False, 8)
     layer.weights["w_g"].zero_()
