@@ -181,7 +181,7 @@ def _ptr(t):
 def _stream():
     """Handle of the current device's current stream (the handle alone: a
     torch.cuda.Stream object costs 2.5 us, as much as a kernel launch)."""
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _need(t, dtype, name, dims=None, shape=None):
@@ -199,8 +199,9 @@ def _need(t, dtype, name, dims=None, shape=None):
         raise MoeError(f"{name} must be contiguous")
     if dims is not None and t.dim() != dims:
         raise MoeError(f"{name} must have {dims} dims")
-    if shape is not None and (t.dim() != len(shape) or
-                              any(s is not None and s != n for s, n in zip(shape, t.shape))):
+    # (a tuple of whole sizes is compared at once, 0.5 us a tensor less)
+    if shape is not None and t.shape != shape and (
+            t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape))):
         want = "[" + ", ".join("*" if s is None else str(s) for s in shape) + "]"
         raise MoeError(f"{name} must be {want}, got {list(t.shape)}")
     return t
@@ -558,10 +559,18 @@ def _in_dtype(t, name):
 
 
 def _codes8(t, name, shape):
-    """8-bit codes: uint8 or float8_e4m3fn (the same bytes)."""
-    if t is not None and t.dtype == torch.float8_e4m3fn:
-        return _need(t, torch.float8_e4m3fn, name, shape=shape)
-    return _need(t, torch.uint8, name, shape=shape)
+    """8-bit codes: uint8 or float8_e4m3fn (the same bytes); shape: of any
+    sizes where it is the number of dims."""
+    f8 = t is not None and t.dtype == torch.float8_e4m3fn
+    dt = torch.float8_e4m3fn if f8 else torch.uint8
+    return _need(t, dt, name, shape) if isinstance(shape, int) else _need(t, dt, name, None, shape)
+
+
+def _codes_like(codes, a):
+    """The output for the codes of a (empty_like is the quickest allocation)."""
+    if codes is None:
+        return torch.empty_like(a, dtype=torch.uint8, memory_format=torch.contiguous_format)
+    return _need(codes, torch.uint8, "codes", None, a.shape)
 
 
 def _blocks(n):
@@ -575,7 +584,7 @@ def quantize_fp8_block(a, codes=None, scales=None):
     dt = _in_dtype(a, "a")
     _need(a, a.dtype, "a", 2)
     rows, K = a.shape
-    codes = _out(codes, torch.uint8, "codes", (rows, K), a.device)
+    codes = _codes_like(codes, a)
     scales = _out(scales, torch.float32, "scales", (rows, _blocks(K)), a.device)
     _check(lib().moe_quantize_fp8_block(_ptr(a), dt, rows, K, _ptr(codes), _ptr(scales),
                                         _stream()), "moe_quantize_fp8_block")
@@ -593,7 +602,7 @@ def quantize_weights_fp8_block(w, codes=None, scales=None):
     _need(w, w.dtype, "w")
     shape = tuple(w.shape)
     G, N, K = (1,) + shape if w.dim() == 2 else shape
-    codes = _out(codes, torch.uint8, "codes", shape, w.device)
+    codes = _codes_like(codes, w)
     scales = _out(scales, torch.float32, "scales", shape[:-2] + (_blocks(N), _blocks(K)),
                   w.device)
     _check(lib().moe_quantize_weights_fp8_block(_ptr(w), dt, G, N, K, _ptr(codes), _ptr(scales),
@@ -607,10 +616,12 @@ def grouped_gemm_fp8_block(a8, a_scale, offsets, w8, w_scale, out_dtype=OUT_BF16
     ceil(K / 128)], w8 [G, N, K], w_scale [G, ceil(N / 128), ceil(K / 128)],
     offsets [G + 1] int32.  Codes uint8 or float8_e4m3fn, scales fp32; K, N
     multiples of 16.  Rows outside every group are not written."""
-    _codes8(a8, "a8", (None, None))
+    _codes8(a8, "a8", 2)
     rows, K = a8.shape
-    _codes8(w8, "w8", (None, None, K))
-    G, N, _ = w8.shape
+    _codes8(w8, "w8", 3)
+    G, N, Kw = w8.shape
+    if Kw != K:
+        raise MoeError(f"w8 must be [*, *, {K}], got {[G, N, Kw]}")
     _need(a_scale, torch.float32, "a_scale", shape=(rows, _blocks(K)))
     _need(w_scale, torch.float32, "w_scale", shape=(G, _blocks(N), _blocks(K)))
     _need(offsets, torch.int32, "offsets", shape=(G + 1,))
@@ -630,11 +641,13 @@ def expert_ffn_fp8_block(a8, a_scale, offsets, w_gate, w_up, w_down, clamp_limit
     (codes [G, out, in], scales) pairs as quantize_weights_fp8_block gives
     them.  Returns (h8 uint8 [rows, F], h_scale fp32 [rows, ceil(F / 128)],
     y [rows, d] of out_dtype)."""
-    _codes8(a8, "a8", (None, None))
+    _codes8(a8, "a8", 2)
     rows, d = a8.shape
     (cg, sg), (cu, su), (cd, sd) = w_gate, w_up, w_down
-    _codes8(cg, "w_gate", (None, None, d))
-    G, F, _ = cg.shape
+    _codes8(cg, "w_gate", 3)
+    G, F, dw = cg.shape
+    if dw != d:
+        raise MoeError(f"w_gate must be [*, *, {d}], got {[G, F, dw]}")
     _codes8(cu, "w_up", (G, F, d))
     _codes8(cd, "w_down", (G, d, F))
     bd, bf = _blocks(d), _blocks(F)
