@@ -685,15 +685,14 @@ __device__ __forceinline__ int wave_scan(int x, int lane) {
 // Row tiles of a group of n rows, tiles of up to `blocks` blocks of 32 rows.
 // 4 and 5 are the usual ones: a group of up to 160 rows is one tile (a second
 // one would fetch the group's weights again), a larger one has tiles of up to
-// 128 or 160 rows.  1 to 3 are for few tiles (n < 2^15), where CUs would have
-// none: lower ones use more CUs, and the weights they share come from the L2.
+// 128 or 160 rows.  1 to 3 are for few tiles, where CUs would have none: lower ones use more CUs, and the weights they share come from the L2.
 // 16 groups x 160 rows x 4096 x 256: 64 us with one tile a group, 27 with five
 // (fp32 output; bf16 35 and 18).
 constexpr int kTallest = BM / 32;
 __device__ __forceinline__ int row_tiles(int n, int blocks) {
     const int c = (n + 31) >> 5;
     if (blocks >= 4) return c <= kTallest ? c > 0 : blocks == 4 ? (c + 3) >> 2 : (c + 4) / 5;
-    return blocks == 1 ? c : blocks == 2 ? (c + 1) >> 1 : (c + 2) * 21846 >> 16;  // (c + 2) / 3
+    return blocks == 1 ? c : blocks == 2 ? (c + 1) >> 1 : (c + 2) / 3;
 }
 
 // Persistent grid, one workgroup a CU.  Items are (group, band of kBand
@@ -718,21 +717,17 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_block_kernel(Fp8GemmArgs p)
     const int NT = (p.N + TN - 1) / TN;
     auto clamped = [&](int v) { return min(max(v, 0), rows); };
     const int run = (G + 63) / 64;
-    // the tiles of this lane's run, NT * (x: of up to b1 blocks, y: of b2)
-    auto tiles_of_my_run = [&](int b1, int b2) {
-        int2 sum = {0, 0};
-        for (int i = 0; i < run; ++i) {
-            const int g = lane * run + i;
-            if (g < G) {
-                const int n = max(clamped(p.offsets[g + 1]) - clamped(p.offsets[g]), 0);
-                sum.x += row_tiles(n, b1);
-                sum.y += row_tiles(n, b2);
-            }
+    // the tiles of this lane's run, of up to 1 .. 5 blocks
+    int tiles[kTallest + 1] = {};
+    for (int i = 0; i < run; ++i) {
+        const int g = lane * run + i;
+        if (g < G) {
+            const int n = max(clamped(p.offsets[g + 1]) - clamped(p.offsets[g]), 0);
+#pragma unroll
+            for (int b = 1; b <= kTallest; ++b) tiles[b] += NT * row_tiles(n, b);
         }
-        return int2{NT * sum.x, NT * sum.y};
-    };
-    const int2 usual = tiles_of_my_run(4, kTallest);
-    int blocks = 4, mine = usual.x, upto = wave_scan(mine, lane);
+    }
+    int blocks = 4, mine = tiles[4], upto = wave_scan(mine, lane);
     // Tiles of 160 rows where they save CUs a fifth of their rounds and more
     // (such a tile takes 1.18 to 1.26 times one of 128 with bf16, 1.24 to 1.30
     // with fp32 output).  64 groups of 126 to 3500 rows x 2048 x 1024, three
@@ -744,22 +739,23 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_block_kernel(Fp8GemmArgs p)
         return (int)(((long long)tiles + cus - 1) / cus);
     };
     const int first = rounds(__builtin_amdgcn_readlane(upto, 63));
-    if (first > 1 && __builtin_amdgcn_ballot_w64(usual.x != usual.y)) {
-        const int sum = wave_scan(usual.y, lane);
+    if (first > 1 && __builtin_amdgcn_ballot_w64(tiles[4] != tiles[kTallest])) {
+        const int sum = wave_scan(tiles[kTallest], lane);
         if (rounds(__builtin_amdgcn_readlane(sum, 63)) * 5ll < first * 4ll) {
             blocks = kTallest;
-            mine = usual.y;
+            mine = tiles[kTallest];
             upto = sum;
         }
     }
     // few tiles: the lowest of which every one still has a CU of its own
     if ((long long)rows * NT <= 96ll * gridDim.x &&
         __builtin_amdgcn_readlane(upto, 63) < (int)gridDim.x) {
+#pragma unroll
         for (int b = 1; b <= 3; ++b) {
-            const int lower = tiles_of_my_run(b, b).x, sum = wave_scan(lower, lane);
+            const int sum = wave_scan(tiles[b], lane);
             if (__builtin_amdgcn_readlane(sum, 63) > (int)gridDim.x) continue;
             blocks = b;
-            mine = lower;
+            mine = tiles[b];
             upto = sum;
             break;
         }
