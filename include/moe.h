@@ -536,8 +536,8 @@ size_t moe_forward_workspace_size(const moe_cfg* cfg);
 size_t moe_workspace_size(const moe_cfg* cfg);
 
 /* Reads the device error-flag word (the MOE_FLAG_* bits that moe_route,
- * moe_permute, moe_route_backward and moe_forward OR into *d_flags) into
- * *out after all work queued on `stream` so far has completed.  Unlike every
+ * moe_permute, moe_route_backward, moe_forward and moe_forward_few OR into
+ * *d_flags) into *out after all work queued on `stream` so far has completed.  Unlike every
  * other entry point it synchronises the host with the stream (a checking or
  * test call, not a per-step one).  d_flags is a device uint32; out a host
  * pointer.  MOE_ERR_NULL if either is NULL, MOE_ERR_HIP if the copy or the
@@ -569,8 +569,8 @@ int moe_forward_timed(const moe_cfg* cfg, const moe_weights* w, const uint16_t* 
 /* ------------------------------------------------------------------------
  * Whole layer forward for a few tokens (decoding): the layer of moe_forward
  * for T <= MOE_FEW_MAX_T tokens, on weights as checkpoints hold them, in two
- * or three kernels without a dispatch permutation.  Arguments, limits and outputs as
- * moe_forward, with
+ * or three kernels without a dispatch permutation.  Arguments, limits and
+ * outputs as moe_forward, with
  *   w->packed == 0: bf16 matrices [out, in], or MOE_WEIGHTS_FP8_BLOCK: 8-bit
  *   codes with fp32 scales of 128 x 128 blocks (moe_weights); activations
  *   stay bf16 (x is not quantised, h is rounded to bf16), sums are fp32;

@@ -725,8 +725,11 @@ class MoeLayer:
         self.cw = MoeWeights(packed=self.packed,
                              **{n: _ptr(self.weights.get(n)) for n in WEIGHT_NAMES})
         self.device = self.weights["w_g"].device
-        self.ws_bytes = int(lib().moe_forward_workspace_size(ctypes.byref(self.cfg)))
-        self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
+        # (forward has no path for block-scaled weights, so needs no workspace)
+        self.ws_bytes = 0 if block else int(
+            lib().moe_forward_workspace_size(ctypes.byref(self.cfg)))
+        self.workspace = None if block else torch.empty(self.ws_bytes, dtype=torch.uint8,
+                                                        device=self.device)
         self.flags = torch.zeros(1, dtype=torch.int32, device=self.device)
 
     def backward_weights(self):
