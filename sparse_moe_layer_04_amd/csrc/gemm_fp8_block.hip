@@ -46,9 +46,10 @@
 // reaches 1395 and 2684).  With neither decoding nor scaling the same loop
 // reaches 1379 (100 us; decoding adds 16, scaling 5 to 10) and, without the
 // scaling, 2160 (64 us; scaling adds 9): the vector units run beside the
-// matrix cores, and the clock drops under both.  384 groups x 128 rows x 4096 x 2048: 3.2 GB of weights, 736 us
-// with bf16 output (memory, 4.9 TB/s), 1036 with fp32 (cores and memory in
-// turn).  Ten rows a group: memory, 5.5 TB/s.
+// matrix cores, and the clock drops under both.  384 groups x 128 rows x 4096
+// x 2048: 3.2 GB of weights, 720 to 736 us with bf16 output (memory, 5 TB/s),
+// 0.98 to 1.04 ms with fp32 (cores and memory in turn).  Ten rows a group:
+// memory, 5.5 TB/s.
 #include <type_traits>
 
 #include "fp8_block.h"
@@ -455,15 +456,19 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t, co
             constexpr int h = decltype(st)::value;
             decode(integral_constant<int, (h + 1) & 7>());
             multiply(st);
-            // one product, then its share of the vector instructions
-            constexpr int V = 4 * (MI + NJ) / NT + (h == 0 ? 16 : 0);
+            // one product, then its share of the vector instructions (one or two
+            // products a step do not cover a step's: what is left open there
+            // saves 5%, 12 groups x 1 row x 4096 x 544 25.3 us to 24.0)
+            if constexpr (NT >= 3) {
+                constexpr int V = 4 * (MI + NJ) / NT + (h == 0 ? 16 : 0);
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                __builtin_amdgcn_sched_group_barrier(0x002, h == 0 ? V : 0, 0);
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x002, h == 0 ? 0 : V, 0);
+                for (int i = 0; i < NT; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x002, h == 0 ? V : 0, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, h == 0 ? 0 : V, 0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
-            __builtin_amdgcn_sched_barrier(0);
         };
         using H0 = integral_constant<int, 0>;
         using H1 = integral_constant<int, 1>;
@@ -685,7 +690,8 @@ __device__ __forceinline__ int wave_scan(int x, int lane) {
 // Row tiles of a group of n rows, tiles of up to `blocks` blocks of 32 rows.
 // 4 and 5 are the usual ones: a group of up to 160 rows is one tile (a second
 // one would fetch the group's weights again), a larger one has tiles of up to
-// 128 or 160 rows.  1 to 3 are for few tiles, where CUs would have none: lower ones use more CUs, and the weights they share come from the L2.
+// 128 or 160 rows.  1 to 3 are for few tiles, where CUs would have none: lower
+// ones use more CUs, and the weights they share come from the L2.
 // 16 groups x 160 rows x 4096 x 256: 64 us with one tile a group, 27 with five
 // (fp32 output; bf16 35 and 18).
 constexpr int kTallest = BM / 32;
