@@ -723,17 +723,17 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_block_kernel(Fp8GemmArgs p)
     const int NT = (p.N + TN - 1) / TN;
     auto clamped = [&](int v) { return min(max(v, 0), rows); };
     const int run = (G + 63) / 64;
-    // the tiles of this lane's run, of up to 1 .. 5 blocks
+    // the row tiles of this lane's run, of up to 1 .. 5 blocks
     int tiles[kTallest + 1] = {};
     for (int i = 0; i < run; ++i) {
         const int g = lane * run + i;
         if (g < G) {
             const int n = max(clamped(p.offsets[g + 1]) - clamped(p.offsets[g]), 0);
 #pragma unroll
-            for (int b = 1; b <= kTallest; ++b) tiles[b] += NT * row_tiles(n, b);
+            for (int b = 1; b <= kTallest; ++b) tiles[b] += row_tiles(n, b);
         }
     }
-    int blocks = 4, mine = tiles[4], upto = wave_scan(mine, lane);
+    int blocks = 4, mine = NT * tiles[4], upto = wave_scan(mine, lane);
     // Tiles of 160 rows where they save CUs a fifth of their rounds and more
     // (such a tile takes 1.18 to 1.26 times one of 128 with bf16, 1.24 to 1.30
     // with fp32 output).  64 groups of 126 to 3500 rows x 2048 x 1024, three
@@ -746,10 +746,10 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_block_kernel(Fp8GemmArgs p)
     };
     const int first = rounds(__builtin_amdgcn_readlane(upto, 63));
     if (first > 1 && __builtin_amdgcn_ballot_w64(tiles[4] != tiles[kTallest])) {
-        const int sum = wave_scan(tiles[kTallest], lane);
+        const int sum = wave_scan(NT * tiles[kTallest], lane);
         if (rounds(__builtin_amdgcn_readlane(sum, 63)) * 5ll < first * 4ll) {
             blocks = kTallest;
-            mine = tiles[kTallest];
+            mine = NT * tiles[kTallest];
             upto = sum;
         }
     }
@@ -758,10 +758,10 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_block_kernel(Fp8GemmArgs p)
         __builtin_amdgcn_readlane(upto, 63) < (int)gridDim.x) {
 #pragma unroll
         for (int b = 1; b <= 3; ++b) {
-            const int sum = wave_scan(tiles[b], lane);
+            const int sum = wave_scan(NT * tiles[b], lane);
             if (__builtin_amdgcn_readlane(sum, 63) > (int)gridDim.x) continue;
             blocks = b;
-            mine = tiles[b];
+            mine = NT * tiles[b];
             upto = sum;
             break;
         }
