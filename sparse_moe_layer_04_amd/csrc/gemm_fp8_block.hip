@@ -277,7 +277,10 @@ __device__ __forceinline__ void run_five(const Fetch<EPI>& f, unsigned char* rin
             slot = next;
         }
     } else {
-        // product L = 5 s + i: half s of the block, rows' operands two ahead
+        // product L = 5 s + i: half s of the block, rows' operands two ahead;
+        // beside product TURN the last of them, then the barrier that gives the
+        // block's slot away
+        constexpr int TURN = 2 * MI - 3;
         u32x4 rw[2][2], ra[2][2];
         auto read2 = [&](u32x4 (&r)[2], int at, int s, int i) {
             r[0] = read(at, 2 * s, i);
@@ -304,13 +307,16 @@ __device__ __forceinline__ void run_five(const Fetch<EPI>& f, unsigned char* rin
                     cat(rw[s]), cat(ra[L & 1]), s == 0 ? zero : part[i][0], 0, 0, 0, 127, 0, 127);
                 if constexpr (kEarly + L < 8)
                     f.template copies<3, kEarly + L, kEarly + L + 1>(j + 2, S, past, last);
-                if constexpr (L == 2 * MI - 3) {
+                static_assert(L2 < 2 ? L >= TURN : L <= TURN,
+                              "the block's reads before the barrier, the next one's after it");
+                if constexpr (L2 >= 2) read2(ra[L & 1], rda + slot, L2 / MI, L2 % MI);
+                if constexpr (L == TURN) {
                     turn();
                     read2(rw[0], rdw + next, 0, 0);
                 }
-                read2(ra[L & 1], rda + (L2 < 2 ? next : slot), L2 / MI, L2 % MI);
-                if constexpr (L >= 2 * MI - 3)
-                    f.template copies<3, L - (2 * MI - 3), L - (2 * MI - 3) + 1>(j + 3, S, past, slot);
+                if constexpr (L2 < 2) read2(ra[L & 1], rda + next, L2 / MI, L2 % MI);
+                if constexpr (L >= TURN)
+                    f.template copies<3, L - TURN, L - TURN + 1>(j + 3, S, past, slot);
                 __builtin_amdgcn_sched_barrier(0);
             });
             slot = next;

@@ -255,6 +255,16 @@ def test_grouped_gemm_bands(counts, out):
     test_grouped_gemm(counts, 144, 2320, out)
 
 
+# The same tiles over several turns of the ring of three blocks of K (9 and 17
+# blocks, the last one short), so that every height refills the slots that its
+# waves have read.
+@pytest.mark.parametrize("out", [ops.OUT_F32, ops.OUT_BF16])
+@pytest.mark.parametrize("K", [1040, 2064])
+@pytest.mark.parametrize("counts", HEIGHTS + [[12123], [1100, 0, 3001, 160, 161]])
+def test_grouped_gemm_turns_of_the_ring(counts, K, out):
+    test_grouped_gemm(counts, K, 2320, out)
+
+
 def test_grouped_gemm_codes_as_float8():
     a, sa, od, offs, w, sw = operands(2, [9, 40], 256, 128, 5)
     f8 = torch.float8_e4m3fn
@@ -383,6 +393,11 @@ def test_expert_ffn_tile_heights(counts):
 
 def test_expert_ffn_bands():
     test_expert_ffn([1100, 161, 6001], 144, 1168, 0, 10.0, ops.OUT_BF16)
+
+
+@pytest.mark.parametrize("counts", HEIGHTS + [[1100, 161, 3001]])
+def test_expert_ffn_turns_of_the_ring(counts):
+    test_expert_ffn(counts, 1040, 1168, 0, 10.0, ops.OUT_BF16)
 
 
 def test_expert_ffn_rows_outside_groups_untouched():
