@@ -265,6 +265,71 @@ def test_grouped_gemm_turns_of_the_ring(counts, K, out):
     test_grouped_gemm(counts, K, 2320, out)
 
 
+@pytest.mark.parametrize("out", [ops.OUT_F32, ops.OUT_BF16])
+@pytest.mark.parametrize("counts,N", [([40], 272), (HEIGHTS[0], 2320), (HEIGHTS[1], 2320),
+                                      (HEIGHTS[2], 2320), (HEIGHTS[3], 2320)])
+def test_grouped_gemm_scales_whose_product_is_no_normal_number(counts, N, out):
+    """Scales of 2^-126 and 2^115 under weight scales near 2^-14 and 2^15: some
+    products of two scales are subnormal and some infinite, the outputs are
+    neither.  Rows of zeros under any finite scales give zeros.  Bounds as in
+    check_product, with the rounding of subnormal sums (2^-149 an addition;
+    bf16: 2^-134, half a step) in the place of a fixed slack."""
+    K = 272
+    a, sa, od, offs, w, sw = operands(len(counts), counts, K, N, N + len(counts))
+    kind = torch.arange(a.shape[0], device=DEV) % 4
+    sa[kind == 0] = 2.0 ** -126
+    sa[kind == 2] = 2.0 ** 115
+    sa[kind == 3] = 2.0 ** 120
+    a[kind == 2] = a[kind == 2] % 4                # codes of 0 to 3 * 2^-9
+    a[kind == 3] = 0
+    big = torch.arange(N, device=DEV) // 128 % 2 == 1
+    w[:, big] = w[:, big] % 4
+    sw[:, 0::2] = sw[:, 0::2] * 2.0 ** -7          # (between 2^-17 and 2^-13)
+    sw[:, 1::2] = sw[:, 1::2] * 2.0 ** 21          # (2^11 to 2^15)
+    y = ops.grouped_gemm_fp8_block(a, sa, od, w, sw, out_dtype=out).to(D)
+    assert bool((y[kind == 3] == 0).all())
+    s = sa.max(1)[0][:, None] * sw.amax((0, 2))
+    assert bool((s[kind == 2] == float("inf")).any()) and bool((s[kind == 0] < 2.0 ** -126).any())
+    for g in range(len(counts)):
+        lo, hi = int(offs[g]), int(offs[g + 1])
+        if lo == hi:
+            continue
+        x, v = values(a[lo:hi], sa[lo:hi]), matrix_values(w[g], sw[g])
+        ref, mag = x @ v.t(), x.abs() @ v.abs().t()
+        assert float(ref.abs().max()) < 2.0 ** 127
+        bound = 2 * (K + 4 * blocks(K)) * 2.0 ** -24 * mag + 2 * blocks(K) * 2.0 ** -149
+        if out == ops.OUT_BF16:
+            bound = 2.0 ** -8 * ref.abs() + 2.0 ** -11 * mag + 2.0 ** -134
+        assert bool(((y[lo:hi] - ref).abs() <= bound).all()), g
+
+
+def test_expert_ffn_scales_whose_product_is_no_normal_number():
+    """Gate sums near 2^-124, from scales whose product is subnormal, times up
+    sums near 1: h near 2^-125, its codes the plain ones or their neighbours.
+    A row of zeros under scales whose product is infinite gives zeros."""
+    d, F, rows = 272, 144, 33
+    g = gen(31)
+    a8 = random_codes((rows, d), g)
+    sa = torch.full((rows, blocks(d)), 2.0 ** -126, device=DEV)
+    a8[7], sa[7] = 0, 2.0 ** 120
+    od = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+    wg, wu = random_codes((1, F, d), g), random_codes((1, F, d), g)
+    sg = torch.full((1, blocks(F), blocks(d)), 1.3 * 2.0 ** -14, device=DEV)
+    su = torch.full((1, blocks(F), blocks(d)), 1.2 * 2.0 ** 110, device=DEV)
+    wd = ops.quantize_weights_fp8_block(torch.randn((1, d, F), generator=g, device=DEV))
+    h8, hs, y = ops.expert_ffn_fp8_block(a8, sa, od, (wg, sg), (wu, su), wd)
+    x = values(a8, sa)
+    gv, uv = x @ matrix_values(wg[0], sg[0]).t(), x @ matrix_values(wu[0], su[0]).t()
+    h = gv / (1 + torch.exp(-gv)) * uv.clamp(-10, 10)
+    codes, scales = plain_rows(h.cpu().numpy())
+    assert np.array_equal(hs.cpu().numpy(), scales)
+    v = h8.view(torch.float8_e4m3fn).double().cpu().numpy()
+    ref = torch.from_numpy(codes).view(torch.float8_e4m3fn).double().numpy()
+    assert np.abs(ref).max() > 1
+    assert np.all(np.abs(v - ref) <= np.maximum(np.abs(ref) * 2.0 ** -3, 2.0 ** -9))
+    assert bool((h8[7] & 0x7f == 0).all()) and bool((y[7] == 0).all())
+
+
 def test_grouped_gemm_codes_as_float8():
     a, sa, od, offs, w, sw = operands(2, [9, 40], 256, 128, 5)
     f8 = torch.float8_e4m3fn
