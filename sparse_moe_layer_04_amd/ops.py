@@ -682,7 +682,6 @@ class MoeLayer:
         self.weights = dict(weights)
         self.plain = dict(weights)     # the [out, in] matrices (for the backward's layouts)
         self.bw = None
-        self.few_ws = None             # forward_few's workspace, made at its first call
         block = packed == "fp8_block"
         _need(self.weights["w_g"], torch.bfloat16, "w_g", shape=(E, d))
         shapes = dict(w_gate=(E, F, d), w_up=(E, F, d), w_down=(E, d, F))
@@ -731,6 +730,25 @@ class MoeLayer:
         self.workspace = None if block else torch.empty(self.ws_bytes, dtype=torch.uint8,
                                                         device=self.device)
         self.flags = torch.zeros(1, dtype=torch.int32, device=self.device)
+        # forward_few: a config a token count, not changed once it is made (the
+        # library reads it while other threads run), and a workspace
+        self.few_cfgs = {}
+        few = self.packed in (0, WEIGHTS_FP8_BLOCK)
+        self.few_ws = self.few_workspace() if few else None
+
+    def _few_cfg(self, T):
+        cfg = self.few_cfgs.get(T)
+        if cfg is None:
+            cfg = MoeCfg.from_buffer_copy(self.cfg)
+            cfg.T = T
+            self.few_cfgs[T] = cfg
+        return cfg
+
+    def few_workspace(self):
+        """A workspace for forward_few's calls of this layer (uint8)."""
+        size = lib().moe_forward_few_workspace_size(
+            ctypes.byref(self._few_cfg(min(self.cfg.T, FEW_MAX_T))))
+        return torch.empty(int(size), dtype=torch.uint8, device=self.device)
 
     def backward_weights(self):
         """The weights in the layouts of the backward's input-gradient
@@ -833,15 +851,10 @@ class MoeLayer:
         _opt(w, torch.float32, "w", shape=(T, c.k))
         dt = torch.float32 if c.out_dtype == OUT_F32 else torch.bfloat16
         y = _out(y, dt, "y", (T, c.d), x.device)
-        if self.few_ws is None:
-            self.few_cfg = MoeCfg.from_buffer_copy(c)
-            self.few_cfg.T = min(c.T, FEW_MAX_T)
-            self.few_ws_bytes = int(lib().moe_forward_few_workspace_size(
-                ctypes.byref(self.few_cfg)))
-            self.few_ws = torch.empty(self.few_ws_bytes, dtype=torch.uint8, device=self.device)
-        self.few_cfg.T = T
-        _check(lib().moe_forward_few(ctypes.byref(self.few_cfg), ctypes.byref(self.cw), _ptr(x),
-                                     _ptr(input_ids), _ptr(modality), _ptr(y), _ptr(logits),
-                                     _ptr(ids), _ptr(w), _ptr(self.flags), _ptr(self.few_ws),
-                                     self.few_ws_bytes, _stream()), "moe_forward_few")
+        ws = self.few_ws
+        _check(lib().moe_forward_few(ctypes.byref(self._few_cfg(T)), ctypes.byref(self.cw),
+                                     _ptr(x), _ptr(input_ids), _ptr(modality), _ptr(y),
+                                     _ptr(logits), _ptr(ids), _ptr(w), _ptr(self.flags), _ptr(ws),
+                                     0 if ws is None else ws.numel(), _stream()),
+               "moe_forward_few")
         return y

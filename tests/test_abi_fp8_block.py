@@ -1,6 +1,7 @@
 """Argument checks of the 128-block 8-bit entry points and of the few-token
 forward: every case returns on the host before the first HIP call."""
 import ctypes
+import threading
 
 import pytest
 import torch
@@ -195,3 +196,52 @@ def test_binding_refuses_host_and_mistyped_tensors():
         ops.grouped_gemm_fp8_block(c, a, a, c, a)
     with pytest.raises(ops.MoeError, match="device tensor"):
         ops.expert_ffn_fp8_block(c, a, a, (c, a), (c, a), (c, a))
+
+
+class OneCall:
+    """The library with moe_forward_few replaced: keeps the arguments, and runs
+    `meanwhile` once before it reads the config, as another thread may while
+    the library is entered without the interpreter's lock."""
+
+    def __init__(self, L):
+        self.lib, self.meanwhile, self.calls = L, None, []
+
+    def __getattr__(self, name):
+        return getattr(self.lib, name)
+
+    def moe_forward_few(self, cfg, weights, x, *args):
+        run, self.meanwhile = self.meanwhile, None
+        if run:
+            run()
+        self.calls.append((cfg._obj.T, x, args[-3], args[-2]))
+        return 0
+
+
+def few_layer(monkeypatch, L, T=33, **kw):
+    fake = OneCall(L)
+    monkeypatch.setattr(ops, "lib", lambda: fake)
+    monkeypatch.setattr(ops, "_need", lambda t, *a, **k: t)
+    monkeypatch.setattr(ops, "_stream", lambda: 0)
+    shapes = dict(w_g=(8, 128), w_gate=(8, 64, 128), w_up=(8, 64, 128), w_down=(8, 128, 64))
+    w = {n: torch.zeros(s, dtype=torch.bfloat16) for n, s in shapes.items()}
+    return fake, ops.MoeLayer(T, 128, 8, 2, 64, 0, w, **kw)
+
+
+def test_forward_few_counts_of_two_threads(L, monkeypatch):
+    """Each call's token count is its own, whatever other threads' calls of the
+    same layer do before the library reads it."""
+    fake, layer = few_layer(monkeypatch, L)
+    rows = {t: torch.zeros((t, 128), dtype=torch.bfloat16) for t in (1, 33)}
+
+    def other():
+        th = threading.Thread(target=layer.forward_few, args=(rows[33],))
+        th.start()
+        th.join()
+    fake.meanwhile = other
+    layer.forward_few(rows[1])
+    assert [c[0] for c in fake.calls] == [33, 1]
+    assert [c[1] for c in fake.calls] == [rows[33].data_ptr(), rows[1].data_ptr()]
+    # one workspace, there from the start and large enough for both
+    assert len({c[2] for c in fake.calls}) == 1 and fake.calls[0][2] == layer.few_ws.data_ptr()
+    assert fake.calls[0][3] >= L.moe_forward_few_workspace_size(
+        ctypes.byref(few_cfg(T=33, F_shared=0)))
