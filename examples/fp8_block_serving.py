@@ -59,19 +59,21 @@ def prefill(layer, x, input_ids=None, modality=None):
 
 
 class Decoder:
-    """forward_few on a fixed number of tokens, captured into a HIP graph."""
+    """forward_few on a fixed number of tokens, captured into a HIP graph, with
+    a workspace of its own (decoders of one layer may run at once)."""
 
     def __init__(self, layer, tokens=1, input_ids=None, modality=None):
         dt = torch.float32 if layer.cfg.out_dtype == ops.OUT_F32 else torch.bfloat16
         self.x = torch.zeros((tokens, layer.cfg.d), dtype=torch.bfloat16, device=layer.device)
         self.y = torch.empty((tokens, layer.cfg.d), dtype=dt, device=layer.device)
         self.ids = torch.empty((tokens, layer.cfg.k), dtype=torch.int32, device=layer.device)
+        self.ws = layer.few_workspace()
         run = lambda: layer.forward_few(self.x, input_ids, modality, y=self.y,  # noqa: E731
-                                        ids=self.ids)
+                                        ids=self.ids, ws=self.ws)
         stream = torch.cuda.Stream(layer.device)
         stream.wait_stream(torch.cuda.current_stream(layer.device))
         with torch.cuda.stream(stream):
-            run()                                  # (makes the workspace)
+            run()                                  # (kernels loaded)
         torch.cuda.current_stream(layer.device).wait_stream(stream)
         self.graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(self.graph, stream=stream):

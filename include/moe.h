@@ -74,8 +74,11 @@ extern "C" {
 
 #define MOE_FLAG_BAD_INPUT_ID 1u  /* an input id outside [0, V) */
 #define MOE_FLAG_BAD_EXPERT_ID 2u /* an expert id outside [0, E) */
-#define MOE_FLAG_OVERLAP 4u       /* moe_forward_few: another call used the
-                                     workspace at the same time */
+#define MOE_FLAG_OVERLAP 4u       /* moe_forward_few: a call gave up waiting for
+                                     its own work after some seconds, because
+                                     another one cleared their workspace
+                                     meanwhile; y is wrong.  (Most overlaps
+                                     give a wrong y and no flag.) */
 
 /* Limits: 1 <= k <= 8, k <= E, 1 <= E <= 1024 (route/permute/forward);
  * d, F multiples of 64 (expert FFN, forward); T * k < 2^31; G <= 4096.
@@ -580,7 +583,9 @@ int moe_forward_timed(const moe_cfg* cfg, const moe_weights* w, const uint16_t* 
  * computes (and writes to logits_out).  A hash-routed token whose id or
  * experts are out of range gets ids -1, weights 0 and the shared expert's
  * output alone.  ws: moe_forward_few_workspace_size(cfg) bytes (0 for an
- * invalid cfg), 256-byte aligned; nothing in it needs to start at zero.
+ * invalid cfg), 256-byte aligned; nothing in it needs to start at zero.  It
+ * serves one call at a time: calls that may run at once, on several streams or
+ * in replays of several graphs, need one each (see MOE_FLAG_OVERLAP).
  */
 #define MOE_FEW_MAX_T 64
 size_t moe_forward_few_workspace_size(const moe_cfg* cfg);

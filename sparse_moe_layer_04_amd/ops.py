@@ -745,7 +745,8 @@ class MoeLayer:
         return cfg
 
     def few_workspace(self):
-        """A workspace for forward_few's calls of this layer (uint8)."""
+        """A workspace for forward_few's calls of this layer (uint8), for
+        callers whose calls overlap in time."""
         size = lib().moe_forward_few_workspace_size(
             ctypes.byref(self._few_cfg(min(self.cfg.T, FEW_MAX_T))))
         return torch.empty(int(size), dtype=torch.uint8, device=self.device)
@@ -834,11 +835,14 @@ class MoeLayer:
         return y
 
     def forward_few(self, x, input_ids=None, modality=None, y=None, logits=None, ids=None,
-                    w=None):
+                    w=None, ws=None):
         """The layer forward for a few tokens (decoding), one C-ABI call
         (moe_forward_few): x [t, d] with t up to the layer's T and at most
         FEW_MAX_T.  Takes plain bf16 weights (packed=False) or 8-bit ones with
-        block scales (packed="fp8_block")."""
+        block scales (packed="fp8_block").  ws: a workspace of few_workspace();
+        None: the layer's own.  A workspace serves one call at a time: calls
+        that may run at once (on several streams, or replays of several
+        graphs) need one each, or give wrong results."""
         c = self.cfg
         _need(x, torch.bfloat16, "x", shape=(None, c.d))
         T = x.shape[0]
@@ -851,7 +855,10 @@ class MoeLayer:
         _opt(w, torch.float32, "w", shape=(T, c.k))
         dt = torch.float32 if c.out_dtype == OUT_F32 else torch.bfloat16
         y = _out(y, dt, "y", (T, c.d), x.device)
-        ws = self.few_ws
+        if ws is None:
+            ws = self.few_ws
+        else:
+            _need(ws, torch.uint8, "ws", 1)
         _check(lib().moe_forward_few(ctypes.byref(self._few_cfg(T)), ctypes.byref(self.cw),
                                      _ptr(x), _ptr(input_ids), _ptr(modality), _ptr(y),
                                      _ptr(logits), _ptr(ids), _ptr(w), _ptr(self.flags), _ptr(ws),

@@ -245,3 +245,21 @@ def test_forward_few_counts_of_two_threads(L, monkeypatch):
     assert len({c[2] for c in fake.calls}) == 1 and fake.calls[0][2] == layer.few_ws.data_ptr()
     assert fake.calls[0][3] >= L.moe_forward_few_workspace_size(
         ctypes.byref(few_cfg(T=33, F_shared=0)))
+
+
+def test_forward_few_on_a_workspace_of_the_callers(L, monkeypatch):
+    fake, layer = few_layer(monkeypatch, L)
+    own = layer.few_workspace()
+    layer.forward_few(torch.zeros((2, 128), dtype=torch.bfloat16), ws=own)
+    assert fake.calls[0][2:] == (own.data_ptr(), own.numel())
+    assert own.data_ptr() != layer.few_ws.data_ptr() and own.numel() == layer.few_ws.numel()
+
+
+def test_forward_few_refuses_other_workspaces(L, monkeypatch):
+    need = ops._need
+    _, layer = few_layer(monkeypatch, L)
+    x = torch.zeros((2, 128), dtype=torch.bfloat16)
+    monkeypatch.setattr(ops, "_need", lambda t, dt, name, *a, **k:
+                        need(t, dt, name, *a, **k) if name == "ws" else t)
+    with pytest.raises(ops.MoeError, match="ws must be a device tensor"):
+        layer.forward_few(x, ws=torch.empty(layer.few_ws.numel(), dtype=torch.uint8))

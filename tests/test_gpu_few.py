@@ -311,3 +311,37 @@ def test_other_stream_and_graph(fp8):
         torch.cuda.synchronize()
         assert torch.equal(y, layer.forward_few(x))
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_calls_at_once_on_workspaces_of_their_own(fp8):
+    """Two graphs of one layer, each with its own workspace, replayed on two
+    streams beside each other, and an eager call on the layer's own beside
+    both."""
+    layer, w, x, _, _ = make(24, 512, 64, 6, 320, 256, fp8, 23)
+    parts = [x[:5].clone(), x[5:].clone(), x[2:20].clone()]
+    want = [layer.forward_few(p) for p in parts]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ws = [layer.few_workspace() for _ in range(2)]
+    ys = [torch.empty_like(v) for v in want]
+    graphs = []
+    torch.cuda.synchronize()
+    for i, s in enumerate(streams):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            for _ in range(8):
+                layer.forward_few(parts[i], y=ys[i], ws=ws[i])
+        graphs.append(graph)
+    for _ in range(4):
+        for y in ys:
+            y.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        for _ in range(8):
+            layer.forward_few(parts[2], y=ys[2])
+        torch.cuda.synchronize()
+        for y, v in zip(ys, want):
+            assert torch.equal(y, v)
+    assert ops.read_error_flags(layer.flags) == 0
