@@ -10,7 +10,6 @@ namespace {
 inline bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 inline int hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
-inline long long blocks(long long n) { return (n + 127) / 128; }
 
 // side of a matrix of the 8-bit products (a 256-row tile of codes stays
 // within 32-bit offsets)
@@ -30,7 +29,7 @@ int gemm_shape_checks(int G, int rows, int K, int N) {
     if ((long long)rows * K >= (1ll << 40) || (long long)rows * N >= (1ll << 40))
         return MOE_ERR_SHAPE;
     // items of the tile loop: 32-bit
-    if (((long long)rows / 128 + G) * blocks(N) >= (1ll << 31)) return MOE_ERR_SHAPE;
+    if (((long long)rows / 128 + G) * block_count(N) >= (1ll << 31)) return MOE_ERR_SHAPE;
     return MOE_OK;
 }
 
@@ -40,7 +39,7 @@ extern "C" {
 
 int moe_quantize_fp8_block(const void* a, int in_dtype, long long rows, int K, uint8_t* codes,
                            float* scales, void* stream) {
-    if (rows < 0 || K < 1 || rows > (1ll << 31) || rows * blocks(K) >= (1ll << 31))
+    if (rows < 0 || K < 1 || rows > (1ll << 31) || rows * block_count(K) >= (1ll << 31))
         return MOE_ERR_SHAPE;
     if (K % 16) return MOE_ERR_UNSUPPORTED;
     if (rows == 0) return MOE_OK;
@@ -53,7 +52,7 @@ int moe_quantize_fp8_block(const void* a, int in_dtype, long long rows, int K, u
 int moe_quantize_weights_fp8_block(const void* w, int in_dtype, int G, int N, int K,
                                    uint8_t* codes, float* scales, void* stream) {
     if (G < 1 || N < 1 || K < 1) return MOE_ERR_SHAPE;
-    if (blocks(N) * blocks(K) >= (1ll << 31) || G * (blocks(N) * blocks(K)) >= (1ll << 31))
+    if (block_count(N) * block_count(K) >= (1ll << 31) || G * (block_count(N) * block_count(K)) >= (1ll << 31))
         return MOE_ERR_SHAPE;
     if (K % 16) return MOE_ERR_UNSUPPORTED;
     const int st = quant_checks(w, in_dtype, codes, scales);

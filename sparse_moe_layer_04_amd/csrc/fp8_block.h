@@ -5,6 +5,10 @@
 
 namespace moe {
 
+// blocks of 128 along a side of n (64-bit: n + 127 passes 2^31 for the longest)
+__host__ __device__ constexpr long long block_count(long long n) { return (n + 127) / 128; }
+static_assert(block_count(0x7fffffff) == 1ll << 24, "the longest side");
+
 // 2^X for X in [-126, 127]
 __device__ __forceinline__ float pow2(int X) { return __uint_as_float((uint32_t)(X + 127) << 23); }
 

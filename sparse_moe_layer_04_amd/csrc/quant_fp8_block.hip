@@ -153,7 +153,7 @@ __global__ __launch_bounds__(256) void quant_matrix_kernel(const void* __restric
 
 hipError_t launch_quant_rows_fp8_block(const void* a, int in_dtype, long long rows, int K,
                                        uint8_t* codes, float* scales, hipStream_t stream) {
-    const int nb = (K + 127) / 128;
+    const int nb = (int)block_count(K);
     const unsigned nblocks = (unsigned)(rows * nb);
     if (nblocks == 0) return hipSuccess;
     const unsigned per = (in_dtype == MOE_IN_F32 ? 8u : 16u) * kU;
@@ -169,7 +169,7 @@ hipError_t launch_quant_rows_fp8_block(const void* a, int in_dtype, long long ro
 
 hipError_t launch_quant_matrix_fp8_block(const void* w, int in_dtype, int G, int N, int K,
                                          uint8_t* codes, float* scales, hipStream_t stream) {
-    const int nbn = (N + 127) / 128, nbk = (K + 127) / 128;
+    const int nbn = (int)block_count(N), nbk = (int)block_count(K);
     const unsigned nblocks = (unsigned)((long long)G * nbn * nbk);
     const dim3 grid = grid_of(nblocks);
     if (in_dtype == MOE_IN_F32)

@@ -188,6 +188,25 @@ def test_quantize_more_matrices_than_one_grid_row():
         assert torch.equal(codes[lo:lo + (1 << 22)], v.to(torch.float8_e4m3fn).view(torch.uint8))
 
 
+@pytest.mark.parametrize("matrix", [False, True])
+def test_quantize_the_longest_row(matrix):
+    """2^31 - 16 values, whose number of blocks, 2^24, is the largest of a
+    side: the same codes and scales as of rows of one block each."""
+    K, whole = (1 << 31) - 16, (1 << 24) - 1
+    v = torch.randn((1, K), generator=gen(41), device=DEV, dtype=torch.bfloat16)
+    v[0, -1] = 300.0
+    quantize = ops.quantize_weights_fp8_block if matrix else ops.quantize_fp8_block
+    codes, scales = quantize(v)
+    assert codes.shape == (1, K) and scales.shape == (1, whole + 1)
+    for lo in range(0, whole, 1 << 22):
+        hi = min(lo + (1 << 22), whole)
+        c, s = ops.quantize_fp8_block(v[0, 128 * lo:128 * hi].view(-1, 128))
+        assert torch.equal(c.view(-1), codes[0, 128 * lo:128 * hi])
+        assert torch.equal(s.view(-1), scales[0, lo:hi])
+    c, s = ops.quantize_fp8_block(v[:, 128 * whole:])
+    assert torch.equal(c, codes[:, 128 * whole:]) and torch.equal(s[0], scales[0, whole:])
+
+
 def test_quantize_nothing():
     codes, scales = ops.quantize_fp8_block(torch.empty((0, 256), device=DEV))
     assert codes.shape == (0, 256) and scales.shape == (0, 2)
