@@ -615,7 +615,10 @@ def grouped_gemm_fp8_block(a8, a_scale, offsets, w8, w_scale, out_dtype=OUT_BF16
     block scales (moe_grouped_gemm_fp8_block): a8 [rows, K], a_scale [rows,
     ceil(K / 128)], w8 [G, N, K], w_scale [G, ceil(N / 128), ceil(K / 128)],
     offsets [G + 1] int32.  Codes uint8 or float8_e4m3fn, scales fp32; K, N
-    multiples of 16.  Rows outside every group are not written."""
+    multiples of 16.  Rows outside every group are not written.  Products are
+    exact with an fp32 output; with a bf16 one the 8-bit matrix cores drop what
+    lies 13 binary places below the largest of eight neighbouring products (see
+    moe.h)."""
     _codes8(a8, "a8", 2)
     rows, K = a8.shape
     _codes8(w8, "w8", 3)

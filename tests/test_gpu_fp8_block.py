@@ -379,6 +379,64 @@ def test_grouped_gemm_all_codes_exactly():
         assert bool((y[:, n:] == 0).all())
 
 
+def test_grouped_gemm_what_a_bf16_output_drops():
+    """2^16 - 2^16 + q: within eight neighbouring k the 8-bit matrix cores keep
+    a power of two q down to 2^(16 - 13), beside other eights down to 2^-6 at
+    least; the fp32 output's products keep what an fp32 sum holds, anywhere."""
+    def run(at, exponents, out):
+        n = len(exponents)
+        a = torch.zeros((n, 128), device=DEV)
+        w = torch.zeros((48, 128), device=DEV)
+        for r, e in enumerate(exponents):
+            high = max(min(e // 2, 8), -6)
+            a[r, 0], a[r, 1], a[r, at] = 256.0, -256.0, 2.0 ** high
+            w[r, 0] = w[r, 1] = 256.0
+            w[r, at] = 2.0 ** (e - high)
+        codes = lambda v: v.to(torch.float8_e4m3fn).view(torch.uint8)  # noqa: E731
+        off = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+        y = ops.grouped_gemm_fp8_block(codes(a), torch.ones((n, 1), device=DEV), off,
+                                       codes(w)[None], torch.ones((1, 1, 1), device=DEV),
+                                       out_dtype=out)
+        want = torch.tensor([2.0 ** e for e in exponents], device=DEV)
+        got = y.float().diagonal()[:n]
+        held = want >= 2.0 ** -7                       # (the 24 bits of an fp32 sum at 2^16)
+        assert torch.equal(got[held], want[held]), (at, got)
+        assert bool(((got - want).abs() <= 2.0 ** -7).all())
+    for at in (2, 7):
+        run(at, range(3, 17), ops.OUT_BF16)
+        run(at, range(-12, 17), ops.OUT_F32)
+    for at in (8, 16, 40, 64, 127):
+        run(at, range(-6, 17), ops.OUT_BF16)
+        run(at, range(-12, 17), ops.OUT_F32)
+
+
+@pytest.mark.parametrize("out", [ops.OUT_F32, ops.OUT_BF16])
+@pytest.mark.parametrize("sign", [False, True])
+def test_grouped_gemm_outliers(sign, out):
+    """One large value in every eight of K beside small ones: the bound of the
+    worst case, 7 * 2^-13 of the sum of the magnitudes truncated (and the fp32
+    sums and the output's rounding), where the small products are all of one
+    sign and where they are not."""
+    a, sa, od, offs, w, sw = operands(2, [70, 41], 272, 272, 51)
+    for v in (a, w):
+        v &= 0xff if sign else 0x7f
+        v[..., 0::8] |= 0x78                           # 256 and more
+        v[..., 0::8] &= 0xfd if sign else 0x7d         # (no NaN)
+        for i in range(1, 8):
+            v[..., i::8] &= 0xbf if sign else 0x3f     # below 2
+    y = ops.grouped_gemm_fp8_block(a, sa, od, w, sw, out_dtype=out)
+    assert bool(torch.isfinite(y).all())
+    K = a.shape[1]
+    for g in range(2):
+        lo, hi = int(offs[g]), int(offs[g + 1])
+        x, v = values(a[lo:hi], sa[lo:hi]), matrix_values(w[g], sw[g])
+        ref, mag = x @ v.t(), x.abs() @ v.abs().t()
+        bound = 2 * (K + 4 * blocks(K)) * 2.0 ** -24 * mag
+        if out == ops.OUT_BF16:
+            bound = bound + 2.0 ** -8 * ref.abs() + 7 * 2.0 ** -13 * mag
+        assert bool(((y[lo:hi].to(D) - ref).abs() <= bound).all())
+
+
 def test_grouped_gemm_nan_stays_in_its_row():
     a, sa, od, offs, w, sw = operands(1, [40], 272, 64, 9)
     clean = ops.grouped_gemm_fp8_block(a, sa, od, w, sw, out_dtype=ops.OUT_F32)
