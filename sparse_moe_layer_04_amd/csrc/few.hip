@@ -437,15 +437,6 @@ __device__ __forceinline__ void route_batch(const FewArgs& p, const Lane& l, Tab
     }
 }
 
-__device__ __forceinline__ int wave_scan(int x, int lane) {   // inclusive
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const int y = __shfl_up(x, off, 64);
-        if (lane >= off) x += y;
-    }
-    return x;
-}
-
 // The table of up to 64 pairs, by one wave: ballots of the ids' bits give each
 // pair the set of its expert's pairs.  (One token of the 64-expert layer takes
 // 1 us less than with the masks in LDS and their barriers.)

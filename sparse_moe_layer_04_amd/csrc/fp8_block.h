@@ -67,6 +67,16 @@ __device__ __forceinline__ float row16_max(float v) {
     return v;
 }
 
+// Inclusive sum over the wave's lanes
+__device__ __forceinline__ int wave_scan(int x, int lane) {
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int y = __shfl_up(x, off, 64);
+        if (lane >= off) x += y;
+    }
+    return x;
+}
+
 // silu(clamp(g)) * clamp(u), the expert FFN's activation (comparisons, so
 // that a NaN passes the clamps)
 __device__ __forceinline__ float clamped_swiglu(float g, float u, float L, int mode) {

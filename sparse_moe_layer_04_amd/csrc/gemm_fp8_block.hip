@@ -717,16 +717,6 @@ __device__ __forceinline__ int scalar_load(const int32_t* p) {
     return v;
 }
 
-// Inclusive sum over the wave's lanes
-__device__ __forceinline__ int wave_scan(int x, int lane) {
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const int y = __shfl_up(x, off, 64);
-        if (lane >= off) x += y;
-    }
-    return x;
-}
-
 // Row tiles of a group of n rows, tiles of up to `blocks` blocks of 32 rows.
 // 4 and 5 are the usual ones: a group of up to 160 rows is one tile (a second
 // one would fetch the group's weights again), a larger one has tiles of up to
