@@ -386,6 +386,142 @@ int moe_expert_ffn_fp8_block(const uint8_t* a8, const float* a_scale, const int3
                              uint8_t* h8, float* h_scale, int out_dtype, void* y, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Root-mean-square norm with the residual's addition, in front of a layer.
+ *   s = x + residual, rounded to the residual's type (s = x without one);
+ *   n = fl32(s / sqrt(mean(s^2) + eps)), the mean over the row and the
+ *   quotient in 64 bits; y = fl32(n w).
+ * Outputs: res_out = s (with a residual; its type, and it may be the residual
+ * or an x of that type itself); y in bf16; y as E4M3 codes with a scale for
+ * each 128 values of a row, what moe_quantize_fp8_block gives for the fp32 y
+ * (y is rounded once, not to bf16 first).
+ *   x [rows, d], residual [rows, d] or NULL, w [d]: each bf16 (MOE_IN_BF16) or
+ *   fp32 (MOE_IN_F32); res_out [rows, d]; y [rows, d] bf16 or NULL; codes
+ *   [rows, d] and scales [rows, ceil(d / 128)] fp32, or both NULL; y or codes
+ *   is given.  eps >= 0 and finite.  d a multiple of 8 (with codes of 16), up
+ *   to 32768; all 16-byte aligned but scales (4).  y, codes and scales overlap
+ *   no input.
+ */
+int moe_add_rms_norm(const void* x, int x_dtype, const void* residual, int res_dtype,
+                     const void* w, int w_dtype, long long rows, int d, double eps,
+                     void* res_out, uint16_t* y, uint8_t* codes, float* scales, void* stream);
+
+/* Its backward.  s [rows, d] is what was normalised (res_out, or x without a
+ * residual), dy the gradient of y, d_res (or NULL) that of res_out from
+ * elsewhere.  With r = 1 / sqrt(mean(s^2) + eps), n = s r and g = dy w:
+ *   dx = r (g - n mean(g n)) + d_res, the gradient of x and of the residual;
+ *   dw[c] = sum_t dy[t, c] n[t, c], fp32.
+ *   s, w, dy, d_res, dx: each bf16 or fp32 (MOE_IN_*); dx may be dy or d_res
+ *   of the same type.  dw [d] is written (zeros with rows = 0).  ws:
+ *   moe_rms_norm_backward_workspace_size(rows, d) bytes, 256-byte aligned (0
+ *   for sizes outside the limits of moe_add_rms_norm).
+ */
+size_t moe_rms_norm_backward_workspace_size(long long rows, int d);
+int moe_rms_norm_backward(const void* s, int s_dtype, const void* w, int w_dtype, const void* dy,
+                          int dy_dtype, const void* d_res, int res_dtype, long long rows, int d,
+                          double eps, void* dx, int dx_dtype, float* dw, void* ws,
+                          size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Balance loss of the routing, with per-expert counts [HP 01: the experts'
+ * load is kept even for text and image tokens apart].  The tokens of sequence
+ * i, offsets[i] <= t < offsets[i + 1], form C groups: one, or with a modality
+ * two, text (0) and image (1).  A token takes part where mask (if any) is not
+ * 0 and all its ids are experts; one with an id outside [0, E) sets
+ * MOE_FLAG_BAD_EXPERT_ID.  For a group g of T_g such tokens:
+ *   counts[g, e] = its (token, slot) pairs with expert e,
+ *   f_e = E counts[g, e] / (k T_g),  p_te = s_te / sum_e s_te, s = S(logits)
+ *   (moe_route's scores),
+ *   loss[g] = 1 / T_g sum_t sum_e f_e p_te  (1 for even load; 0 if T_g = 0).
+ * Sums over tokens are held in 64 bits.
+ *   logits [T, E] fp32, topk_ids [T, k] int32; offsets [S + 1] int32 in DEVICE
+ *   memory, non-decreasing within [0, T] (entries outside are clamped; NULL
+ *   with S = 1: all tokens); modality, mask [T] u8 or NULL; loss [S, C] fp32,
+ *   counts [S, C, E] int32 (written).  Same limits on E and k as moe_route
+ *   (k > E is allowed: hash tables may repeat an expert); 1 <= S <= 2^20.  ws:
+ *   moe_balance_loss_workspace_size(T) bytes, 256-byte aligned (NULL with 0).
+ */
+size_t moe_balance_loss_workspace_size(int T);
+int moe_balance_loss(const float* logits, const int32_t* topk_ids, const int32_t* offsets,
+                     const uint8_t* modality, const uint8_t* mask, int T, int E, int k, int S,
+                     float* loss, int32_t* counts, uint32_t* d_flags, void* ws, size_t ws_bytes,
+                     void* stream);
+
+/* Its gradient in the logits, for a gradient d_loss [S, C] of the losses (the
+ * counts are constants):
+ *   d_logits[t, j] = d_loss[g] / T_g (f_j - sum_e f_e p_te) p_tj (1 - s_tj)
+ *                    + add[t, j],
+ * 0 (+ add) for tokens that take no part.  counts: what moe_balance_loss gave
+ * for the same tokens; add [T, E] fp32 or NULL, as from moe_route_backward (it
+ * may be d_logits itself).  d_logits [T, E] fp32, every entry written.
+ */
+int moe_balance_loss_backward(const float* logits, const int32_t* topk_ids,
+                              const int32_t* offsets, const uint8_t* modality,
+                              const uint8_t* mask, const int32_t* counts, const float* d_loss,
+                              const float* add, int T, int E, int k, int S, float* d_logits,
+                              void* stream);
+
+/* ------------------------------------------------------------------------
+ * Norm of many gradient tensors, and their clipping [HP 03: the training run
+ * reports the gradients' norm].
+ *   norm = sqrt(sum of the squares of all values), added in 64 bits;
+ *   out = fl(grad * max_norm / norm) where max_norm < norm < inf, else grad:
+ *   gradients with an infinity or NaN stay as they are, and norm says so.
+ * The tensors are laid out once: moe_grad_plan writes, on the host, the plan
+ * of moe_grad_plan_size bytes (0: nothing, or bad arguments), which the caller
+ * copies to the device and keeps as long as the tensors stay where they are.
+ *   grad, out: DEVICE, 16-byte aligned, n >= 0 values of dtype (MOE_IN_BF16 or
+ *   MOE_IN_F32); out may be grad (in place), else it overlaps no grad; no two
+ *   outs overlap (a tensor listed twice would be scaled twice:
+ *   MOE_ERR_UNSUPPORTED).
+ */
+typedef struct moe_grad_tensor {
+    const void* grad;
+    void* out;
+    int64_t n;
+    int dtype;
+} moe_grad_tensor;
+size_t moe_grad_plan_size(const moe_grad_tensor* tensors, int count);
+int moe_grad_plan(const moe_grad_tensor* tensors, int count, void* host_plan, size_t plan_bytes);
+
+/* plan: DEVICE, 32-byte aligned, plan_bytes as moe_grad_plan_size gave (0:
+ * norm = 0).  norm: one fp32, DEVICE (inf where the norm passes fp32; the
+ * clipping is right all the same).  max_norm >= 0, not NaN.  ws:
+ * MOE_GRAD_WORKSPACE_BYTES, 256-byte aligned. */
+#define MOE_GRAD_WORKSPACE_BYTES 16384
+int moe_grad_norm(const void* plan, size_t plan_bytes, float* norm, void* ws, size_t ws_bytes,
+                  void* stream);
+int moe_clip_grad_norm(const void* plan, size_t plan_bytes, double max_norm, float* norm, void* ws,
+                       size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * MXFP4 rows and their grouped product [CN outlook: MxFP4], on row-major codes
+ * as checkpoints hold them.  Quantisation: per 32 consecutive values of a row,
+ *   X = floor(log2(max |v|)) - 2 clamped to [-127, 127] (0 for zeros),
+ *   code = E2M1(v / 2^X), nearest, ties to even, saturating at +-6,
+ * scale byte X + 127; a block that holds an infinity or NaN gets the scale
+ * byte 255 (NaN: all its values).  Rows of matrices are quantised alike.
+ *   a [rows, K] bf16 (MOE_IN_BF16) or fp32 (MOE_IN_F32); codes [rows, K / 2],
+ *   the lower column in the low nibble; scales [rows, K / 32].  K a multiple
+ *   of 32; a, codes 16-byte aligned.
+ */
+int moe_quantize_mxfp4(const void* a, int in_dtype, long long rows, int K, uint8_t* codes,
+                       uint8_t* scales, void* stream);
+
+/* For offsets[g] <= r < offsets[g + 1]:
+ *   out[r, n] = sum_b 2^(Xa[r, b] + Xw[g, n, b]) sum_{k in block b} a[r, k] w[g, n, k],
+ * out bf16 (MOE_OUT_BF16) or fp32 (MOE_OUT_F32), fp32 sums on the scaled matrix
+ * cores; rows outside every group are left untouched.
+ *   a4 [rows, K / 2], a_scale [rows, K / 32], w4 [G, N, K / 2], w_scale [G, N,
+ *   K / 32] (codes and scale bytes as above); offsets [G + 1] int32 in DEVICE
+ *   memory, non-decreasing within [0, rows] (entries outside are clamped).  K
+ *   a multiple of 32, N of 16, up to 2^22; a4, w4, out 16-byte aligned.  No
+ *   workspace.
+ */
+int moe_grouped_gemm_mxfp4(const uint8_t* a4, const uint8_t* a_scale, const int32_t* offsets,
+                           int G, int rows, int K, int N, const uint8_t* w4,
+                           const uint8_t* w_scale, int out_dtype, void* out, void* stream);
+
+/* ------------------------------------------------------------------------
  * Result return merged by routing weight [TW], plus the always-on shared
  * expert with weight 1 [MS]:
  *   y[t,o] = y_shared[t,o] + sum_j topk_w[t,j] * y_perm[dest[t,j], o]

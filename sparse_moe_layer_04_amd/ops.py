@@ -57,6 +57,8 @@ WEIGHTS_FP8_BLOCK = 5
 # scaled block of the 8-bit operators, largest T of forward_few
 FP8_BLOCK = 128
 FEW_MAX_T = 64
+# workspace of the gradients' norm and clipping
+GRAD_WORKSPACE_BYTES = 16384
 IN_BF16 = 0
 IN_F32 = 1
 MATRIX_NAMES = ("w_g", "w_gate", "w_up", "w_down", "s_gate", "s_up", "s_down")
@@ -72,6 +74,11 @@ GRAD_NAMES = ("dx", "dw_g", "dw_gate", "dw_up", "dw_down", "ds_gate", "ds_up", "
 
 class MoeBwdWeights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in BWD_WEIGHT_NAMES]
+
+
+class MoeGradTensor(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("dtype", ctypes.c_int)]
 
 
 class MoeGrads(ctypes.Structure):
@@ -129,6 +136,22 @@ def lib():
     L.moe_grouped_gemm_fp8_block.argtypes = [P, P, P, I, I, I, I, P, P, I, P, P]
     L.moe_expert_ffn_fp8_block.argtypes = [P, P, P, I, I, I, I, P, P, P, P, P, P, F, I, P, P, I,
                                            P, P]
+    LL, D = ctypes.c_longlong, ctypes.c_double
+    L.moe_add_rms_norm.argtypes = [P, I, P, I, P, I, LL, I, D, P, P, P, P, P]
+    L.moe_rms_norm_backward_workspace_size.argtypes = [LL, I]
+    L.moe_rms_norm_backward_workspace_size.restype = S
+    L.moe_rms_norm_backward.argtypes = [P, I, P, I, P, I, P, I, LL, I, D, P, I, P, P, S, P]
+    L.moe_balance_loss_workspace_size.argtypes = [I]
+    L.moe_balance_loss_workspace_size.restype = S
+    L.moe_balance_loss.argtypes = [P, P, P, P, P, I, I, I, I, P, P, P, P, S, P]
+    L.moe_balance_loss_backward.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, P, P]
+    L.moe_grad_plan_size.argtypes = [ctypes.POINTER(MoeGradTensor), I]
+    L.moe_grad_plan_size.restype = S
+    L.moe_grad_plan.argtypes = [ctypes.POINTER(MoeGradTensor), I, P, S]
+    L.moe_grad_norm.argtypes = [P, S, P, P, S, P]
+    L.moe_clip_grad_norm.argtypes = [P, S, D, P, P, S, P]
+    L.moe_quantize_mxfp4.argtypes = [P, I, LL, I, P, P, P]
+    L.moe_grouped_gemm_mxfp4.argtypes = [P, P, P, I, I, I, I, P, P, I, P, P]
     L.moe_forward_few_workspace_size.argtypes = [ctypes.POINTER(MoeCfg)]
     L.moe_forward_few_workspace_size.restype = S
     L.moe_forward_workspace_size.argtypes = [ctypes.POINTER(MoeCfg)]
@@ -151,7 +174,10 @@ def lib():
                  "moe_pack_weights_fp8", "moe_pack_weights_fp4", "moe_quantize_mxfp8",
                  "moe_expert_ffn_a8w4", "moe_quantize_fp8_block",
                  "moe_quantize_weights_fp8_block", "moe_grouped_gemm_fp8_block",
-                 "moe_expert_ffn_fp8_block", "moe_forward_few"):
+                 "moe_expert_ffn_fp8_block", "moe_forward_few", "moe_add_rms_norm",
+                 "moe_rms_norm_backward", "moe_balance_loss", "moe_balance_loss_backward",
+                 "moe_grad_plan", "moe_grad_norm", "moe_clip_grad_norm", "moe_quantize_mxfp4",
+                 "moe_grouped_gemm_mxfp4"):
         getattr(L, name).restype = I
     _lib = L
     return L
@@ -670,6 +696,234 @@ def expert_ffn_fp8_block(a8, a_scale, offsets, w_gate, w_up, w_down, clamp_limit
                                           _ptr(h_scale), int(out_dtype), _ptr(y), _stream()),
            "moe_expert_ffn_fp8_block")
     return h8, h_scale, y
+
+
+def _here(t, *others):
+    """All tensors on the current device, whose stream the call goes to."""
+    dev = torch._C._cuda_getDevice()
+    for u in (t,) + others:
+        if u is not None and u.get_device() != dev:
+            raise MoeError(f"tensors must be on the current device (cuda:{dev}), got {u.device}")
+
+
+def _any_dtype(t, name, shape=None, dims=None):
+    """A bf16 or fp32 tensor: returns its MOE_IN_* type."""
+    dt = _in_dtype(t, name)
+    _need(t, t.dtype, name, dims, shape)
+    return dt
+
+
+def add_rms_norm(x, w, residual=None, eps=1e-6, fp8=False, want_y=True, res=None, y=None,
+                 codes=None, scales=None):
+    """s = x + residual (in the residual's type), n = s / sqrt(mean(s^2) +
+    eps), y = n w (moe_add_rms_norm), for x, residual [rows, d] and w [d] of
+    bf16 or fp32.  Returns (s, y, codes, scales): s = x without a residual; y
+    bf16, None without want_y; with fp8 the E4M3 codes of the fp32 y and their
+    scales of 128 values as expert_ffn_fp8_block takes them, else None.  d is a
+    multiple of 8 (with fp8 of 16) up to 32768; res may be the residual (or x)
+    itself, to update the stream in place."""
+    xt = _any_dtype(x, "x", dims=2)
+    rows, d = x.shape
+    wt = _any_dtype(w, "w", (d,))
+    rt = 0
+    if residual is not None:
+        rt = _any_dtype(residual, "residual", (rows, d))
+        res = _out(res, residual.dtype, "res", (rows, d), x.device)
+    elif res is not None:
+        raise MoeError("res is an output of the residual's addition: it needs a residual")
+    if not (want_y or fp8):
+        raise MoeError("add_rms_norm needs an output: want_y or fp8")
+    y = _out(y, torch.bfloat16, "y", (rows, d), x.device) if want_y else None
+    if fp8:
+        codes = _codes_like(codes, x)
+        scales = _out(scales, torch.float32, "scales", (rows, _blocks(d)), x.device)
+    else:
+        codes = scales = None
+    _here(x, w, residual, res, y, codes, scales)
+    _check(lib().moe_add_rms_norm(_ptr(x), xt, _ptr(residual), rt, _ptr(w), wt, rows, d,
+                                  float(eps), _ptr(res), _ptr(y), _ptr(codes), _ptr(scales),
+                                  _stream()), "moe_add_rms_norm")
+    return x if residual is None else res, y, codes, scales
+
+
+def rms_norm_backward_workspace_size(rows, d):
+    return int(lib().moe_rms_norm_backward_workspace_size(rows, d))
+
+
+def rms_norm_backward(s, w, dy, eps=1e-6, d_res=None, dx_dtype=OUT_F32, dx=None, dw=None,
+                      workspace=None):
+    """Backward of add_rms_norm (moe_rms_norm_backward): s what was normalised
+    (its first result), dy the gradient of y, d_res that of s from elsewhere
+    (or None); bf16 or fp32 each.  Returns (dx [rows, d] of dx_dtype, the
+    gradient of x and of the residual, dw [d] fp32)."""
+    st = _any_dtype(s, "s", dims=2)
+    rows, d = s.shape
+    wt = _any_dtype(w, "w", (d,))
+    gt = _any_dtype(dy, "dy", (rows, d))
+    rt = 0 if d_res is None else _any_dtype(d_res, "d_res", (rows, d))
+    dt = torch.float32 if dx_dtype == OUT_F32 else torch.bfloat16
+    dx = _out(dx, dt, "dx", (rows, d), s.device)
+    dw = _out(dw, torch.float32, "dw", (d,), s.device)
+    if workspace is None:
+        workspace = torch.empty(rms_norm_backward_workspace_size(rows, d), dtype=torch.uint8,
+                                device=s.device)
+    _need(workspace, torch.uint8, "workspace", 1)
+    _here(s, w, dy, d_res, dx, dw, workspace)
+    _check(lib().moe_rms_norm_backward(_ptr(s), st, _ptr(w), wt, _ptr(dy), gt, _ptr(d_res), rt,
+                                       rows, d, float(eps), _ptr(dx),
+                                       IN_F32 if dt == torch.float32 else IN_BF16, _ptr(dw),
+                                       _ptr(workspace), workspace.numel(), _stream()),
+           "moe_rms_norm_backward")
+    return dx, dw
+
+
+def _balance_args(logits, ids, offsets, modality, mask):
+    _need(logits, torch.float32, "logits", 2)
+    T, E = logits.shape
+    _need(ids, torch.int32, "ids", shape=(T, None))
+    _opt(modality, torch.uint8, "modality", shape=(T,))
+    _opt(mask, torch.uint8, "mask", shape=(T,))
+    S = 1
+    if offsets is not None:
+        _need(offsets, torch.int32, "offsets", 1)
+        S = offsets.numel() - 1
+    return T, E, ids.shape[1], S, 1 if modality is None else 2
+
+
+def balance_loss_workspace_size(T):
+    return int(lib().moe_balance_loss_workspace_size(T))
+
+
+def balance_loss(logits, ids, offsets=None, modality=None, mask=None, flags=None, loss=None,
+                 counts=None, workspace=None):
+    """Balance loss and per-expert counts (moe_balance_loss) of the routes ids
+    [T, k] on logits [T, E]: per sequence (offsets [S + 1] int32, or None: one
+    of all tokens) and, with a modality [T] u8, per class.  mask [T] u8: tokens
+    of 0 take no part.  Returns (loss [S, C] fp32, counts [S, C, E] int32)."""
+    T, E, k, S, C = _balance_args(logits, ids, offsets, modality, mask)
+    _flags(flags)
+    loss = _out(loss, torch.float32, "loss", (S, C), logits.device)
+    counts = _out(counts, torch.int32, "counts", (S, C, E), logits.device)
+    if workspace is None:
+        workspace = torch.empty(balance_loss_workspace_size(T), dtype=torch.uint8,
+                                device=logits.device)
+    _need(workspace, torch.uint8, "workspace", 1)
+    _here(logits, ids, offsets, modality, mask, flags, loss, counts, workspace)
+    _check(lib().moe_balance_loss(_ptr(logits), _ptr(ids), _ptr(offsets), _ptr(modality),
+                                  _ptr(mask), T, E, k, S, _ptr(loss), _ptr(counts), _ptr(flags),
+                                  _ptr(workspace), workspace.numel(), _stream()),
+           "moe_balance_loss")
+    return loss, counts
+
+
+def balance_loss_backward(logits, ids, counts, d_loss, offsets=None, modality=None, mask=None,
+                          add=None, out=None):
+    """Gradient of balance_loss in the logits (moe_balance_loss_backward) for
+    d_loss [S, C], counts as balance_loss gave them; add [T, E] is added, as
+    route_backward's d_logits (out may be add).  Returns d_logits [T, E]."""
+    T, E, k, S, C = _balance_args(logits, ids, offsets, modality, mask)
+    _need(counts, torch.int32, "counts", shape=(S, C, E))
+    _need(d_loss, torch.float32, "d_loss", shape=(S, C))
+    _opt(add, torch.float32, "add", shape=(T, E))
+    out = _out(out, torch.float32, "out", (T, E), logits.device)
+    _here(logits, ids, counts, d_loss, offsets, modality, mask, add, out)
+    _check(lib().moe_balance_loss_backward(_ptr(logits), _ptr(ids), _ptr(offsets), _ptr(modality),
+                                           _ptr(mask), _ptr(counts), _ptr(d_loss), _ptr(add), T,
+                                           E, k, S, _ptr(out), _stream()),
+           "moe_balance_loss_backward")
+    return out
+
+
+class GradClip:
+    """Norm and clipping of gradient tensors (moe_grad_norm,
+    moe_clip_grad_norm): bf16 or fp32 tensors of any shapes on one device, laid
+    out once and kept (the plan holds them), as a program keeps its gradient
+    buffers.  out: tensors of the same shapes and types for the clipped
+    gradients; None: in place.  A tensor listed twice, or one that overlaps
+    another's out, is refused.  A GradClip serves one call at a time (its
+    workspace)."""
+
+    def __init__(self, grads, out=None):
+        self.grads = list(grads)
+        self.out = self.grads if out is None else list(out)
+        if len(self.out) != len(self.grads):
+            raise MoeError(f"out must hold {len(self.grads)} tensors, got {len(self.out)}")
+        if not self.grads:
+            raise MoeError("grads must hold a tensor")
+        entries = (MoeGradTensor * len(self.grads))()
+        for i, (g, o) in enumerate(zip(self.grads, self.out)):
+            dt = _any_dtype(g, f"grads[{i}]")
+            _need(o, g.dtype, f"out[{i}]", shape=tuple(g.shape))
+            _here(g, o)
+            entries[i] = MoeGradTensor(_ptr(g) or None, _ptr(o) or None, g.numel(), dt)
+        self.device = self.grads[0].device
+        size = int(lib().moe_grad_plan_size(entries, len(entries)))
+        host = torch.empty(size, dtype=torch.uint8)
+        _check(lib().moe_grad_plan(entries, len(entries), host.data_ptr() if size else None, size),
+               "moe_grad_plan")
+        self.plan = host.to(self.device)
+        self.workspace = torch.empty(GRAD_WORKSPACE_BYTES, dtype=torch.uint8, device=self.device)
+
+    def norm(self, norm=None):
+        """The norm of the gradients as they are now, [1] fp32."""
+        return self._run(lambda n: lib().moe_grad_norm(
+            _ptr(self.plan), self.plan.numel(), n, _ptr(self.workspace), GRAD_WORKSPACE_BYTES,
+            _stream()), norm, "moe_grad_norm")
+
+    def clip(self, max_norm, norm=None):
+        """Scales the gradients to max_norm where their norm is larger (and
+        finite), into out; returns the norm before, [1] fp32."""
+        max_norm = float(max_norm)
+        return self._run(lambda n: lib().moe_clip_grad_norm(
+            _ptr(self.plan), self.plan.numel(), max_norm, n, _ptr(self.workspace),
+            GRAD_WORKSPACE_BYTES, _stream()), norm, "moe_clip_grad_norm")
+
+    def _run(self, call, norm, what):
+        norm = _out(norm, torch.float32, "norm", (1,), self.device)
+        _here(norm, self.plan)
+        _check(call(_ptr(norm)), what)
+        return norm
+
+
+def quantize_mxfp4(a, codes=None, scales=None):
+    """Rows a [..., K] (bf16 or fp32, 2 or 3 dims, K a multiple of 32) as
+    MXFP4 (moe_quantize_mxfp4): returns (codes uint8 [..., K / 2], the lower
+    column in the low nibble, scale bytes X + 127 uint8 [..., K / 32])."""
+    dt = _any_dtype(a, "a")
+    if a.dim() not in (2, 3):
+        raise MoeError("a must have 2 or 3 dims")
+    shape = tuple(a.shape)
+    K = shape[-1]
+    codes = _out(codes, torch.uint8, "codes", shape[:-1] + (K // 2,), a.device)
+    scales = _out(scales, torch.uint8, "scales", shape[:-1] + (K // 32,), a.device)
+    _here(a, codes, scales)
+    rows = shape[0] if len(shape) == 2 else shape[0] * shape[1]
+    _check(lib().moe_quantize_mxfp4(_ptr(a), dt, rows, K, _ptr(codes), _ptr(scales), _stream()),
+           "moe_quantize_mxfp4")
+    return codes, scales
+
+
+def grouped_gemm_mxfp4(a4, a_scale, offsets, w4, w_scale, out_dtype=OUT_BF16, out=None):
+    """out[r] = a[r] @ w[g].T for the rows of group g, operands in MXFP4
+    (moe_grouped_gemm_mxfp4): a4 [rows, K / 2], a_scale [rows, K / 32], w4 [G,
+    N, K / 2], w_scale [G, N, K / 32], uint8 as quantize_mxfp4 gives them;
+    offsets [G + 1] int32.  K a multiple of 32, N of 16.  Rows outside every
+    group are not written."""
+    _need(a4, torch.uint8, "a4", 2)
+    rows, half = a4.shape
+    K = 2 * half
+    _need(w4, torch.uint8, "w4", shape=(None, None, half))
+    G, N = w4.shape[:2]
+    _need(a_scale, torch.uint8, "a_scale", shape=(rows, K // 32))
+    _need(w_scale, torch.uint8, "w_scale", shape=(G, N, K // 32))
+    _need(offsets, torch.int32, "offsets", shape=(G + 1,))
+    dt = torch.float32 if out_dtype == OUT_F32 else torch.bfloat16
+    out = _out(out, dt, "out", (rows, N), a4.device)
+    _here(a4, a_scale, offsets, w4, w_scale, out)
+    _check(lib().moe_grouped_gemm_mxfp4(_ptr(a4), _ptr(a_scale), _ptr(offsets), G, rows, K, N,
+                                        _ptr(w4), _ptr(w_scale), int(out_dtype), _ptr(out),
+                                        _stream()), "moe_grouped_gemm_mxfp4")
+    return out
 
 
 class MoeLayer:
