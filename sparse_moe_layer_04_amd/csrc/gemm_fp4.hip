@@ -3,70 +3,442 @@
 //   out[r, n] = sum_b 2^(Xa[r, b] + Xw[g, n, b]) sum_{k in block b} a[r, k] w[g, n, k],
 // b the blocks of 32 of K, codes E2M1, scale bytes X + 127 (255: NaN).
 //
-// The scaled matrix instructions take both operands as they are: lane l holds
-// of row (column) l % 32 the 16 bytes of block 2 s + l / 32 of step s, and that
-// block's scale byte.
+// The scaled matrix instructions (32 x 32 outputs, 64 of K) take both operands
+// as they are: lane l holds of row (column) l % 32 the 16 bytes of block 2 s +
+// l / 32 of step s, and that block's scale byte, one of four of a register.
+//
+// Tile: up to 128 rows x 256 weight rows, 8 waves of 64 x 64 or (rows of the
+// tile) x 32 outputs, 256 of K (128 bytes a row) a stage, four steps.  The
+// codes of both operands go to a ring of three LDS slots by copies that pass
+// no register, two stages ahead (a wave's copy covers 8 rows x 128 bytes; LDS
+// row r holds its 16-byte chunk c at c ^ ((r >> 1) & 7), so that the lanes of
+// an operand read spread over the banks).  A row's 8 scale bytes of a stage
+// start at any byte (K / 32 need not be a multiple of 4): the 16 bytes from the
+// word that holds the first one are copied, one stage ahead and into one of two
+// places, and each lane shifts its own out.
 #include "fp4.h"
+#include "lds_ring.h"
 
 namespace moe {
 namespace {
 
-template <bool F32>
-__global__ __launch_bounds__(256) void gemm_mxfp4_kernel(Fp4GemmArgs p) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5, l32 = lane & 31;
-    auto clamped = [&](int v) { return min(max(v, 0), p.rows); };
-    int local = blockIdx.x, g = 0, r0 = 0, n = 0;
-    for (;; ++g) {
-        if (g == p.G) return;
-        r0 = clamped(p.offsets[g]);
-        n = max(clamped(p.offsets[g + 1]) - r0, 0);
-        const int tiles = (n + 31) >> 5;
-        if (local < tiles) break;
-        local -= tiles;
-    }
-    const int row = r0 + 32 * local + l32, end = r0 + n;
-    const int n0 = (blockIdx.y * 4 + wave) * 32;
-    if (n0 >= p.N) return;
-    const int nb = p.K / 32;
-    const size_t ar = (size_t)min(row, end - 1), wr = (size_t)g * p.N + min(n0 + l32, p.N - 1);
-    const u32x4* ac = (const u32x4*)(p.a + ar * (p.K / 2));
-    const u32x4* wc = (const u32x4*)(p.w + wr * (p.K / 2));
-    const uint8_t* as = p.as + ar * nb;
-    const uint8_t* ws = p.ws + wr * nb;
-    f32x16 acc;
+constexpr int BM = 128;                    // rows a tile, at most
+constexpr int BN = 256;                    // weight rows a tile
+constexpr int BK = 128;                    // bytes of a row a stage: 256 of K
+constexpr int kThreads = 512;
+constexpr int kSlotW = BN * BK;
+constexpr int kSlot = kSlotW + BM * BK;
+constexpr int kRing = 3 * kSlot;
+constexpr int kScales = 16 * (BN + BM);    // a stage's scales: 16 bytes a row, W's first
+constexpr int kLds = kRing + 2 * kScales;
+static_assert(kLds <= 160 * 1024 && kSlot % 128 == 0, "three slots of LDS");
+
+struct Tile {
+    int g, row0, valid, n0;                // n0: first weight row
+};
+
+// copies of codes a wave and stage: 4 of W, NA (one for each 64 rows) of A
+constexpr int row_copies(int blocks) { return (blocks + 1) / 2; }
+constexpr int kEarly = 3;                  // of them, issued in the stage before
+
+// The copies of a tile's operands into LDS, set up once per tile: buffer
+// resources over the tile's rows (wave-uniform base, 32-bit offsets; rows past
+// the tile's or the matrix's end lie past them and fetch nothing).
+struct Fetch {
+    u32x4 wsrc, asrc, ssrc;
+    int wo[4], ao[2], so;
+
+    __device__ __forceinline__ void set(const Fp4GemmArgs& p, const Tile& t) {
+        const int tid = threadIdx.x, lane = tid & 63;
+        const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const int Kb = p.K / 2, nb = p.K / 32;
+        const int lr = tid >> 3, c = (tid & 7) ^ swz(lr);   // chunk c of row lr + 64 q
+        const size_t wfirst = (size_t)t.g * p.N + t.n0;
+        const int wrows = min(p.N - t.n0, BN);
+        wsrc = uniform_rsrc(p.w + wfirst * Kb, (size_t)wrows * Kb);
+        asrc = uniform_rsrc(p.a + (size_t)t.row0 * Kb, (size_t)t.valid * Kb);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-    for (int b = half; b - half < nb; b += 2) {
-        const bool in = b < nb;
-        u32x4 x = {0u, 0u, 0u, 0u}, y = x;
-        int sx = 127, sy = 127;
-        if (in) x = wc[b], y = ac[b], sx = ws[b], sy = as[b];
-        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-            v8i{(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0},
-            v8i{(int)y[0], (int)y[1], (int)y[2], (int)y[3], 0, 0, 0, 0}, acc, 4, 4, 0, sx, 0, sy);
-    }
-    if (row >= end) return;
+        for (int q = 0; q < 4; ++q) wo[q] = (lr + 64 * q) * Kb + 16 * c;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const int col = n0 + 8 * q + 4 * half;
-        if (col >= p.N) continue;
-        const size_t at = (size_t)row * p.N + col;
-        if constexpr (F32)
-            *(f32x4*)((float*)p.out + at) =
-                f32x4{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
+        for (int q = 0; q < 2; ++q) ao[q] = wo[q];
+        // scales: waves 0-3 the weight rows', 4 and 5 the rows' (6 and 7 the
+        // same again, so that every wave issues the same number of copies);
+        // whole words from the one that holds the first byte on
+        const bool isw = wave < 4;
+        const uint8_t* first = isw ? p.ws + wfirst * nb : p.as + (size_t)t.row0 * nb;
+        const int mis = (int)((uintptr_t)first & 3);
+        ssrc = uniform_rsrc(first - mis,
+                            ((size_t)(isw ? wrows : t.valid) * nb + mis + 3) & ~size_t(3));
+        so = ((64 * (isw ? wave : wave & 1) + lane) * nb + mis) & ~3;
+    }
+
+    // Copy q (of 4 + NA) of stage j into the slot at LDS byte `at`.  Stage 0
+    // takes K's last bytes, the short stage if any, stage j the j'th 128 bytes
+    // but one.  (Every stage issues its copies: past the last stage with offsets
+    // past the resources.)  `past`: the bytes that this thread's chunk reaches
+    // past K in the last stage; it fetches the row's last chunk instead, which
+    // is overwritten by zeros when it has landed.
+    template <int NA>
+    __device__ __forceinline__ void copy(int q, int j, int S, int past, int at) const {
+        const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+        const int b = j == 0 ? S - 1 : min(j, S) - 1;
+        const int back = j == 0 ? past : 0, out = j < S ? 0 : (int)0x80000000;
+        if (q < 4)
+            copy16(wsrc, (wo[q] - back) | out, b * BK, at + q * 64 * BK + wave * 1024);
         else
-            *(u32x2*)((uint16_t*)p.out + at) = u32x2{bf16_pack2(acc[4 * q], acc[4 * q + 1]),
-                                                     bf16_pack2(acc[4 * q + 2], acc[4 * q + 3])};
+            copy16(asrc, (ao[q - 4] - back) | out, b * BK,
+                   at + kSlotW + (q - 4) * 64 * BK + wave * 1024);
     }
+    template <int NA, int Q0, int Q1>
+    __device__ __forceinline__ void copies(int j, int S, int past, int at) const {
+#pragma unroll
+        for (int q = Q0; q < Q1 && q < 4 + NA; ++q) copy<NA>(q, j, S, past, at);
+    }
+    // the scales of stage j
+    __device__ __forceinline__ void scales(int j, int S) const {
+        const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+        const int b = j == 0 ? S - 1 : min(j, S) - 1, out = j < S ? 0 : (int)0x80000000;
+        copy16(ssrc, so | out, b * 8,
+               kRing + (j & 1) * kScales + (wave < 6 ? wave : wave - 2) * 1024);
+    }
+    // what is on its way when a tile (of NA row copies) begins
+    template <int NA>
+    __device__ __forceinline__ void first(int S, int past) const {
+        copies<NA, 0, 6>(0, S, past, 0);
+        scales(0, S);
+        copies<NA, 0, 6>(1, S, past, kSlot);
+        scales(1, S);
+        copies<NA, 0, kEarly>(2, S, past, 2 * kSlot);
+    }
+    __device__ __forceinline__ void first_stages(int valid, int S, int past) const {
+        if (valid <= 64) first<1>(S, past);
+        else first<2>(S, past);
+    }
+};
+
+// One tile, whose first three stages are on their way into the ring; sends the
+// next tile's (if there are more) off before this one's results are written.
+template <bool F32, int MB>
+__device__ __forceinline__ void run_tile(const Fp4GemmArgs& p, const Tile& t, const Tile& next_t,
+                                         bool more, int past, unsigned char* ring) {
+    // (the thread's place as a value of this variant's own: address terms
+    // shared by the variants would be kept, or spilled, for all of them)
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
+    const int lane = tid & 63, half = lane >> 5, l32 = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    Fetch f;
+    f.set(p, t);
+    // waves: WM along the rows x WN along the weight rows, each MI x NJ
+    // blocks of 32 x 32
+    constexpr int WM = MB == 4 ? 2 : 1, WN = 8 / WM, MI = MB / WM, NJ = 8 / WN, NT = MI * NJ;
+    constexpr int NA = row_copies(MB), kCopies = 4 + NA;
+    const int wm = wave / WN, wn = wave % WN;
+    const int N = p.N, nb = p.K / 32;
+    const int S = (p.K / 2 + BK - 1) / BK;
+
+    // LDS rows 32 apart share their swizzle, so the rest of an operand's
+    // address is an immediate; the chunk index enters it by exclusive or
+    const int rd0 = l32 * BK + ((half ^ swz(l32)) << 4);
+    const int rdw = wn * NJ * 32 * BK + rd0;
+    const int rda = kSlotW + wm * MI * 32 * BK + rd0;
+    const int rsw = kRing + (wn * NJ * 32 + l32) * 16;
+    const int rsa = kRing + (BN + wm * MI * 32 + l32) * 16;
+    // bits from the copied words' first byte to this half's first scale
+    const uint32_t wbase = (uint32_t)((uintptr_t)p.ws + ((size_t)t.g * N + t.n0) * nb);
+    const uint32_t abase = (uint32_t)((uintptr_t)p.as + (size_t)t.row0 * nb);
+    int shw[NJ], sha[MI];
+#pragma unroll
+    for (int n = 0; n < NJ; ++n)
+        shw[n] = 8 * (int)((wbase + (uint32_t)((wn * NJ + n) * 32 + l32) * nb) & 3) + 8 * half;
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+        sha[i] = 8 * (int)((abase + (uint32_t)((wm * MI + i) * 32 + l32) * nb) & 3) + 8 * half;
+
+    u32x4 qw[NJ], qa[MI];                  // a stage's scale words as copied
+    auto read_s = [&](int j) {
+#pragma unroll
+        for (int n = 0; n < NJ; ++n)
+            qw[n] = *(const u32x4*)(ring + rsw + (j & 1) * kScales + n * 32 * 16);
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+            qa[i] = *(const u32x4*)(ring + rsa + (j & 1) * kScales + i * 32 * 16);
+    };
+    // bytes 0 and 2 of word 0: the scales of steps 0 and 1, of word 1: 2 and 3
+    int cw[NJ][2], ca[MI][2];
+    auto shift = [](const u32x4& q, int by, int (&c)[2]) {
+        c[0] = (int)(uint32_t)((((uint64_t)q[1] << 32) | q[0]) >> by);
+        c[1] = (int)(uint32_t)((((uint64_t)q[2] << 32) | q[1]) >> by);
+    };
+    auto scales = [&]() {
+#pragma unroll
+        for (int n = 0; n < NJ; ++n) shift(qw[n], shw[n], cw[n]);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) shift(qa[i], sha[i], ca[i]);
+    };
+
+    f32x16 acc[MI][NJ];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int n = 0; n < NJ; ++n)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][n][e] = 0.0f;
+
+    // stage 0 has landed; zeros over this thread's own copies past K
+    wait_vm<kCopies + 1 + kEarly>();
+    if (past) {
+        const u32x4 z = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int q = 0; q < 4 + NA; ++q) *(u32x4*)(ring + q * 64 * BK + tid * 16) = z;
+    }
+    __syncthreads();
+    // The middle of stage j: stage j + 1 has landed (the copies behind its scales
+    // are stage j + 2's codes) and every wave has read stage j's operands, whose
+    // slot takes stage j + 3's, and its scales, whose place takes stage j + 2's.
+    auto turn = [&]() {
+        wait_vm<kCopies>();
+        __syncthreads();
+    };
+
+    u32x4 rw[2][NJ], ra[2][MI];
+    auto read = [&](int slot, auto step) {
+        constexpr int q = decltype(step)::value, B = q & 1;
+#pragma unroll
+        for (int n = 0; n < NJ; ++n)
+            rw[B][n] = *(const u32x4*)(ring + ((rdw + slot) ^ (q << 5)) + n * 32 * BK);
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+            ra[B][i] = *(const u32x4*)(ring + ((rda + slot) ^ (q << 5)) + i * 32 * BK);
+    };
+    auto wide = [](const u32x4& v) {
+        return v8i{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
+    };
+    // the products of a step, a copy (of up to four) behind each
+    auto multiply = [&](auto step, auto copy) {
+        constexpr int q = decltype(step)::value, B = q & 1, W = q >> 1, O = 2 * (q & 1);
+        static_for<0, 4>([&](auto index) {
+            constexpr int x = decltype(index)::value, i = x / NJ, n = x % NJ;
+            if constexpr (x < NT)
+                acc[i][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    wide(rw[B][n]), wide(ra[B][i]), acc[i][n], 4, 4, O, cw[n][W], O, ca[i][W]);
+            copy(index);
+        });
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    using Q0 = std::integral_constant<int, 0>;
+    using Q1 = std::integral_constant<int, 1>;
+    using Q2 = std::integral_constant<int, 2>;
+    using Q3 = std::integral_constant<int, 3>;
+    read(0, Q0());
+    read_s(0);
+    scales();
+    if (nb & 7) {
+        // stage 0's blocks past K (of zero codes): any finite scale
+        const int v = nb & 7;
+        auto mask = [&](int (&c)[2]) {
+            if (half >= v) c[0] = (c[0] & ~0xff) | 127;
+            if (2 + half >= v) c[0] = (c[0] & ~0xff0000) | 127 << 16;
+            if (4 + half >= v) c[1] = (c[1] & ~0xff) | 127;
+            if (6 + half >= v) c[1] = (c[1] & ~0xff0000) | 127 << 16;
+        };
+#pragma unroll
+        for (int n = 0; n < NJ; ++n) mask(cw[n]);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) mask(ca[i]);
+    }
+    int slot = 0;
+    for (int j = 0; j < S; ++j) {
+        const int next = slot == 2 * kSlot ? 0 : slot + kSlot;
+        const int last = next == 2 * kSlot ? 0 : next + kSlot;
+        read(slot, Q1());
+        multiply(Q0(), [&](auto x) {
+            constexpr int c = 3 + decltype(x)::value;
+            if constexpr (c < 5) f.template copies<NA, c, c + 1>(j + 2, S, past, last);
+        });
+        read(slot, Q2());
+        multiply(Q1(), [&](auto x) {
+            constexpr int c = 5 + decltype(x)::value;
+            if constexpr (c < 6) f.template copies<NA, c, c + 1>(j + 2, S, past, last);
+        });
+        read(slot, Q3());
+        multiply(Q2(), [](auto) {});
+        turn();
+        read(next, Q0());                           // (past the end: not used)
+        read_s(j + 1);
+        f.scales(j + 2, S);
+        multiply(Q3(), [&](auto x) {
+            constexpr int c = decltype(x)::value;
+            if constexpr (c < kEarly) f.template copies<NA, c, c + 1>(j + 3, S, past, slot);
+        });
+        scales();
+        slot = next;
+    }
+    // (every wave has read the last stage; what the ring still holds is unused)
+    if (more) {
+        Fetch nf;
+        nf.set(p, next_t);
+        nf.first_stages(next_t.valid, S, past);
+    }
+
+    // Lane l holds, of row l % 32 of its block, weight rows 8 q + 4 (l / 32) +
+    // (0 .. 3), q < 4.  The stores of a wave fill 32 to 64 bytes of a row each;
+    // the L2 joins them to lines.
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+        const int r = (wm * MI + i) * 32 + l32;
+        const size_t at = (size_t)(t.row0 + r) * N + t.n0;
+#pragma unroll
+        for (int n = 0; n < NJ; ++n) {
+            const f32x16& v = acc[i][n];
+            if constexpr (F32) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int col = (wn * NJ + n) * 32 + 8 * q + 4 * half;
+                    if (r < t.valid && t.n0 + col < N)
+                        *(f32x4*)((float*)p.out + at + col) =
+                            f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+                }
+            } else {
+                // (the half-waves exchange, so that a lane holds 8 columns in a row)
+#pragma unroll
+                for (int q = 0; q < 4; q += 2) {
+                    const u32x2 x = swap_halves(bf16_pack2(v[4 * q], v[4 * q + 1]),
+                                                bf16_pack2(v[4 * q + 4], v[4 * q + 5]));
+                    const u32x2 y = swap_halves(bf16_pack2(v[4 * q + 2], v[4 * q + 3]),
+                                                bf16_pack2(v[4 * q + 6], v[4 * q + 7]));
+                    const int col = (wn * NJ + n) * 32 + 8 * (q + half);
+                    if (r < t.valid && t.n0 + col < N)
+                        *(u32x4*)((uint16_t*)p.out + at + col) = u32x4{x[0], y[0], x[1], y[1]};
+                }
+            }
+        }
+    }
+}
+
+// row tiles of a group of n rows, tiles of up to `blocks` blocks of 32 rows
+__device__ __forceinline__ int row_tiles(int n, int blocks) {
+    const int c = (n + 31) >> 5;
+    return blocks == 1 ? c : blocks == 2 ? (c + 1) >> 1 : blocks == 3 ? (c + 2) / 3 : (c + 3) >> 2;
+}
+
+// Persistent grid, one workgroup a CU.  Items are (group, band of kBand
+// m-tiles, n-tile, m-tile), the 8 XCDs take contiguous ranges, so that the
+// m-tiles of a weight tile and the n-tiles of a group's rows meet in one XCD's
+// L2.  A group's rows split evenly over its m-tiles.  The group of an item
+// comes from a two-level sum that every wave keeps in registers: lane l holds
+// the items before run l of ceil(G / 64) groups, and looks into the run that
+// holds the item.
+constexpr int kBand = 8;
+constexpr int kTallest = BM / 32;
+static_assert(MOE_MAX_GROUPS <= 64 * 64, "one lane a run, one lane a group of a run");
+
+template <bool F32>
+__global__ __launch_bounds__(kThreads) void gemm_mxfp4_kernel(Fp4GemmArgs p) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int G = p.G, rows = p.rows, Kb = p.K / 2, S = (Kb + BK - 1) / BK;
+    const int NT = (p.N + BN - 1) / BN;
+    auto clamped = [&](int v) { return min(max(v, 0), rows); };
+    const int run = (G + 63) / 64;
+    // the row tiles of this lane's run, of up to 1 .. 4 blocks
+    int tiles[kTallest + 1] = {};
+    for (int i = 0; i < run; ++i) {
+        const int g = lane * run + i;
+        if (g < G) {
+            const int n = max(clamped(p.offsets[g + 1]) - clamped(p.offsets[g]), 0);
+#pragma unroll
+            for (int b = 1; b <= kTallest; ++b) tiles[b] += row_tiles(n, b);
+        }
+    }
+    int blocks = kTallest, mine = NT * tiles[kTallest], upto = wave_scan(mine, lane);
+    // few tiles: the lowest of which every one still has a CU of its own
+    if ((long long)rows * NT <= 96ll * gridDim.x &&
+        __builtin_amdgcn_readlane(upto, 63) < (int)gridDim.x) {
+#pragma unroll
+        for (int b = 1; b < kTallest; ++b) {
+            const int sum = wave_scan(NT * tiles[b], lane);
+            if (__builtin_amdgcn_readlane(sum, 63) > (int)gridDim.x) continue;
+            blocks = b;
+            mine = NT * tiles[b];
+            upto = sum;
+            break;
+        }
+    }
+    const long long Q = __builtin_amdgcn_readlane(upto, 63);
+    const int xcd = blockIdx.x & 7, step = gridDim.x >> 3;
+    const int end = (int)(Q * (xcd + 1) / 8);
+    auto find = [&](int q, Tile& t) {
+        // the first lane whose sum passes q, then the groups of its run in
+        // turn (scalar loads: a vector load would wait for the copies that are
+        // on their way)
+        const int r = __builtin_ctzll(__builtin_amdgcn_ballot_w64(upto > q));
+        int local = q - __builtin_amdgcn_readlane(upto - mine, r);
+        t.g = r * run;
+        int r0 = clamped(scalar_load(p.offsets + t.g)), n, mt;
+        for (;; ++t.g) {                             // (ends: the run holds item q)
+            const int r1 = clamped(scalar_load(p.offsets + t.g + 1));
+            n = max(r1 - r0, 0);
+            mt = row_tiles(n, blocks);
+            if (local < NT * mt || t.g + 1 >= G) break;
+            local -= NT * mt;
+            r0 = r1;
+        }
+        const int per = ((n + mt - 1) / mt + 31) & ~31;
+        const int band = local / (kBand * NT) * kBand, high = min(kBand, mt - band);
+        local -= band * NT;
+        t.n0 = local / high * BN;
+        t.row0 = r0 + (band + local % high) * per;
+        t.valid = min(per, r0 + n - t.row0);
+    };
+    // bytes that this thread's chunk of K's last stage reaches past K
+    const int past = max(0, (S - 1) * BK + 16 * ((tid & 7) ^ swz(tid >> 3)) + 16 - Kb);
+    int q = (int)(Q * xcd / 8) + (int)(blockIdx.x >> 3);
+    if (q >= end) return;
+    Tile t;
+    find(q, t);
+    {
+        Fetch f;
+        f.set(p, t);
+        f.first_stages(t.valid, S, past);
+    }
+    for (;;) {
+        const bool more = q + step < end;
+        Tile next = t;
+        if (more) find(q + step, next);
+        switch ((t.valid + 31) >> 5) {
+            case 1: run_tile<F32, 1>(p, t, next, more, past, smem); break;
+            case 2: run_tile<F32, 2>(p, t, next, more, past, smem); break;
+            case 3: run_tile<F32, 3>(p, t, next, more, past, smem); break;
+            default: run_tile<F32, 4>(p, t, next, more, past, smem); break;
+        }
+        if (!more) break;
+        t = next;
+        q += step;
+    }
+}
+
+template <bool F32>
+hipError_t launch(const Fp4GemmArgs& g, hipStream_t stream) {
+    static DeviceSetup setup;
+    long long grid = 0, unused = 0;
+    const hipError_t err =
+        device_setup(setup, grid, unused, [](int, long long& gr, long long&) {
+            gr = (device_cu_count() + 7) & ~7;
+            return hipFuncSetAttribute((const void*)gemm_mxfp4_kernel<F32>,
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+        });
+    if (err != hipSuccess) return err;
+    hipLaunchKernelGGL((gemm_mxfp4_kernel<F32>), dim3((unsigned)grid), dim3(kThreads), kLds, stream,
+                       g);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_grouped_gemm_mxfp4(bool f32, const Fp4GemmArgs& g, hipStream_t stream) {
-    const dim3 grid((unsigned)(g.rows / 32 + g.G), (unsigned)((g.N + 127) / 128));
-    if (f32) hipLaunchKernelGGL(gemm_mxfp4_kernel<true>, grid, dim3(256), 0, stream, g);
-    else hipLaunchKernelGGL(gemm_mxfp4_kernel<false>, grid, dim3(256), 0, stream, g);
-    return hipGetLastError();
+    if (g.K < 32 || g.K % 32 || g.N < 16 || g.N % 16 || g.G < 1) return hipErrorInvalidValue;
+    return f32 ? launch<true>(g, stream) : launch<false>(g, stream);
 }
 
 }  // namespace moe

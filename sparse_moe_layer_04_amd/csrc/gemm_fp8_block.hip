@@ -57,9 +57,7 @@
 // 0.98 to 1.04 ms with fp32 (cores and memory in turn).  Ten rows a group:
 // memory, 5.5 TB/s.  One row of each of few groups: the chain of K's blocks on
 // few CUs (12 groups x 4096 x 544: 36 tiles, 16 us with bf16, 25 with fp32).
-#include <type_traits>
-
-#include "fp8_block.h"
+#include "lds_ring.h"
 
 namespace moe {
 namespace {
@@ -75,58 +73,6 @@ constexpr int kRing = 3 * kSlot;
 constexpr int kMaxX = 8 * BM;              // SwiGLU: the waves' row exponents, a byte each
 constexpr int kLds = kRing + kMaxX;
 static_assert(kLds <= 160 * 1024 && kSlot % 128 == 0, "three slots of LDS");
-
-// Copies from memory into LDS that pass no register: lane l's 16 (4) bytes go
-// to LDS byte lds + 16 l (4 l), lds wave-uniform.  M0 carries the LDS address
-// when the copy issues (one wait state after the write); the compiler may
-// keep a value of its own there, so each block leaves M0 as it found it.  The
-// compiler does not count these copies: wait_vm does.
-__device__ __forceinline__ void copy16(u32x4 rsrc, int voffset, int soffset, int lds) {
-    const int at = __builtin_amdgcn_readfirstlane(lds);
-    soffset = __builtin_amdgcn_readfirstlane(soffset);
-    int saved;
-    asm volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %1\n\t"
-        "s_nop 0\n\t"
-        "buffer_load_dwordx4 %2, %3, %4 offen lds\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(saved)
-        : "s"(at), "v"(voffset), "s"(rsrc), "s"(soffset)
-        : "memory");
-}
-__device__ __forceinline__ void copy4(const void* from, int lds) {
-    const int at = __builtin_amdgcn_readfirstlane(lds);
-    int saved;
-    asm volatile(
-        "s_mov_b32 %0, m0\n\t"
-        "s_mov_b32 m0, %1\n\t"
-        "s_nop 0\n\t"
-        "global_load_lds_dword %2, off\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(saved)
-        : "s"(at), "v"(from)
-        : "memory");
-}
-// at most N of this wave's memory operations outstanding
-template <int N>
-__device__ __forceinline__ void wait_vm() {
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
-
-// Buffer resource over [base, base + bytes), wave-uniform (read from the
-// first lane, so that it lives in scalar registers)
-__device__ __forceinline__ u32x4 uniform_rsrc(const void* base, size_t bytes) {
-    const uint64_t p = (uint64_t)(uintptr_t)base;
-    u32x4 r;
-    r[0] = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)p);
-    r[1] = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32)) & 0xffffu;
-    r[2] = (uint32_t)__builtin_amdgcn_readfirstlane((int)min(bytes, (size_t)0x7fffffff));
-    r[3] = 0x00020000u;
-    return r;
-}
 
 struct Tile {
     int g, row0, valid, n0;                // n0: first weight row (SwiGLU: feature)
@@ -215,15 +161,6 @@ struct Fetch {
         else first<3>(S, past);
     }
 };
-
-// f(integral_constant<int, I>()) for I in [I0, I1)
-template <int I0, int I1, class F>
-__device__ __forceinline__ void static_for(const F& f) {
-    if constexpr (I0 < I1) {
-        f(std::integral_constant<int, I0>());
-        static_for<I0 + 1, I1>(f);
-    }
-}
 
 // The stages of a tile of five blocks of rows (its registers do not hold two
 // sets of operands): the same steps, taken a product at a time, the operands
@@ -706,17 +643,6 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t, co
                 p.out_scale[(size_t)(t.row0 + r) * nbf + t.n0 / 128] = pow2(X);
         }
     }
-}
-
-// *p for a wave-uniform p
-__device__ __forceinline__ int scalar_load(const int32_t* p) {
-    const uint64_t a = (uint64_t)(uintptr_t)p;
-    const uint64_t u = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a) |
-                       (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32))
-                           << 32;
-    int v;
-    asm volatile("s_load_dword %0, %1, 0x0\n\ts_waitcnt lgkmcnt(0)" : "=s"(v) : "s"(u));
-    return v;
 }
 
 // Row tiles of a group of n rows, tiles of up to `blocks` blocks of 32 rows.
