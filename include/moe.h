@@ -398,7 +398,7 @@ int moe_expert_ffn_fp8_block(const uint8_t* a8, const float* a_scale, const int3
  *   fp32 (MOE_IN_F32); res_out [rows, d]; y [rows, d] bf16 or NULL; codes
  *   [rows, d] and scales [rows, ceil(d / 128)] fp32, or both NULL; y or codes
  *   is given.  eps >= 0 and finite.  d a multiple of 8 (with codes of 16), up
- *   to 32768; all 16-byte aligned but scales (4).  y, codes and scales overlap
+ *   to 16384; all 16-byte aligned but scales (4).  y, codes and scales overlap
  *   no input.
  */
 int moe_add_rms_norm(const void* x, int x_dtype, const void* residual, int res_dtype,

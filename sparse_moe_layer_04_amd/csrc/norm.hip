@@ -7,6 +7,8 @@
 // the root and s / root are held in 64 bits: no sum overflows or vanishes
 // (|s| up to the type's largest), and y comes out the same bits for any order
 // of the sum, so that codes and scales next to a border do too.
+#include <type_traits>
+
 #include "step.h"
 
 namespace moe {
@@ -23,87 +25,102 @@ __device__ __forceinline__ long long workgroup() {
     return (long long)blockIdx.y * gridDim.x + blockIdx.x;
 }
 
-// W waves a row (blockDim.x / 64 of them, or 1 with a row for every wave of
-// the workgroup), NC chunks of 8 values a lane: chunk c of lane l of the row's
-// wave w holds values 8 (64 (W c + w) + l) + (0 .. 7), so 16 lanes hold a
-// block of 128.
-template <int NC, bool ONE>
+// eight weights at i
+__device__ __forceinline__ void load_w(const void* w, bool f32, int i, float (&v)[8]) {
+    if (f32) {
+        Raw8<true> r;
+        r.load(w, i);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = r.get(j);
+    } else {
+        Raw8<false> r;
+        r.load(w, i);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = r.get(j);
+    }
+}
+
+enum Res : int { RES_NONE = 0, RES_BF16 = 1, RES_F32 = 2 };
+
+// W waves a row (those of the workgroup; or ONE, a row for every wave), NC
+// chunks of 8 values a lane: chunk c of lane l of the row's wave w holds values
+// 8 (64 (W c + w) + l) + (0 .. 7), so 16 lanes hold a block of 128.  (Lanes
+// past d load the row's start, so that no load stands behind a branch.)
+template <bool XF32, int RES, int NC, bool ONE>
 __global__ __launch_bounds__(ONE ? 256 : 1024) void add_rms_norm_kernel(NormArgs p) {
     __shared__ double part[ONE ? 1 : 16];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int W = ONE ? 1 : (int)(blockDim.x >> 6), d = p.d;
+    const int W = ONE ? 1 : (int)(blockDim.x >> 6), d = p.d, nb = (d + 127) / 128;
     const long long row = ONE ? workgroup() * 4 + wave : workgroup();
     if (row >= p.rows) return;
-    const size_t at = (size_t)row * d;
     const int first = 8 * ((ONE ? 0 : wave * 64) + lane), step = 512 * W;
-    float s[NC][8];
+    int at[NC];
+    bool in[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-        const int i = first + c * step;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[c][j] = 0.0f;
-        if (i < d) load8(p.x, at + i, p.x_f32, s[c]);
+        in[c] = first + c * step < d;
+        at[c] = in[c] ? first + c * step : 0;
     }
-    if (p.res) {
-        float r[NC][8];
+    Raw8<XF32> x[NC];
+    Raw8<RES == RES_F32> r[NC];
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-            if (first + c * step < d) load8(p.res, at + first + c * step, p.res_f32, r[c]);
+    for (int c = 0; c < NC; ++c) x[c].load(p.x, (size_t)row * d + at[c]);
+    if constexpr (RES != RES_NONE)
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const int i = first + c * step;
-            if (i >= d) continue;
+        for (int c = 0; c < NC; ++c) r[c].load(p.res, (size_t)row * d + at[c]);
+    float w[NC][8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s[c][j] += r[c][j];
-            if (!p.res_f32) {
-                const u32x4 b = bf16_pack8(s[c]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    s[c][2 * j] = __uint_as_float(b[j] << 16);
-                    s[c][2 * j + 1] = __uint_as_float(b[j] & 0xffff0000u);
-                }
-                *(u32x4*)((uint16_t*)p.res_out + at + i) = b;
-            } else {
-                store8(p.res_out, at + i, true, s[c]);
-            }
-        }
-    }
+    for (int c = 0; c < NC; ++c) load_w(p.w, p.w_f32, at[c], w[c]);
+    float s[NC][8];
     double sum = 0.0;
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
+    for (int c = 0; c < NC; ++c) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum = __builtin_fma((double)s[c][j], (double)s[c][j], sum);
+        for (int j = 0; j < 8; ++j) {
+            s[c][j] = x[c].get(j);
+            if constexpr (RES != RES_NONE) s[c][j] += r[c].get(j);
+        }
+        const size_t to = (size_t)row * d + at[c];
+        if constexpr (RES == RES_BF16) {
+            Raw8<false> b;
+            b.v[0] = bf16_pack8(s[c]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[c][j] = b.get(j);
+            if (in[c]) *(u32x4*)((uint16_t*)p.res_out + to) = b.v[0];
+        }
+        if constexpr (RES == RES_F32)
+            if (in[c]) store8(p.res_out, to, true, s[c]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const double v = in[c] ? (double)s[c][j] : 0.0;
+            sum = __builtin_fma(v, v, sum);
+        }
+    }
     sum = wave_sum(sum);
     if constexpr (!ONE) {
         if (lane == 0) part[wave] = sum;
         __syncthreads();
         sum = part[0];
-        for (int w = 1; w < W; ++w) sum += part[w];
+        for (int v = 1; v < W; ++v) sum += part[v];
     }
     const double rstd = 1.0 / __builtin_sqrt(sum / d + p.eps);
-    const int nb = (d + 127) / 128;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-        const int i = first + c * step;
-        const bool in = i < d;
-        float w[8];
+        const size_t to = (size_t)row * d + at[c];
+        float y[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = 0.0f;
-        if (in) load8(p.w, i, p.w_f32, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] *= (float)((double)s[c][j] * rstd);
-        if (in && p.y) store8(p.y, at + i, false, w);
+        for (int j = 0; j < 8; ++j) y[j] = w[c][j] * (float)((double)s[c][j] * rstd);
+        if (p.y && in[c]) store8(p.y, to, false, y);
         if (p.codes) {
             float m = 0.0f;
-            if (in)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) m = fmaxf(m, finite_abs(w[j]));
-            const int X = block_exponent(row16_max(m));
+            for (int j = 0; j < 8; ++j) m = fmaxf(m, finite_abs(y[j]));
+            const int X = block_exponent(row16_max(in[c] ? m : 0.0f));
             const float inv = pow2(-X);
-            if (in) {
-                *(u32x2*)(p.codes + at + i) = u32x2{e4m3_pack4(w[0], w[1], w[2], w[3], inv),
-                                                    e4m3_pack4(w[4], w[5], w[6], w[7], inv)};
-                if ((lane & 15) == 0) p.scales[(size_t)row * nb + i / 128] = pow2(X);
+            if (in[c]) {
+                *(u32x2*)(p.codes + to) = u32x2{e4m3_pack4(y[0], y[1], y[2], y[3], inv),
+                                                e4m3_pack4(y[4], y[5], y[6], y[7], inv)};
+                if ((lane & 15) == 0) p.scales[(size_t)row * nb + at[c] / 128] = pow2(X);
             }
         }
     }
@@ -117,7 +134,7 @@ __global__ __launch_bounds__(ONE ? 256 : 1024) void add_rms_norm_kernel(NormArgs
 // workgroup takes rows t, t + stride, ... and keeps its columns' dw in
 // registers (fp32, at most a few dozen terms each); its sums go to a row of
 // `part`, which the second kernel adds up (64 bits), always in the same order.
-template <int NC, bool ONE>
+template <bool SF32, bool GF32, int RES, int NC, bool ONE>
 __global__ __launch_bounds__(ONE ? 256 : 1024) void rms_norm_backward_kernel(NormBwdArgs p) {
     __shared__ double part[2][ONE ? 1 : 16][2];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -125,36 +142,45 @@ __global__ __launch_bounds__(ONE ? 256 : 1024) void rms_norm_backward_kernel(Nor
     const long long slot = ONE ? (long long)blockIdx.x * 4 + wave : (long long)blockIdx.x;
     const long long stride = ONE ? (long long)gridDim.x * 4 : (long long)gridDim.x;
     const int first = 8 * ((ONE ? 0 : wave * 64) + lane), step = 512 * W;
+    int at[NC];
+    bool in[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        in[c] = first + c * step < d;
+        at[c] = in[c] ? first + c * step : 0;
+    }
+    Raw8<SF32> s[NC];
+    Raw8<GF32> g[NC];
+    Raw8<RES == RES_F32> r[NC];
+    auto load = [&](long long t) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            s[c].load(p.s, (size_t)t * d + at[c]);
+            g[c].load(p.dy, (size_t)t * d + at[c]);
+            if constexpr (RES != RES_NONE) r[c].load(p.d_res, (size_t)t * d + at[c]);
+        }
+    };
+    if (slot < p.rows) load(slot);
     float dw[NC][8], w[NC][8];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
+        load_w(p.w, p.w_f32, at[c], w[c]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dw[c][j] = 0.0f, w[c][j] = 0.0f;
-        if (first + c * step < d) load8(p.w, first + c * step, p.w_f32, w[c]);
+        for (int j = 0; j < 8; ++j) {
+            dw[c][j] = 0.0f;
+            w[c][j] = in[c] ? w[c][j] : 0.0f;    // (lanes past d add nothing)
+        }
     }
     int turn = 0;
     for (long long row = slot; row < p.rows; row += stride, turn ^= 1) {
-        const size_t at = (size_t)row * d;
-        float s[NC][8], dy[NC][8], r[NC][8];
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const int i = first + c * step;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) s[c][j] = 0.0f, dy[c][j] = 0.0f, r[c][j] = 0.0f;
-            if (i < d) {
-                load8(p.s, at + i, p.s_f32, s[c]);
-                load8(p.dy, at + i, p.dy_f32, dy[c]);
-                if (p.d_res) load8(p.d_res, at + i, p.res_f32, r[c]);
-            }
-        }
         double ss = 0.0, gs = 0.0;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const double v = s[c][j];
+                const double v = in[c] ? (double)s[c].get(j) : 0.0;
                 ss = __builtin_fma(v, v, ss);
-                gs = __builtin_fma((double)dy[c][j] * (double)w[c][j], v, gs);
+                gs = __builtin_fma((double)g[c].get(j) * (double)w[c][j], v, gs);
             }
         ss = wave_sum(ss);
         gs = wave_sum(gs);
@@ -170,108 +196,157 @@ __global__ __launch_bounds__(ONE ? 256 : 1024) void rms_norm_backward_kernel(Nor
         const double along = gs / d * rstd * rstd * rstd;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const int i = first + c * step;
             float out[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const double g = (double)dy[c][j] * (double)w[c][j];
-                out[j] = (float)__builtin_fma(g, rstd,
-                                              __builtin_fma(-along, (double)s[c][j],
-                                                            (double)r[c][j]));
-                dw[c][j] = __builtin_fmaf(dy[c][j], (float)((double)s[c][j] * rstd), dw[c][j]);
+                const float dy = g[c].get(j);
+                const double v = s[c].get(j);
+                double o = RES == RES_NONE ? 0.0 : (double)r[c].get(j);
+                o = __builtin_fma(-along, v, o);
+                out[j] = (float)__builtin_fma((double)dy * (double)w[c][j], rstd, o);
+                dw[c][j] = __builtin_fmaf(dy, (float)(v * rstd), dw[c][j]);
             }
-            if (i < d) store8(p.dx, at + i, p.dx_f32, out);
+            if (in[c]) store8(p.dx, (size_t)row * d + at[c], p.dx_f32, out);
         }
+        if (row + stride < p.rows) load(row + stride);
     }
 #pragma unroll
     for (int c = 0; c < NC; ++c)
-        if (first + c * step < d)
-            store8(p.part, (size_t)slot * d + first + c * step, true, dw[c]);
+        if (in[c]) store8(p.part, (size_t)slot * d + at[c], true, dw[c]);
 }
 
-// dw[c] = sum of part[., c]: 32 columns a workgroup, its 32 groups of 8 lanes
-// take rows 32 apart
+// dw[c] = sum of part[., c]: 16 columns a workgroup, its 64 groups of 4 lanes
+// take rows 64 apart, eight loads in flight
 __global__ __launch_bounds__(256) void norm_dw_kernel(const float* __restrict__ part, int parts,
                                                       int d, float* __restrict__ dw) {
-    __shared__ double sum[32][33];
-    const int li = threadIdx.x & 7, r0 = threadIdx.x >> 3, c = blockIdx.x * 32 + li * 4;
+    __shared__ double sum[64][17];
+    const int li = threadIdx.x & 3, r0 = threadIdx.x >> 2, c = blockIdx.x * 16 + li * 4;
+    const float* from = part + (c < d ? c : 0);
     double a[4] = {0.0, 0.0, 0.0, 0.0};
-    if (c < d)
-        for (int r = r0; r < parts; r += 32) {
-            const f32x4 v = *(const f32x4*)(part + (size_t)r * d + c);
+    for (int r = r0; r < parts; r += 64 * 8) {
+        f32x4 v[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) a[j] += (double)v[j];
-        }
+        for (int u = 0; u < 8; ++u)
+            v[u] = *(const f32x4*)(from + (size_t)min(r + 64 * u, parts - 1) * d);
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) a[j] += r + 64 * u < parts ? (double)v[u][j] : 0.0;
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) sum[r0][li * 4 + j] = a[j];
     __syncthreads();
-    if (threadIdx.x < 32 && blockIdx.x * 32 + threadIdx.x < d) {
-        double v = 0.0;
-        for (int r = 0; r < 32; ++r) v += sum[r][threadIdx.x];
-        dw[blockIdx.x * 32 + threadIdx.x] = (float)v;
+    // 16 threads a column, then one
+    const int col = threadIdx.x & 15, q = threadIdx.x >> 4;
+    double v = 0.0;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v += sum[4 * q + r][col];
+    __syncthreads();
+    sum[q][col] = v;
+    __syncthreads();
+    if (threadIdx.x < 16 && blockIdx.x * 16 + threadIdx.x < d) {
+        v = 0.0;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) v += sum[r][threadIdx.x];
+        dw[blockIdx.x * 16 + threadIdx.x] = (float)v;
     }
+}
+
+// chunks a lane and waves a row
+struct Shape {
+    bool one;                          // a wave a row
+    int chunks, threads;
+};
+Shape shape_of(int d, int chunks) {
+    const int n = (d + 511) / 512;     // chunks of a row, a wave each
+    Shape s;
+    s.one = n <= chunks;
+    s.chunks = s.one ? n : n <= 16 * chunks ? chunks : 2;
+    s.threads = s.one ? 256 : 64 * ((n + s.chunks - 1) / s.chunks);
+    return s;
+}
+
+template <bool XF32, int RES>
+void launch_norm(const NormArgs& p, const Shape& s, dim3 grid, hipStream_t stream) {
+#define MOE_NORM(NC, ONE)                                                                      \
+    hipLaunchKernelGGL((add_rms_norm_kernel<XF32, RES, NC, ONE>), grid, dim3(s.threads), 0,    \
+                       stream, p)
+    if (s.one && s.chunks == 1) MOE_NORM(1, true);
+    else if (s.one) MOE_NORM(2, true);
+    else if (s.chunks == 1) MOE_NORM(1, false);
+    else MOE_NORM(2, false);
+#undef MOE_NORM
+}
+
+template <bool SF32, bool GF32, int RES>
+void launch_backward(const NormBwdArgs& p, const Shape& s, dim3 grid, hipStream_t stream) {
+#define MOE_NORM(NC, ONE)                                                                      \
+    hipLaunchKernelGGL((rms_norm_backward_kernel<SF32, GF32, RES, NC, ONE>), grid,             \
+                       dim3(s.threads), 0, stream, p)
+    if (s.one && s.chunks == 1) MOE_NORM(1, true);
+    else if (s.one) MOE_NORM(2, true);
+    else if (s.chunks == 1) MOE_NORM(1, false);
+    else MOE_NORM(2, false);
+#undef MOE_NORM
+}
+
+// Rows of the backward's `part`: as many workgroups as are resident at once, 8
+// waves for each of 512.  8192 x 4096, fp32: 92 us with 512, 97 with 1024 (half
+// of them wait), 101 with 256; 8191 x 1024 (a wave a row): 28.5 us with 1024
+// waves, 38 with 2048 (more partial sums).
+constexpr int kNormParts = 512;
+
+Shape backward_shape(int d) { return shape_of(d, 1); }
+int backward_parts(long long rows, const Shape& s) {
+    const long long most = s.one ? (rows + 3) / 4 * 4 : rows;
+    const long long parts = s.one ? 2 * kNormParts : s.threads <= 256 ? 2 * kNormParts : kNormParts;
+    return (int)(most < parts ? most : parts);
 }
 
 }  // namespace
 
 hipError_t launch_add_rms_norm(const NormArgs& p, hipStream_t stream) {
     if (p.rows == 0) return hipSuccess;
-    const int chunks = (p.d + 511) / 512;          // of a wave
-    const bool many = p.rows >= 1024 && chunks <= 8;
-    if (many || chunks == 1) {
-        const dim3 grid = grid_of((p.rows + 3) / 4);
-        if (chunks <= 1) hipLaunchKernelGGL((add_rms_norm_kernel<1, true>), grid, dim3(256), 0, stream, p);
-        else if (chunks <= 2) hipLaunchKernelGGL((add_rms_norm_kernel<2, true>), grid, dim3(256), 0, stream, p);
-        else if (chunks <= 4) hipLaunchKernelGGL((add_rms_norm_kernel<4, true>), grid, dim3(256), 0, stream, p);
-        else hipLaunchKernelGGL((add_rms_norm_kernel<8, true>), grid, dim3(256), 0, stream, p);
+    // two chunks a lane where there are rows for every CU (8191 x 4096 bf16 24.4
+    // -> 21.8 us), one where a row's chain of waits is what counts
+    const Shape s = shape_of(p.d, p.rows < 1024 ? 1 : 2);
+    const dim3 grid = grid_of(s.one ? (p.rows + 3) / 4 : p.rows);
+    const int res = !p.res ? RES_NONE : p.res_f32 ? RES_F32 : RES_BF16;
+    if (p.x_f32) {
+        if (res == RES_NONE) launch_norm<true, RES_NONE>(p, s, grid, stream);
+        else if (res == RES_BF16) launch_norm<true, RES_BF16>(p, s, grid, stream);
+        else launch_norm<true, RES_F32>(p, s, grid, stream);
     } else {
-        const dim3 grid = grid_of(p.rows);
-        if (chunks <= 16) hipLaunchKernelGGL((add_rms_norm_kernel<1, false>), grid, dim3(64 * chunks), 0, stream, p);
-        else if (chunks <= 32) hipLaunchKernelGGL((add_rms_norm_kernel<2, false>), grid, dim3(64 * ((chunks + 1) / 2)), 0, stream, p);
-        else hipLaunchKernelGGL((add_rms_norm_kernel<4, false>), grid, dim3(64 * ((chunks + 3) / 4)), 0, stream, p);
+        if (res == RES_NONE) launch_norm<false, RES_NONE>(p, s, grid, stream);
+        else if (res == RES_BF16) launch_norm<false, RES_BF16>(p, s, grid, stream);
+        else launch_norm<false, RES_F32>(p, s, grid, stream);
     }
     return hipGetLastError();
 }
 
-namespace {
-constexpr int kNormParts = 1024;       // rows of `part`, at most
-struct NormBwdShape {
-    bool one;                          // a wave a row
-    int threads, chunks;               // chunks a lane
-    int parts;
-};
-NormBwdShape norm_bwd_shape(long long rows, int d) {
-    const int waves = (d + 511) / 512;
-    NormBwdShape s;
-    s.one = waves <= 2;
-    s.chunks = s.one ? waves : waves <= 16 ? 1 : waves <= 32 ? 2 : 4;
-    if (!s.one && waves > 4 && waves <= 16) s.chunks = 2;
-    s.threads = s.one ? 256 : 64 * ((waves + s.chunks - 1) / s.chunks);
-    const long long most = s.one ? (rows + 3) / 4 * 4 : rows;
-    s.parts = (int)(most < kNormParts ? most : kNormParts);
-    return s;
-}
-}  // namespace
-
-int norm_backward_parts(long long rows, int d) { return norm_bwd_shape(rows, d).parts; }
+int norm_backward_parts(long long rows, int d) { return backward_parts(rows, backward_shape(d)); }
 
 hipError_t launch_rms_norm_backward(const NormBwdArgs& p, hipStream_t stream) {
-    const NormBwdShape s = norm_bwd_shape(p.rows, p.d);
-    if (s.parts > 0) {
-        const dim3 grid((unsigned)(s.one ? s.parts / 4 : s.parts)), block(s.threads);
-        if (s.one) {
-            if (s.chunks == 1) hipLaunchKernelGGL((rms_norm_backward_kernel<1, true>), grid, block, 0, stream, p);
-            else hipLaunchKernelGGL((rms_norm_backward_kernel<2, true>), grid, block, 0, stream, p);
-        } else if (s.chunks == 1) {
-            hipLaunchKernelGGL((rms_norm_backward_kernel<1, false>), grid, block, 0, stream, p);
-        } else if (s.chunks == 2) {
-            hipLaunchKernelGGL((rms_norm_backward_kernel<2, false>), grid, block, 0, stream, p);
-        } else {
-            hipLaunchKernelGGL((rms_norm_backward_kernel<4, false>), grid, block, 0, stream, p);
-        }
+    const Shape s = backward_shape(p.d);
+    const int parts = backward_parts(p.rows, s);
+    if (parts > 0) {
+        const dim3 grid((unsigned)(s.one ? parts / 4 : parts));
+        const int res = !p.d_res ? RES_NONE : p.res_f32 ? RES_F32 : RES_BF16;
+        auto by_res = [&](auto sf, auto gf) {
+            constexpr bool S = decltype(sf)::value, G = decltype(gf)::value;
+            if (res == RES_NONE) launch_backward<S, G, RES_NONE>(p, s, grid, stream);
+            else if (res == RES_BF16) launch_backward<S, G, RES_BF16>(p, s, grid, stream);
+            else launch_backward<S, G, RES_F32>(p, s, grid, stream);
+        };
+        using std::false_type;
+        using std::true_type;
+        if (p.s_f32 && p.dy_f32) by_res(true_type(), true_type());
+        else if (p.s_f32) by_res(true_type(), false_type());
+        else if (p.dy_f32) by_res(false_type(), true_type());
+        else by_res(false_type(), false_type());
     }
-    hipLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)((p.d + 31) / 32)), dim3(256), 0, stream,
-                       p.part, s.parts, p.d, p.dw);
+    hipLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)((p.d + 15) / 16)), dim3(256), 0, stream,
+                       p.part, parts, p.d, p.dw);
     return hipGetLastError();
 }
 

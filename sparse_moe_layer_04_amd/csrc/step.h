@@ -32,22 +32,22 @@ __device__ __forceinline__ double wave_sum(double v) {
     return __builtin_bit_cast(double, (uint64_t)(uint32_t)lo | (uint64_t)(uint32_t)hi << 32);
 }
 
-// eight values of a row in bf16 (16 bytes) or fp32 (32 bytes)
-__device__ __forceinline__ void load8(const void* p, size_t at, bool f32, float (&v)[8]) {
-    if (f32) {
-        const f32x4 a = *(const f32x4*)((const float*)p + at);
-        const f32x4 b = *(const f32x4*)((const float*)p + at + 4);
+// Eight values of a row in bf16 (16 bytes) or fp32 (32 bytes) as they are in
+// memory: loads of several rows are issued together and converted later.
+template <bool F32>
+struct Raw8 {
+    u32x4 v[F32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void* p, size_t at) {
+        const u32x4* q = (const u32x4*)((const uint8_t*)p + at * (F32 ? 4 : 2));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
-    } else {
-        const u32x4 w = *(const u32x4*)((const uint16_t*)p + at);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+        for (int i = 0; i < (F32 ? 2 : 1); ++i) v[i] = q[i];
     }
-}
+    __device__ __forceinline__ float get(int j) const {
+        if constexpr (F32) return __uint_as_float(v[j >> 2][j & 3]);
+        const uint32_t u = v[0][j >> 1];
+        return __uint_as_float(j & 1 ? u & 0xffff0000u : u << 16);
+    }
+};
 __device__ __forceinline__ u32x4 bf16_pack8(const float (&v)[8]) {
     return u32x4{bf16_pack2(v[0], v[1]), bf16_pack2(v[2], v[3]), bf16_pack2(v[4], v[5]),
                  bf16_pack2(v[6], v[7])};
@@ -63,7 +63,7 @@ __device__ __forceinline__ void store8(void* p, size_t at, bool f32, const float
 
 // ----------------------------------------------------------------- host -----
 // largest row of the norm
-constexpr int kNormMaxD = 32768;
+constexpr int kNormMaxD = 16384;
 
 struct NormArgs {
     const void* x;       // [rows, d]

@@ -720,7 +720,7 @@ def add_rms_norm(x, w, residual=None, eps=1e-6, fp8=False, want_y=True, res=None
     bf16 or fp32.  Returns (s, y, codes, scales): s = x without a residual; y
     bf16, None without want_y; with fp8 the E4M3 codes of the fp32 y and their
     scales of 128 values as expert_ffn_fp8_block takes them, else None.  d is a
-    multiple of 8 (with fp8 of 16) up to 32768; res may be the residual (or x)
+    multiple of 8 (with fp8 of 16) up to 16384; res may be the residual (or x)
     itself, to update the stream in place."""
     xt = _any_dtype(x, "x", dims=2)
     rows, d = x.shape

@@ -26,7 +26,7 @@ def test_add_rms_norm(L):
     assert f(rows=1 << 31) == ERR_SHAPE
     assert f(d=0) == ERR_SHAPE
     assert f(d=12) == ERR_UNSUPPORTED
-    assert f(d=32776) == ERR_UNSUPPORTED
+    assert f(d=16392) == ERR_UNSUPPORTED
     assert f(d=24) == ERR_UNSUPPORTED                  # codes: a multiple of 16
     assert f(eps=-1e-6) == ERR_SHAPE
     assert f(eps=NAN) == ERR_SHAPE
@@ -47,7 +47,7 @@ def test_add_rms_norm(L):
 
 def test_rms_norm_backward(L):
     size = L.moe_rms_norm_backward_workspace_size
-    assert size(-1, 128) == size(4, 0) == size(4, 12) == size(4, 32776) == 0
+    assert size(-1, 128) == size(4, 0) == size(4, 12) == size(4, 16392) == 0
     assert size(0, 8) >= 32 and size(10 ** 6, 4096) >= 4096 * 4
     need = size(4, 128)
 

@@ -93,7 +93,7 @@ def check_norm(x, r, w, eps=1e-6, fp8=True, want_y=True, inplace=False):
 
 
 @pytest.mark.parametrize("d", [16, 64, 112, 128, 144, 512, 528, 1024, 2000, 4096, 4112, 8192,
-                               16384, 32768])
+                               9008, 16384])
 @pytest.mark.parametrize("rows", [1, 3, 1029])
 def test_norm_sizes(rows, d):
     if rows > 100 and d > 8192:
@@ -185,7 +185,7 @@ def check_backward(rows, d, st=F32, wt=F32, gt=F32, rt=F32, xt=F32, eps=1e-6, se
     near(gw, dw, (rows + 2) * 2.0 ** -24 * dmag + TINY[F32], "dw")
 
 
-@pytest.mark.parametrize("d", [8, 64, 520, 1024, 1032, 2056, 4096, 4104, 8192, 9000, 32768])
+@pytest.mark.parametrize("d", [8, 64, 520, 1024, 1032, 2056, 4096, 4104, 8192, 9000, 16384])
 @pytest.mark.parametrize("rows", [1, 5, 1031])
 def test_backward_sizes(rows, d):
     check_backward(min(rows, 67) if d > 8192 else rows, d)
