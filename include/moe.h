@@ -438,9 +438,10 @@ int moe_rms_norm_backward(const void* s, int s_dtype, const void* w, int w_dtype
  *   with S = 1: all tokens); modality, mask [T] u8 or NULL; loss [S, C] fp32,
  *   counts [S, C, E] int32 (written).  Same limits on E and k as moe_route
  *   (k > E is allowed: hash tables may repeat an expert); 1 <= S <= 2^20.  ws:
- *   moe_balance_loss_workspace_size(T) bytes, 256-byte aligned (NULL with 0).
+ *   moe_balance_loss_workspace_size(T, E, S, C) bytes (0 for sizes outside the
+ *   limits), 256-byte aligned; nothing in it needs to start at zero.
  */
-size_t moe_balance_loss_workspace_size(int T);
+size_t moe_balance_loss_workspace_size(int T, int E, int S, int classes);
 int moe_balance_loss(const float* logits, const int32_t* topk_ids, const int32_t* offsets,
                      const uint8_t* modality, const uint8_t* mask, int T, int E, int k, int S,
                      float* loss, int32_t* counts, uint32_t* d_flags, void* ws, size_t ws_bytes,

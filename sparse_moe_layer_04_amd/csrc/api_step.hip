@@ -127,8 +127,14 @@ int moe_rms_norm_backward(const void* s, int s_dtype, const void* w, int w_dtype
     return hip_status(launch_rms_norm_backward(p, (hipStream_t)stream));
 }
 
-size_t moe_balance_loss_workspace_size(int T) {
-    return T > 0 ? align256((size_t)T * sizeof(float)) : 0;
+size_t moe_balance_loss_workspace_size(int T, int E, int S, int classes) {
+    if (balance_shape(T, E, 1, S) != MOE_OK || classes < 1 || classes > 2) return 0;
+    BalanceArgs p{};
+    p.T = T;
+    p.E = E;
+    p.S = S;
+    p.C = classes;
+    return balance_layout(p, nullptr);
 }
 
 int moe_balance_loss(const float* logits, const int32_t* topk_ids, const int32_t* offsets,
@@ -138,9 +144,7 @@ int moe_balance_loss(const float* logits, const int32_t* topk_ids, const int32_t
     const int st = balance_shape(T, E, k, S);
     if (st != MOE_OK) return st;
     if (!offsets && S != 1) return MOE_ERR_NULL;
-    if (!loss || !counts || (T > 0 && (!logits || !topk_ids || !ws))) return MOE_ERR_NULL;
-    if (!aligned(ws, 256) || ws_bytes < moe_balance_loss_workspace_size(T))
-        return MOE_ERR_WORKSPACE;
+    if (!loss || !counts || !ws || (T > 0 && (!logits || !topk_ids))) return MOE_ERR_NULL;
     BalanceArgs p{};
     p.logits = logits;
     p.ids = topk_ids;
@@ -154,7 +158,7 @@ int moe_balance_loss(const float* logits, const int32_t* topk_ids, const int32_t
     p.C = modality ? 2 : 1;
     p.counts = counts;
     p.loss = loss;
-    p.q = (float*)ws;
+    if (!aligned(ws, 256) || ws_bytes < balance_layout(p, (char*)ws)) return MOE_ERR_WORKSPACE;
     p.flags = d_flags;
     return hip_status(launch_balance_loss(p, (hipStream_t)stream));
 }

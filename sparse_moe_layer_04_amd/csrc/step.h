@@ -105,13 +105,18 @@ struct BalanceArgs {
     int T, E, k, S, C;       // C: classes of tokens (2 with a modality)
     int32_t* counts;         // [S, C, E]
     float* loss;             // [S, C]
-    float* q;                // [T] workspace: sum_e c_e s_e / sum_e s_e, -1 where
-                             // the token takes no part
+    int chunk;               // tokens of a chunk
+    float* piece_sum;        // workspace: [chunks + S, C, E] sums of normalised scores
+    int* piece_num;          // and pairs of the pieces
+    double* part;            // [S, slices, 2, 2]
+    int* ticket;             // [S]
     uint32_t* flags;
     const float* d_loss;     // [S, C] (gradient)
     const float* add;        // [T, E] or NULL
     float* d_logits;         // [T, E]
 };
+// lays the workspace out (sizes are set; base may be NULL): its bytes
+size_t balance_layout(BalanceArgs& p, char* base);
 hipError_t launch_balance_loss(const BalanceArgs& p, hipStream_t stream);
 hipError_t launch_balance_loss_backward(const BalanceArgs& p, hipStream_t stream);
 

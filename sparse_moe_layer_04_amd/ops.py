@@ -6,6 +6,7 @@ no fallback: if the library is missing or a call fails, an exception is
 raised.
 """
 import ctypes
+import functools
 import os
 import re
 
@@ -141,7 +142,7 @@ def lib():
     L.moe_rms_norm_backward_workspace_size.argtypes = [LL, I]
     L.moe_rms_norm_backward_workspace_size.restype = S
     L.moe_rms_norm_backward.argtypes = [P, I, P, I, P, I, P, I, LL, I, D, P, I, P, P, S, P]
-    L.moe_balance_loss_workspace_size.argtypes = [I]
+    L.moe_balance_loss_workspace_size.argtypes = [I, I, I, I]
     L.moe_balance_loss_workspace_size.restype = S
     L.moe_balance_loss.argtypes = [P, P, P, P, P, I, I, I, I, P, P, P, P, S, P]
     L.moe_balance_loss_backward.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, P, P]
@@ -698,19 +699,49 @@ def expert_ffn_fp8_block(a8, a_scale, offsets, w_gate, w_up, w_down, clamp_limit
     return h8, h_scale, y
 
 
-def _here(t, *others):
-    """All tensors on the current device, whose stream the call goes to."""
-    dev = torch._C._cuda_getDevice()
-    for u in (t,) + others:
-        if u is not None and u.get_device() != dev:
-            raise MoeError(f"tensors must be on the current device (cuda:{dev}), got {u.device}")
+_IN_TYPES = {torch.bfloat16: IN_BF16, torch.float32: IN_F32}
 
 
-def _any_dtype(t, name, shape=None, dims=None):
-    """A bf16 or fp32 tensor: returns its MOE_IN_* type."""
-    dt = _in_dtype(t, name)
-    _need(t, t.dtype, name, dims, shape)
+def _device(t, name):
+    """The device of a call's first tensor: the current one, whose stream the
+    call goes to."""
+    if t is None:
+        raise MoeError(f"{name} is required")
+    dev = t.get_device()
+    if dev < 0:
+        raise MoeError(f"{name} must be a device tensor")
+    if dev != torch._C._cuda_getDevice():
+        raise MoeError(f"{name} must be on the current device, got {t.device}")
+    return dev
+
+
+def _on(t, dev, dtype, name, shape):
+    """_need of a tensor on device `dev`: the checks that pass cost a third of a
+    microsecond, what is wrong is found and named after one fails."""
+    if (t is None or t.dtype != dtype or t.get_device() != dev or t.shape != shape
+            or not t.is_contiguous()):
+        _need(t, dtype, name, shape=shape)
+        raise MoeError(f"{name} must be on the current device (cuda:{dev}), got {t.device}")
+    return t
+
+
+def _typed(t, dev, name, shape):
+    """_on for bf16 or fp32: returns the tensor's MOE_IN_* type."""
+    dt = None if t is None else _IN_TYPES.get(t.dtype)
+    if dt is None:
+        _in_dtype(t, name)
+    _on(t, dev, t.dtype, name, shape)
     return dt
+
+
+def _two_dims(t, name):
+    if t is None or t.dim() != 2:
+        raise MoeError(f"{name} must be a tensor of 2 dims")
+    return t.shape
+
+
+def _raw_stream(dev):
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def add_rms_norm(x, w, residual=None, eps=1e-6, fp8=False, want_y=True, res=None, y=None,
@@ -722,30 +753,50 @@ def add_rms_norm(x, w, residual=None, eps=1e-6, fp8=False, want_y=True, res=None
     scales of 128 values as expert_ffn_fp8_block takes them, else None.  d is a
     multiple of 8 (with fp8 of 16) up to 16384; res may be the residual (or x)
     itself, to update the stream in place."""
-    xt = _any_dtype(x, "x", dims=2)
-    rows, d = x.shape
-    wt = _any_dtype(w, "w", (d,))
-    rt = 0
+    dev = _device(x, "x")
+    shape = rows, d = _two_dims(x, "x")
+    xt = _typed(x, dev, "x", shape)
+    wt = _typed(w, dev, "w", (d,))
+    rt = rp = resp = yp = cp = sp = 0
     if residual is not None:
-        rt = _any_dtype(residual, "residual", (rows, d))
-        res = _out(res, residual.dtype, "res", (rows, d), x.device)
+        rt = _typed(residual, dev, "residual", shape)
+        if res is None:
+            res = torch.empty_like(residual, memory_format=torch.contiguous_format)
+        else:
+            _on(res, dev, residual.dtype, "res", shape)
+        rp, resp = residual.data_ptr(), res.data_ptr()
     elif res is not None:
         raise MoeError("res is an output of the residual's addition: it needs a residual")
-    if not (want_y or fp8):
+    if want_y:
+        if y is None:
+            y = torch.empty_like(x, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
+        else:
+            _on(y, dev, torch.bfloat16, "y", shape)
+        yp = y.data_ptr()
+    elif fp8:
+        y = None
+    else:
         raise MoeError("add_rms_norm needs an output: want_y or fp8")
-    y = _out(y, torch.bfloat16, "y", (rows, d), x.device) if want_y else None
     if fp8:
-        codes = _codes_like(codes, x)
-        scales = _out(scales, torch.float32, "scales", (rows, _blocks(d)), x.device)
+        if codes is None:
+            codes = torch.empty_like(x, dtype=torch.uint8, memory_format=torch.contiguous_format)
+        else:
+            _on(codes, dev, torch.uint8, "codes", shape)
+        if scales is None:
+            scales = x.new_empty((rows, _blocks(d)), dtype=torch.float32)
+        else:
+            _on(scales, dev, torch.float32, "scales", (rows, _blocks(d)))
+        cp, sp = codes.data_ptr(), scales.data_ptr()
     else:
         codes = scales = None
-    _here(x, w, residual, res, y, codes, scales)
-    _check(lib().moe_add_rms_norm(_ptr(x), xt, _ptr(residual), rt, _ptr(w), wt, rows, d,
-                                  float(eps), _ptr(res), _ptr(y), _ptr(codes), _ptr(scales),
-                                  _stream()), "moe_add_rms_norm")
+    st = lib().moe_add_rms_norm(x.data_ptr(), xt, rp, rt, w.data_ptr(), wt, rows, d, eps, resp, yp,
+                                cp, sp, _raw_stream(dev))
+    if st:
+        _check(st, "moe_add_rms_norm")
     return x if residual is None else res, y, codes, scales
 
 
+@functools.lru_cache(maxsize=256)
 def rms_norm_backward_workspace_size(rows, d):
     return int(lib().moe_rms_norm_backward_workspace_size(rows, d))
 
@@ -756,42 +807,55 @@ def rms_norm_backward(s, w, dy, eps=1e-6, d_res=None, dx_dtype=OUT_F32, dx=None,
     (its first result), dy the gradient of y, d_res that of s from elsewhere
     (or None); bf16 or fp32 each.  Returns (dx [rows, d] of dx_dtype, the
     gradient of x and of the residual, dw [d] fp32)."""
-    st = _any_dtype(s, "s", dims=2)
-    rows, d = s.shape
-    wt = _any_dtype(w, "w", (d,))
-    gt = _any_dtype(dy, "dy", (rows, d))
-    rt = 0 if d_res is None else _any_dtype(d_res, "d_res", (rows, d))
+    dev = _device(s, "s")
+    shape = rows, d = _two_dims(s, "s")
+    st = _typed(s, dev, "s", shape)
+    wt = _typed(w, dev, "w", (d,))
+    gt = _typed(dy, dev, "dy", shape)
+    rt = rp = 0
+    if d_res is not None:
+        rt, rp = _typed(d_res, dev, "d_res", shape), d_res.data_ptr()
     dt = torch.float32 if dx_dtype == OUT_F32 else torch.bfloat16
-    dx = _out(dx, dt, "dx", (rows, d), s.device)
-    dw = _out(dw, torch.float32, "dw", (d,), s.device)
+    if dx is None:
+        dx = torch.empty_like(s, dtype=dt, memory_format=torch.contiguous_format)
+    else:
+        _on(dx, dev, dt, "dx", shape)
+    if dw is None:
+        dw = s.new_empty((d,), dtype=torch.float32)
+    else:
+        _on(dw, dev, torch.float32, "dw", (d,))
     if workspace is None:
-        workspace = torch.empty(rms_norm_backward_workspace_size(rows, d), dtype=torch.uint8,
-                                device=s.device)
-    _need(workspace, torch.uint8, "workspace", 1)
-    _here(s, w, dy, d_res, dx, dw, workspace)
-    _check(lib().moe_rms_norm_backward(_ptr(s), st, _ptr(w), wt, _ptr(dy), gt, _ptr(d_res), rt,
-                                       rows, d, float(eps), _ptr(dx),
-                                       IN_F32 if dt == torch.float32 else IN_BF16, _ptr(dw),
-                                       _ptr(workspace), workspace.numel(), _stream()),
-           "moe_rms_norm_backward")
+        workspace = s.new_empty((rms_norm_backward_workspace_size(rows, d),), dtype=torch.uint8)
+    else:
+        _on(workspace, dev, torch.uint8, "workspace", (workspace.numel(),))
+    status = lib().moe_rms_norm_backward(
+        s.data_ptr(), st, w.data_ptr(), wt, dy.data_ptr(), gt, rp, rt, rows, d, eps, dx.data_ptr(),
+        _IN_TYPES[dt], dw.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(dev))
+    if status:
+        _check(status, "moe_rms_norm_backward")
     return dx, dw
 
 
-def _balance_args(logits, ids, offsets, modality, mask):
-    _need(logits, torch.float32, "logits", 2)
-    T, E = logits.shape
-    _need(ids, torch.int32, "ids", shape=(T, None))
-    _opt(modality, torch.uint8, "modality", shape=(T,))
-    _opt(mask, torch.uint8, "mask", shape=(T,))
-    S = 1
+def _balance_args(dev, logits, ids, offsets, modality, mask):
+    shape = T, E = _two_dims(logits, "logits")
+    _on(logits, dev, torch.float32, "logits", shape)
+    _on(ids, dev, torch.int32, "ids", (T, _two_dims(ids, "ids")[1]))
+    op = mp = kp = 0
+    S = C = 1
     if offsets is not None:
-        _need(offsets, torch.int32, "offsets", 1)
         S = offsets.numel() - 1
-    return T, E, ids.shape[1], S, 1 if modality is None else 2
+        op = _on(offsets, dev, torch.int32, "offsets", (S + 1,)).data_ptr()
+    if modality is not None:
+        C = 2
+        mp = _on(modality, dev, torch.uint8, "modality", (T,)).data_ptr()
+    if mask is not None:
+        kp = _on(mask, dev, torch.uint8, "mask", (T,)).data_ptr()
+    return T, E, ids.shape[1], S, C, op, mp, kp
 
 
-def balance_loss_workspace_size(T):
-    return int(lib().moe_balance_loss_workspace_size(T))
+@functools.lru_cache(maxsize=256)
+def balance_loss_workspace_size(T, E, S=1, classes=1):
+    return int(lib().moe_balance_loss_workspace_size(T, E, S, classes))
 
 
 def balance_loss(logits, ids, offsets=None, modality=None, mask=None, flags=None, loss=None,
@@ -800,19 +864,26 @@ def balance_loss(logits, ids, offsets=None, modality=None, mask=None, flags=None
     [T, k] on logits [T, E]: per sequence (offsets [S + 1] int32, or None: one
     of all tokens) and, with a modality [T] u8, per class.  mask [T] u8: tokens
     of 0 take no part.  Returns (loss [S, C] fp32, counts [S, C, E] int32)."""
-    T, E, k, S, C = _balance_args(logits, ids, offsets, modality, mask)
-    _flags(flags)
-    loss = _out(loss, torch.float32, "loss", (S, C), logits.device)
-    counts = _out(counts, torch.int32, "counts", (S, C, E), logits.device)
+    dev = _device(logits, "logits")
+    T, E, k, S, C, op, mp, kp = _balance_args(dev, logits, ids, offsets, modality, mask)
+    fp = 0 if flags is None else _on(flags, dev, torch.int32, "flags", (1,)).data_ptr()
+    if loss is None:
+        loss = logits.new_empty((S, C))
+    else:
+        _on(loss, dev, torch.float32, "loss", (S, C))
+    if counts is None:
+        counts = ids.new_empty((S, C, E))
+    else:
+        _on(counts, dev, torch.int32, "counts", (S, C, E))
     if workspace is None:
-        workspace = torch.empty(balance_loss_workspace_size(T), dtype=torch.uint8,
-                                device=logits.device)
-    _need(workspace, torch.uint8, "workspace", 1)
-    _here(logits, ids, offsets, modality, mask, flags, loss, counts, workspace)
-    _check(lib().moe_balance_loss(_ptr(logits), _ptr(ids), _ptr(offsets), _ptr(modality),
-                                  _ptr(mask), T, E, k, S, _ptr(loss), _ptr(counts), _ptr(flags),
-                                  _ptr(workspace), workspace.numel(), _stream()),
-           "moe_balance_loss")
+        workspace = logits.new_empty((balance_loss_workspace_size(T, E, S, C),), dtype=torch.uint8)
+    else:
+        _on(workspace, dev, torch.uint8, "workspace", (workspace.numel(),))
+    st = lib().moe_balance_loss(logits.data_ptr(), ids.data_ptr(), op, mp, kp, T, E, k, S,
+                                loss.data_ptr(), counts.data_ptr(), fp, workspace.data_ptr(),
+                                workspace.numel(), _raw_stream(dev))
+    if st:
+        _check(st, "moe_balance_loss")
     return loss, counts
 
 
@@ -821,16 +892,20 @@ def balance_loss_backward(logits, ids, counts, d_loss, offsets=None, modality=No
     """Gradient of balance_loss in the logits (moe_balance_loss_backward) for
     d_loss [S, C], counts as balance_loss gave them; add [T, E] is added, as
     route_backward's d_logits (out may be add).  Returns d_logits [T, E]."""
-    T, E, k, S, C = _balance_args(logits, ids, offsets, modality, mask)
-    _need(counts, torch.int32, "counts", shape=(S, C, E))
-    _need(d_loss, torch.float32, "d_loss", shape=(S, C))
-    _opt(add, torch.float32, "add", shape=(T, E))
-    out = _out(out, torch.float32, "out", (T, E), logits.device)
-    _here(logits, ids, counts, d_loss, offsets, modality, mask, add, out)
-    _check(lib().moe_balance_loss_backward(_ptr(logits), _ptr(ids), _ptr(offsets), _ptr(modality),
-                                           _ptr(mask), _ptr(counts), _ptr(d_loss), _ptr(add), T,
-                                           E, k, S, _ptr(out), _stream()),
-           "moe_balance_loss_backward")
+    dev = _device(logits, "logits")
+    T, E, k, S, C, op, mp, kp = _balance_args(dev, logits, ids, offsets, modality, mask)
+    _on(counts, dev, torch.int32, "counts", (S, C, E))
+    _on(d_loss, dev, torch.float32, "d_loss", (S, C))
+    ap = 0 if add is None else _on(add, dev, torch.float32, "add", (T, E)).data_ptr()
+    if out is None:
+        out = torch.empty_like(logits, memory_format=torch.contiguous_format)
+    else:
+        _on(out, dev, torch.float32, "out", (T, E))
+    st = lib().moe_balance_loss_backward(logits.data_ptr(), ids.data_ptr(), op, mp, kp,
+                                         counts.data_ptr(), d_loss.data_ptr(), ap, T, E, k, S,
+                                         out.data_ptr(), _raw_stream(dev))
+    if st:
+        _check(st, "moe_balance_loss_backward")
     return out
 
 
@@ -851,10 +926,11 @@ class GradClip:
         if not self.grads:
             raise MoeError("grads must hold a tensor")
         entries = (MoeGradTensor * len(self.grads))()
+        dev = _device(self.grads[0], "grads[0]")
         for i, (g, o) in enumerate(zip(self.grads, self.out)):
-            dt = _any_dtype(g, f"grads[{i}]")
-            _need(o, g.dtype, f"out[{i}]", shape=tuple(g.shape))
-            _here(g, o)
+            dt = _in_dtype(g, f"grads[{i}]")
+            _on(g, dev, g.dtype, f"grads[{i}]", g.shape)
+            _on(o, dev, g.dtype, f"out[{i}]", g.shape)
             entries[i] = MoeGradTensor(_ptr(g) or None, _ptr(o) or None, g.numel(), dt)
         self.device = self.grads[0].device
         size = int(lib().moe_grad_plan_size(entries, len(entries)))
@@ -866,40 +942,55 @@ class GradClip:
 
     def norm(self, norm=None):
         """The norm of the gradients as they are now, [1] fp32."""
-        return self._run(lambda n: lib().moe_grad_norm(
-            _ptr(self.plan), self.plan.numel(), n, _ptr(self.workspace), GRAD_WORKSPACE_BYTES,
-            _stream()), norm, "moe_grad_norm")
+        dev, norm = self._norm(norm)
+        _check(lib().moe_grad_norm(self.plan.data_ptr(), self.plan.numel(), norm.data_ptr(),
+                                   self.workspace.data_ptr(), GRAD_WORKSPACE_BYTES,
+                                   _raw_stream(dev)), "moe_grad_norm")
+        return norm
 
     def clip(self, max_norm, norm=None):
         """Scales the gradients to max_norm where their norm is larger (and
         finite), into out; returns the norm before, [1] fp32."""
-        max_norm = float(max_norm)
-        return self._run(lambda n: lib().moe_clip_grad_norm(
-            _ptr(self.plan), self.plan.numel(), max_norm, n, _ptr(self.workspace),
-            GRAD_WORKSPACE_BYTES, _stream()), norm, "moe_clip_grad_norm")
-
-    def _run(self, call, norm, what):
-        norm = _out(norm, torch.float32, "norm", (1,), self.device)
-        _here(norm, self.plan)
-        _check(call(_ptr(norm)), what)
+        dev, norm = self._norm(norm)
+        _check(lib().moe_clip_grad_norm(self.plan.data_ptr(), self.plan.numel(), max_norm,
+                                        norm.data_ptr(), self.workspace.data_ptr(),
+                                        GRAD_WORKSPACE_BYTES, _raw_stream(dev)),
+               "moe_clip_grad_norm")
         return norm
+
+    def _norm(self, norm):
+        dev = torch._C._cuda_getDevice()
+        if dev != self.device.index:
+            raise MoeError(f"the gradients are on {self.device}, the current device is cuda:{dev}")
+        if norm is None:
+            return dev, torch.empty((1,), dtype=torch.float32, device=self.device)
+        return dev, _on(norm, dev, torch.float32, "norm", (1,))
 
 
 def quantize_mxfp4(a, codes=None, scales=None):
     """Rows a [..., K] (bf16 or fp32, 2 or 3 dims, K a multiple of 32) as
     MXFP4 (moe_quantize_mxfp4): returns (codes uint8 [..., K / 2], the lower
     column in the low nibble, scale bytes X + 127 uint8 [..., K / 32])."""
-    dt = _any_dtype(a, "a")
+    dt = _in_dtype(a, "a")
     if a.dim() not in (2, 3):
         raise MoeError("a must have 2 or 3 dims")
+    dev = _device(a, "a")
     shape = tuple(a.shape)
-    K = shape[-1]
-    codes = _out(codes, torch.uint8, "codes", shape[:-1] + (K // 2,), a.device)
-    scales = _out(scales, torch.uint8, "scales", shape[:-1] + (K // 32,), a.device)
-    _here(a, codes, scales)
-    rows = shape[0] if len(shape) == 2 else shape[0] * shape[1]
-    _check(lib().moe_quantize_mxfp4(_ptr(a), dt, rows, K, _ptr(codes), _ptr(scales), _stream()),
-           "moe_quantize_mxfp4")
+    _on(a, dev, a.dtype, "a", shape)
+    lead, K = shape[:-1], shape[-1]
+    if codes is None:
+        codes = a.new_empty(lead + (K // 2,), dtype=torch.uint8)
+    else:
+        _on(codes, dev, torch.uint8, "codes", lead + (K // 2,))
+    if scales is None:
+        scales = a.new_empty(lead + (K // 32,), dtype=torch.uint8)
+    else:
+        _on(scales, dev, torch.uint8, "scales", lead + (K // 32,))
+    rows = lead[0] if len(lead) == 1 else lead[0] * lead[1]
+    st = lib().moe_quantize_mxfp4(a.data_ptr(), dt, rows, K, codes.data_ptr(), scales.data_ptr(),
+                                  _raw_stream(dev))
+    if st:
+        _check(st, "moe_quantize_mxfp4")
     return codes, scales
 
 
@@ -909,20 +1000,27 @@ def grouped_gemm_mxfp4(a4, a_scale, offsets, w4, w_scale, out_dtype=OUT_BF16, ou
     N, K / 2], w_scale [G, N, K / 32], uint8 as quantize_mxfp4 gives them;
     offsets [G + 1] int32.  K a multiple of 32, N of 16.  Rows outside every
     group are not written."""
-    _need(a4, torch.uint8, "a4", 2)
-    rows, half = a4.shape
-    K = 2 * half
-    _need(w4, torch.uint8, "w4", shape=(None, None, half))
+    dev = _device(a4, "a4")
+    rows, half = _two_dims(a4, "a4")
+    _on(a4, dev, torch.uint8, "a4", (rows, half))
+    if w4 is None or w4.dim() != 3:
+        raise MoeError("w4 must be a tensor of 3 dims")
     G, N = w4.shape[:2]
-    _need(a_scale, torch.uint8, "a_scale", shape=(rows, K // 32))
-    _need(w_scale, torch.uint8, "w_scale", shape=(G, N, K // 32))
-    _need(offsets, torch.int32, "offsets", shape=(G + 1,))
+    K = 2 * half
+    _on(w4, dev, torch.uint8, "w4", (G, N, half))
+    _on(a_scale, dev, torch.uint8, "a_scale", (rows, K // 32))
+    _on(w_scale, dev, torch.uint8, "w_scale", (G, N, K // 32))
+    _on(offsets, dev, torch.int32, "offsets", (G + 1,))
     dt = torch.float32 if out_dtype == OUT_F32 else torch.bfloat16
-    out = _out(out, dt, "out", (rows, N), a4.device)
-    _here(a4, a_scale, offsets, w4, w_scale, out)
-    _check(lib().moe_grouped_gemm_mxfp4(_ptr(a4), _ptr(a_scale), _ptr(offsets), G, rows, K, N,
-                                        _ptr(w4), _ptr(w_scale), int(out_dtype), _ptr(out),
-                                        _stream()), "moe_grouped_gemm_mxfp4")
+    if out is None:
+        out = a4.new_empty((rows, N), dtype=dt)
+    else:
+        _on(out, dev, dt, "out", (rows, N))
+    st = lib().moe_grouped_gemm_mxfp4(a4.data_ptr(), a_scale.data_ptr(), offsets.data_ptr(), G,
+                                      rows, K, N, w4.data_ptr(), w_scale.data_ptr(),
+                                      int(out_dtype), out.data_ptr(), _raw_stream(dev))
+    if st:
+        _check(st, "moe_grouped_gemm_mxfp4")
     return out
 
 

@@ -71,8 +71,11 @@ def test_rms_norm_backward(L):
 
 def test_balance_loss(L):
     size = L.moe_balance_loss_workspace_size
-    assert size(0) == size(-1) == 0 and size(1) == 256
-    need = size(64)
+    assert size(-1, 8, 1, 1) == size(8, 0, 1, 1) == size(8, 8, 0, 1) == size(8, 8, 1, 3) == 0
+    assert size(8, 1025, 1, 1) == size(8, 8, (1 << 20) + 1, 1) == 0
+    assert size(0, 8, 1, 1) > 0
+    need = size(64, 8, 3, 1)
+    assert size(64, 8, 3, 2) > need
 
     def f(lg=FAKE, ids=FAKE, off=FAKE, mod=None, mask=None, T=64, E=8, k=2, S=3, loss=FAKE,
           counts=FAKE, ws=FAKE, wsb=need):

@@ -541,7 +541,7 @@ def test_graph_replays():
     off = torch.tensor([0, 700, 1200, 1300], dtype=torch.int32, device="cuda")
     loss, counts = torch.empty(3, 1, device="cuda"), torch.empty(3, 1, E, dtype=torch.int32,
                                                                  device="cuda")
-    bws = torch.empty(ops.balance_loss_workspace_size(T), dtype=torch.uint8, device="cuda")
+    bws = torch.empty(ops.balance_loss_workspace_size(T, E, 3), dtype=torch.uint8, device="cuda")
     dl, dlg = torch.ones(3, 1, device="cuda"), torch.empty(T, E, device="cuda")
     clipped = [torch.empty_like(dx), torch.empty_like(dw)]
     clip, norm = ops.GradClip([dx, dw], out=clipped), torch.empty(1, device="cuda")
