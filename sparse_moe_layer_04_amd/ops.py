@@ -971,10 +971,10 @@ def quantize_mxfp4(a, codes=None, scales=None):
     """Rows a [..., K] (bf16 or fp32, 2 or 3 dims, K a multiple of 32) as
     MXFP4 (moe_quantize_mxfp4): returns (codes uint8 [..., K / 2], the lower
     column in the low nibble, scale bytes X + 127 uint8 [..., K / 32])."""
+    dev = _device(a, "a")
     dt = _in_dtype(a, "a")
     if a.dim() not in (2, 3):
         raise MoeError("a must have 2 or 3 dims")
-    dev = _device(a, "a")
     shape = tuple(a.shape)
     _on(a, dev, a.dtype, "a", shape)
     lead, K = shape[:-1], shape[-1]

@@ -226,5 +226,8 @@ def test_binding_refuses_host_tensors():
         ops.quantize_mxfp4(x)
     with pytest.raises(ops.MoeError, match="device tensor"):
         ops.grouped_gemm_mxfp4(u8, u8, off, u8, u8)
-    with pytest.raises(ops.MoeError, match="bfloat16 or float32"):
-        ops.add_rms_norm(x.half(), w)
+    for call in (lambda: ops.add_rms_norm(None, w), lambda: ops.rms_norm_backward(None, w, x),
+                 lambda: ops.balance_loss(None, ids), lambda: ops.quantize_mxfp4(None),
+                 lambda: ops.GradClip([None]), lambda: ops.grouped_gemm_mxfp4(None, u8, off, u8, u8)):
+        with pytest.raises(ops.MoeError, match="is required"):
+            call()

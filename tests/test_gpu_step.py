@@ -490,6 +490,33 @@ def test_clip_limits():
     assert not g.any()
 
 
+def test_refusals():
+    """What the binding refuses with tensors on the device."""
+    x, w = torch.randn(8, 64, device="cuda"), torch.ones(64, device="cuda")
+    ids = torch.zeros(8, 2, dtype=torch.int32, device="cuda")
+    loss, counts = ops.balance_loss(x, ids)
+    for call in (lambda: ops.add_rms_norm(x.half(), w), lambda: ops.add_rms_norm(x, w[:32]),
+                 lambda: ops.add_rms_norm(x.t(), w), lambda: ops.add_rms_norm(x, w.cpu()),
+                 lambda: ops.add_rms_norm(x, w, residual=x[:4]),
+                 lambda: ops.add_rms_norm(x, w, res=x), lambda: ops.add_rms_norm(x[0], w),
+                 lambda: ops.add_rms_norm(x, w, want_y=False),
+                 lambda: ops.add_rms_norm(x, w, residual=x, res=x.to(BF16)),
+                 lambda: ops.add_rms_norm(x, w, eps=-1.0),
+                 lambda: ops.add_rms_norm(x[:, :12].contiguous(), w[:12]),
+                 lambda: ops.rms_norm_backward(x, w, x[:, :32]),
+                 lambda: ops.rms_norm_backward(x, w, x, dx=x.to(BF16)),
+                 lambda: ops.rms_norm_backward(x, w, x, workspace=torch.empty(
+                     8, dtype=torch.uint8, device="cuda")),
+                 lambda: ops.balance_loss(x, ids.long()), lambda: ops.balance_loss(x, ids[:4]),
+                 lambda: ops.balance_loss(x, ids, offsets=ids[:1, :1].reshape(-1)),
+                 lambda: ops.balance_loss(x, ids, mask=torch.ones(8, device="cuda")),
+                 lambda: ops.balance_loss_backward(x, ids, counts[0], loss),
+                 lambda: ops.balance_loss_backward(x, ids, counts, loss, add=x[:4]),
+                 lambda: ops.balance_loss_backward(x, ids, counts, loss.double())):
+        with pytest.raises(ops.MoeError):
+            call()
+
+
 def test_clip_refuses():
     a = torch.randn(64, device="cuda")
     for grads, out in (([a, a], None), ([a, a[16:32]], None), ([a], [torch.zeros(63).cuda()]),
