@@ -12,10 +12,15 @@
 // codes of both operands go to a ring of three LDS slots by copies that pass
 // no register, two stages ahead (a wave's copy covers 8 rows x 128 bytes; LDS
 // row r holds its 16-byte chunk c at c ^ ((r >> 1) & 7), so that the lanes of
-// an operand read spread over the banks).  A row's 8 scale bytes of a stage
-// start at any byte (K / 32 need not be a multiple of 4): the 16 bytes from the
-// word that holds the first one are copied, one stage ahead and into one of two
-// places, and each lane shifts its own out.
+// an operand read spread over the banks).
+//
+// Scales: a row's 8 bytes of a stage, but fetched 32 at a time: the 16 bytes of
+// one stage for each of 384 rows are 384 lines touched, as many as its codes
+// (384 groups x 128 rows x 4096 x 2048: 560 us; without any scales 448).  A
+// slab of 32 bytes a row from the word that holds the first one is four stages
+// (K / 32 and the scales' address multiples of 4) or three (any others, the
+// bytes shifted out of the words).  Its place in LDS is read into registers at
+// the slab's first stage and takes the next slab from then on.
 #include "fp4.h"
 #include "lds_ring.h"
 
@@ -29,8 +34,8 @@ constexpr int kThreads = 512;
 constexpr int kSlotW = BN * BK;
 constexpr int kSlot = kSlotW + BM * BK;
 constexpr int kRing = 3 * kSlot;
-constexpr int kScales = 16 * (BN + BM);    // a stage's scales: 16 bytes a row, W's first
-constexpr int kLds = kRing + 2 * kScales;
+constexpr int kSlab = 32 * (BN + BM);      // scales: 32 bytes a row, W's first
+constexpr int kLds = kRing + kSlab;
 static_assert(kLds <= 160 * 1024 && kSlot % 128 == 0, "three slots of LDS");
 
 struct Tile {
@@ -45,8 +50,8 @@ constexpr int kEarly = 3;                  // of them, issued in the stage befor
 // resources over the tile's rows (wave-uniform base, 32-bit offsets; rows past
 // the tile's or the matrix's end lie past them and fetch nothing).
 struct Fetch {
-    u32x4 wsrc, asrc, ssrc;
-    int wo[4], ao[2], so;
+    u32x4 wsrc, asrc, wscale, ascale;
+    int wo[4], sw, sa;
 
     __device__ __forceinline__ void set(const Fp4GemmArgs& p, const Tile& t) {
         const int tid = threadIdx.x, lane = tid & 63;
@@ -59,60 +64,56 @@ struct Fetch {
         asrc = uniform_rsrc(p.a + (size_t)t.row0 * Kb, (size_t)t.valid * Kb);
 #pragma unroll
         for (int q = 0; q < 4; ++q) wo[q] = (lr + 64 * q) * Kb + 16 * c;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) ao[q] = wo[q];
-        // scales: waves 0-3 the weight rows', 4 and 5 the rows' (6 and 7 the
-        // same again, so that every wave issues the same number of copies);
-        // whole words from the one that holds the first byte on
-        const bool isw = wave < 4;
-        const uint8_t* first = isw ? p.ws + wfirst * nb : p.as + (size_t)t.row0 * nb;
-        const int mis = (int)((uintptr_t)first & 3);
-        ssrc = uniform_rsrc(first - mis,
-                            ((size_t)(isw ? wrows : t.valid) * nb + mis + 3) & ~size_t(3));
-        so = ((64 * (isw ? wave : wave & 1) + lane) * nb + mis) & ~3;
+        // scales: wave w the slab's weight rows 32 w + (0 .. 31) and rows 32 (w &
+        // 3) + (0 .. 31) (half of them twice, so that every wave issues the same
+        // number of copies), 16 bytes a lane; whole words from the one that
+        // holds the first byte on
+        auto scales = [&](const uint8_t* first, int rows, u32x4& src) {
+            const int mis = (int)((uintptr_t)first & 3);
+            src = uniform_rsrc(first - mis, ((size_t)rows * nb + mis + 3) & ~size_t(3));
+            return mis;
+        };
+        const int r = lane >> 1, piece = 16 * (lane & 1);
+        sw = (((32 * wave + r) * nb + scales(p.ws + wfirst * nb, wrows, wscale)) & ~3) + piece;
+        sa = (((32 * (wave & 3) + r) * nb +
+               scales(p.as + (size_t)t.row0 * nb, t.valid, ascale)) & ~3) + piece;
     }
 
-    // Copy q (of 4 + NA) of stage j into the slot at LDS byte `at`.  Stage 0
-    // takes K's last bytes, the short stage if any, stage j the j'th 128 bytes
-    // but one.  (Every stage issues its copies: past the last stage with offsets
-    // past the resources.)  `past`: the bytes that this thread's chunk reaches
-    // past K in the last stage; it fetches the row's last chunk instead, which
-    // is overwritten by zeros when it has landed.
+    // Copy q (of 4 + NA) of stage j into the slot at LDS byte `at`.  (Every
+    // stage issues its copies: past the last stage with offsets past the
+    // resources.  What the last stage holds past K is left out when it is
+    // multiplied.)
     template <int NA>
-    __device__ __forceinline__ void copy(int q, int j, int S, int past, int at) const {
+    __device__ __forceinline__ void copy(int q, int j, int S, int at) const {
         const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-        const int b = j == 0 ? S - 1 : min(j, S) - 1;
-        const int back = j == 0 ? past : 0, out = j < S ? 0 : (int)0x80000000;
+        const int b = min(j, S - 1) * BK, out = j < S ? 0 : (int)0x80000000;
         if (q < 4)
-            copy16(wsrc, (wo[q] - back) | out, b * BK, at + q * 64 * BK + wave * 1024);
+            copy16(wsrc, wo[q] | out, b, at + q * 64 * BK + wave * 1024);
         else
-            copy16(asrc, (ao[q - 4] - back) | out, b * BK,
-                   at + kSlotW + (q - 4) * 64 * BK + wave * 1024);
+            copy16(asrc, wo[q - 4] | out, b, at + kSlotW + (q - 4) * 64 * BK + wave * 1024);
     }
     template <int NA, int Q0, int Q1>
-    __device__ __forceinline__ void copies(int j, int S, int past, int at) const {
+    __device__ __forceinline__ void copies(int j, int S, int at) const {
 #pragma unroll
-        for (int q = Q0; q < Q1 && q < 4 + NA; ++q) copy<NA>(q, j, S, past, at);
+        for (int q = Q0; q < Q1 && q < 4 + NA; ++q) copy<NA>(q, j, S, at);
     }
-    // the scales of stage j
-    __device__ __forceinline__ void scales(int j, int S) const {
+    // the slab whose first stage is j: two copies
+    __device__ __forceinline__ void slab(int j) const {
         const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-        const int b = j == 0 ? S - 1 : min(j, S) - 1, out = j < S ? 0 : (int)0x80000000;
-        copy16(ssrc, so | out, b * 8,
-               kRing + (j & 1) * kScales + (wave < 6 ? wave : wave - 2) * 1024);
+        copy16(wscale, sw, j * 8, kRing + wave * 1024);
+        copy16(ascale, sa, j * 8, kRing + 32 * BN + (wave & 3) * 1024);
     }
     // what is on its way when a tile (of NA row copies) begins
     template <int NA>
-    __device__ __forceinline__ void first(int S, int past) const {
-        copies<NA, 0, 6>(0, S, past, 0);
-        scales(0, S);
-        copies<NA, 0, 6>(1, S, past, kSlot);
-        scales(1, S);
-        copies<NA, 0, kEarly>(2, S, past, 2 * kSlot);
+    __device__ __forceinline__ void first(int S) const {
+        slab(0);
+        copies<NA, 0, 6>(0, S, 0);
+        copies<NA, 0, 6>(1, S, kSlot);
+        copies<NA, 0, kEarly>(2, S, 2 * kSlot);
     }
-    __device__ __forceinline__ void first_stages(int valid, int S, int past) const {
-        if (valid <= 64) first<1>(S, past);
-        else first<2>(S, past);
+    __device__ __forceinline__ void first_stages(int valid, int S) const {
+        if (valid <= 64) first<1>(S);
+        else first<2>(S);
     }
 };
 
@@ -120,7 +121,7 @@ struct Fetch {
 // next tile's (if there are more) off before this one's results are written.
 template <bool F32, int MB>
 __device__ __forceinline__ void run_tile(const Fp4GemmArgs& p, const Tile& t, const Tile& next_t,
-                                         bool more, int past, unsigned char* ring) {
+                                         bool more, int per, unsigned char* ring) {
     // (the thread's place as a value of this variant's own: address terms
     // shared by the variants would be kept, or spilled, for all of them)
     int tid = threadIdx.x;
@@ -136,14 +137,15 @@ __device__ __forceinline__ void run_tile(const Fp4GemmArgs& p, const Tile& t, co
     const int wm = wave / WN, wn = wave % WN;
     const int N = p.N, nb = p.K / 32;
     const int S = (p.K / 2 + BK - 1) / BK;
+    const int tail = nb & 7;               // blocks of a short last stage
 
     // LDS rows 32 apart share their swizzle, so the rest of an operand's
     // address is an immediate; the chunk index enters it by exclusive or
     const int rd0 = l32 * BK + ((half ^ swz(l32)) << 4);
     const int rdw = wn * NJ * 32 * BK + rd0;
     const int rda = kSlotW + wm * MI * 32 * BK + rd0;
-    const int rsw = kRing + (wn * NJ * 32 + l32) * 16;
-    const int rsa = kRing + (BN + wm * MI * 32 + l32) * 16;
+    const int rsw = kRing + (wn * NJ * 32 + l32) * 32;
+    const int rsa = kRing + (BN + wm * MI * 32 + l32) * 32;
     // bits from the copied words' first byte to this half's first scale
     const uint32_t wbase = (uint32_t)((uintptr_t)p.ws + ((size_t)t.g * N + t.n0) * nb);
     const uint32_t abase = (uint32_t)((uintptr_t)p.as + (size_t)t.row0 * nb);
@@ -155,26 +157,47 @@ __device__ __forceinline__ void run_tile(const Fp4GemmArgs& p, const Tile& t, co
     for (int i = 0; i < MI; ++i)
         sha[i] = 8 * (int)((abase + (uint32_t)((wm * MI + i) * 32 + l32) * nb) & 3) + 8 * half;
 
-    u32x4 qw[NJ], qa[MI];                  // a stage's scale words as copied
-    auto read_s = [&](int j) {
+    // a slab's words; two are used up a stage
+    u32x4 qw[NJ][2], qa[MI][2];
+    auto read_slab = [&]() {
 #pragma unroll
         for (int n = 0; n < NJ; ++n)
-            qw[n] = *(const u32x4*)(ring + rsw + (j & 1) * kScales + n * 32 * 16);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                qw[n][h] = *(const u32x4*)(ring + rsw + n * 32 * 32 + 16 * h);
 #pragma unroll
         for (int i = 0; i < MI; ++i)
-            qa[i] = *(const u32x4*)(ring + rsa + (j & 1) * kScales + i * 32 * 16);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                qa[i][h] = *(const u32x4*)(ring + rsa + i * 32 * 32 + 16 * h);
     };
-    // bytes 0 and 2 of word 0: the scales of steps 0 and 1, of word 1: 2 and 3
+    // The next stage's scales: bytes 0 and 2 of word 0 those of steps 0 and 1, of
+    // word 1 of 2 and 3
     int cw[NJ][2], ca[MI][2];
-    auto shift = [](const u32x4& q, int by, int (&c)[2]) {
-        c[0] = (int)(uint32_t)((((uint64_t)q[1] << 32) | q[0]) >> by);
-        c[1] = (int)(uint32_t)((((uint64_t)q[2] << 32) | q[1]) >> by);
-    };
     auto scales = [&]() {
+        auto take = [](u32x4& x, u32x4& y, int by, int& c0, int& c1) {
+            c0 = (int)(uint32_t)((((uint64_t)x[1] << 32) | x[0]) >> by);
+            c1 = (int)(uint32_t)((((uint64_t)x[2] << 32) | x[1]) >> by);
+            x = u32x4{x[2], x[3], y[0], y[1]};
+            y = u32x4{y[2], y[3], 0u, 0u};
+        };
 #pragma unroll
-        for (int n = 0; n < NJ; ++n) shift(qw[n], shw[n], cw[n]);
+        for (int n = 0; n < NJ; ++n) take(qw[n][0], qw[n][1], shw[n], cw[n][0], cw[n][1]);
 #pragma unroll
-        for (int i = 0; i < MI; ++i) shift(qa[i], sha[i], ca[i]);
+        for (int i = 0; i < MI; ++i) take(qa[i][0], qa[i][1], sha[i], ca[i][0], ca[i][1]);
+    };
+    // the last stage's blocks past K: any finite scale
+    auto finite = [&]() {
+        auto mask = [&](int& c0, int& c1) {
+            if (half >= tail) c0 = (c0 & ~0xff) | 127;
+            if (2 + half >= tail) c0 = (c0 & ~0xff0000) | 127 << 16;
+            if (4 + half >= tail) c1 = (c1 & ~0xff) | 127;
+            if (6 + half >= tail) c1 = (c1 & ~0xff0000) | 127 << 16;
+        };
+#pragma unroll
+        for (int n = 0; n < NJ; ++n) mask(cw[n][0], cw[n][1]);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) mask(ca[i][0], ca[i][1]);
     };
 
     f32x16 acc[MI][NJ];
@@ -185,19 +208,27 @@ __device__ __forceinline__ void run_tile(const Fp4GemmArgs& p, const Tile& t, co
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][n][e] = 0.0f;
 
-    // stage 0 has landed; zeros over this thread's own copies past K
-    wait_vm<kCopies + 1 + kEarly>();
-    if (past) {
-        const u32x4 z = {0u, 0u, 0u, 0u};
+    // Of the last stage, what this thread copied from past K becomes zeros (in W
+    // alone: the products are then zero, as no code is an infinity or NaN).
+    auto zeros = [&](int slot) {
+        if (((tid & 7) ^ swz(tid >> 3)) >= tail)
 #pragma unroll
-        for (int q = 0; q < 4 + NA; ++q) *(u32x4*)(ring + q * 64 * BK + tid * 16) = z;
-    }
+            for (int q = 0; q < 4; ++q)
+                *(u32x4*)(ring + slot + q * 64 * BK + tid * 16) = u32x4{0u, 0u, 0u, 0u};
+    };
+    // stage 0 and the first slab have landed
+    wait_vm<kCopies + kEarly>();
+    if (tail && S == 1) zeros(0);
     __syncthreads();
-    // The middle of stage j: stage j + 1 has landed (the copies behind its scales
-    // are stage j + 2's codes) and every wave has read stage j's operands, whose
-    // slot takes stage j + 3's, and its scales, whose place takes stage j + 2's.
-    auto turn = [&]() {
-        wait_vm<kCopies>();
+    // The middle of stage j: stage j + 1 has landed (the copies behind it are
+    // stage j + 2's, and a slab that was sent off just before those) and every
+    // wave has read stage j's operands, whose slot takes stage j + 3's, and the
+    // slab if stage j is its first.
+    bool sent = false;
+    auto turn = [&](int j, int next) {
+        if (sent) wait_vm<kCopies + 2>();
+        else wait_vm<kCopies>();
+        if (tail && j == S - 2) zeros(next);
         __syncthreads();
     };
 
@@ -224,6 +255,12 @@ __device__ __forceinline__ void run_tile(const Fp4GemmArgs& p, const Tile& t, co
                     wide(rw[B][n]), wide(ra[B][i]), acc[i][n], 4, 4, O, cw[n][W], O, ca[i][W]);
             copy(index);
         });
+        // (the products stay here: the compiler would take them all to the end of
+        // the stage, behind its branches)
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int n = 0; n < NJ; ++n) asm volatile("" : "+v"(acc[i][n]));
         __builtin_amdgcn_sched_barrier(0);
     };
     using Q0 = std::integral_constant<int, 0>;
@@ -231,54 +268,46 @@ __device__ __forceinline__ void run_tile(const Fp4GemmArgs& p, const Tile& t, co
     using Q2 = std::integral_constant<int, 2>;
     using Q3 = std::integral_constant<int, 3>;
     read(0, Q0());
-    read_s(0);
+    read_slab();
     scales();
-    if (nb & 7) {
-        // stage 0's blocks past K (of zero codes): any finite scale
-        const int v = nb & 7;
-        auto mask = [&](int (&c)[2]) {
-            if (half >= v) c[0] = (c[0] & ~0xff) | 127;
-            if (2 + half >= v) c[0] = (c[0] & ~0xff0000) | 127 << 16;
-            if (4 + half >= v) c[1] = (c[1] & ~0xff) | 127;
-            if (6 + half >= v) c[1] = (c[1] & ~0xff0000) | 127 << 16;
-        };
-#pragma unroll
-        for (int n = 0; n < NJ; ++n) mask(cw[n]);
-#pragma unroll
-        for (int i = 0; i < MI; ++i) mask(ca[i]);
-    }
-    int slot = 0;
+    if (tail && S == 1) finite();
+    int slot = 0, at = 0;                           // at: the stage's place in its slab
     for (int j = 0; j < S; ++j) {
         const int next = slot == 2 * kSlot ? 0 : slot + kSlot;
         const int last = next == 2 * kSlot ? 0 : next + kSlot;
         read(slot, Q1());
         multiply(Q0(), [&](auto x) {
             constexpr int c = 3 + decltype(x)::value;
-            if constexpr (c < 5) f.template copies<NA, c, c + 1>(j + 2, S, past, last);
+            if constexpr (c < 5) f.template copies<NA, c, c + 1>(j + 2, S, last);
         });
         read(slot, Q2());
         multiply(Q1(), [&](auto x) {
             constexpr int c = 5 + decltype(x)::value;
-            if constexpr (c < 6) f.template copies<NA, c, c + 1>(j + 2, S, past, last);
+            if constexpr (c < 6) f.template copies<NA, c, c + 1>(j + 2, S, last);
         });
         read(slot, Q3());
         multiply(Q2(), [](auto) {});
-        turn();
+        turn(j, next);
         read(next, Q0());                           // (past the end: not used)
-        read_s(j + 1);
-        f.scales(j + 2, S);
+        sent = at == 0 && j + per < S;
+        if (sent) f.slab(j + per);
+        if (++at == per) {
+            at = 0;
+            read_slab();
+        }
         multiply(Q3(), [&](auto x) {
             constexpr int c = decltype(x)::value;
-            if constexpr (c < kEarly) f.template copies<NA, c, c + 1>(j + 3, S, past, slot);
+            if constexpr (c < kEarly) f.template copies<NA, c, c + 1>(j + 3, S, slot);
         });
         scales();
+        if (tail && j == S - 2) finite();
         slot = next;
     }
     // (every wave has read the last stage; what the ring still holds is unused)
     if (more) {
         Fetch nf;
         nf.set(p, next_t);
-        nf.first_stages(next_t.valid, S, past);
+        nf.first_stages(next_t.valid, S);
     }
 
     // Lane l holds, of row l % 32 of its block, weight rows 8 q + 4 (l / 32) +
@@ -391,8 +420,8 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_kernel(Fp4GemmArgs p) {
         t.row0 = r0 + (band + local % high) * per;
         t.valid = min(per, r0 + n - t.row0);
     };
-    // bytes that this thread's chunk of K's last stage reaches past K
-    const int past = max(0, (S - 1) * BK + 16 * ((tid & 7) ^ swz(tid >> 3)) + 16 - Kb);
+    // stages of a slab of scales
+    const int per = (p.K & 127) || (((uintptr_t)p.as | (uintptr_t)p.ws) & 3) ? 3 : 4;
     int q = (int)(Q * xcd / 8) + (int)(blockIdx.x >> 3);
     if (q >= end) return;
     Tile t;
@@ -400,17 +429,17 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_kernel(Fp4GemmArgs p) {
     {
         Fetch f;
         f.set(p, t);
-        f.first_stages(t.valid, S, past);
+        f.first_stages(t.valid, S);
     }
     for (;;) {
         const bool more = q + step < end;
         Tile next = t;
         if (more) find(q + step, next);
         switch ((t.valid + 31) >> 5) {
-            case 1: run_tile<F32, 1>(p, t, next, more, past, smem); break;
-            case 2: run_tile<F32, 2>(p, t, next, more, past, smem); break;
-            case 3: run_tile<F32, 3>(p, t, next, more, past, smem); break;
-            default: run_tile<F32, 4>(p, t, next, more, past, smem); break;
+            case 1: run_tile<F32, 1>(p, t, next, more, per, smem); break;
+            case 2: run_tile<F32, 2>(p, t, next, more, per, smem); break;
+            case 3: run_tile<F32, 3>(p, t, next, more, per, smem); break;
+            default: run_tile<F32, 4>(p, t, next, more, per, smem); break;
         }
         if (!more) break;
         t = next;
