@@ -4,8 +4,10 @@
 // b the blocks of 32 of K, codes E2M1, scale bytes X + 127 (255: NaN).
 //
 // The scaled matrix instructions (32 x 32 outputs, 64 of K) take both operands
-// as they are: lane l holds of row (column) l % 32 the 16 bytes of block 2 s +
-// l / 32 of step s, and that block's scale byte, one of four of a register.
+// as they are: lane l holds of row (column) l % 32 the 16 bytes of one block of
+// 32 and that block's scale byte, one of the four of a register.  Of a stage's
+// eight blocks the lower half of the lanes takes 0 to 3 in the stage's four
+// steps, the upper half 4 to 7, so that a half's four scales are one word.
 //
 // Tile: up to 128 rows x 256 weight rows, 8 waves of 64 x 64 or (rows of the
 // tile) x 32 outputs, 256 of K (128 bytes a row) a stage, four steps.  The
@@ -44,6 +46,16 @@ struct Tile {
 
 // copies of codes a wave and stage: 4 of W, NA (one for each 64 rows) of A
 constexpr int row_copies(int blocks) { return (blocks + 1) / 2; }
+// Waves of a tile of `blocks` blocks of 32 rows: along the rows x along the
+// weight rows, each MI x NJ blocks of 32 x 32.  With NJ = 2 the two blocks of
+// weight rows hold every other one of 64, so that a lane has neighbouring
+// columns of the output.
+template <int MB>
+struct Waves {
+    static constexpr int WM = MB == 4 || MB == 2 ? 2 : 1, WN = 8 / WM, MI = MB / WM, NJ = 8 / WN;
+    static constexpr int kStores = 16 * MI;   // of a wave, whatever the output's type
+};
+__device__ __forceinline__ bool in_pairs(int valid) { return ((valid - 1) >> 5) & 1; }
 constexpr int kEarly = 3;                  // of them, issued in the stage before
 
 // The copies of a tile's operands into LDS, set up once per tile: buffer
@@ -51,7 +63,7 @@ constexpr int kEarly = 3;                  // of them, issued in the stage befor
 // the tile's or the matrix's end lie past them and fetch nothing).
 struct Fetch {
     u32x4 wsrc, asrc, wscale, ascale;
-    int wo[4], sw, sa;
+    int wo, ao, step, sw, sa;
 
     __device__ __forceinline__ void set(const Fp4GemmArgs& p, const Tile& t) {
         const int tid = threadIdx.x, lane = tid & 63;
@@ -62,8 +74,9 @@ struct Fetch {
         const int wrows = min(p.N - t.n0, BN);
         wsrc = uniform_rsrc(p.w + wfirst * Kb, (size_t)wrows * Kb);
         asrc = uniform_rsrc(p.a + (size_t)t.row0 * Kb, (size_t)t.valid * Kb);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) wo[q] = (lr + 64 * q) * Kb + 16 * c;
+        wo = (in_pairs(t.valid) ? 2 * (lr & 31) + (lr >> 5) : lr) * Kb + 16 * c;
+        ao = lr * Kb + 16 * c;
+        step = 64 * Kb;
         // scales: wave w the slab's weight rows 32 w + (0 .. 31) and rows 32 (w &
         // 3) + (0 .. 31) (half of them twice, so that every wave issues the same
         // number of copies), 16 bytes a lane; whole words from the one that
@@ -79,23 +92,22 @@ struct Fetch {
                scales(p.as + (size_t)t.row0 * nb, t.valid, ascale)) & ~3) + piece;
     }
 
-    // Copy q (of 4 + NA) of stage j into the slot at LDS byte `at`.  (Every
-    // stage issues its copies: past the last stage with offsets past the
-    // resources.  What the last stage holds past K is left out when it is
-    // multiplied.)
-    template <int NA>
-    __device__ __forceinline__ void copy(int q, int j, int S, int at) const {
+    // Stage j's copies into the slot at LDS byte `at`, in two parts.  (Every
+    // stage issues its copies: past the last stage with empty resources.  What
+    // the last stage holds past K is left out when it is multiplied.)
+    __device__ __forceinline__ int offset(int j, int S) const { return min(j, S - 1) * BK; }
+    __device__ __forceinline__ void early(int j, int S, int at) {
         const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-        const int b = min(j, S - 1) * BK, out = j < S ? 0 : (int)0x80000000;
-        if (q < 4)
-            copy16(wsrc, wo[q] | out, b, at + q * 64 * BK + wave * 1024);
-        else
-            copy16(asrc, wo[q - 4] | out, b, at + kSlotW + (q - 4) * 64 * BK + wave * 1024);
+        if (j >= S) wsrc[2] = 0;
+        copies16<3>(wsrc, wo, wsrc, wo + step, wsrc, wo + 2 * step, offset(j, S),
+                    at + wave * 1024);
     }
-    template <int NA, int Q0, int Q1>
-    __device__ __forceinline__ void copies(int j, int S, int at) const {
-#pragma unroll
-        for (int q = Q0; q < Q1 && q < 4 + NA; ++q) copy<NA>(q, j, S, at);
+    template <int NA>
+    __device__ __forceinline__ void rest(int j, int S, int at) {
+        const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+        if (j >= S) asrc[2] = 0;
+        copies16<1 + NA>(wsrc, wo + 3 * step, asrc, ao, asrc, ao + step, offset(j, S),
+                         at + 3 * 64 * BK + wave * 1024);
     }
     // the slab whose first stage is j: two copies
     __device__ __forceinline__ void slab(int j) const {
@@ -105,23 +117,41 @@ struct Fetch {
     }
     // what is on its way when a tile (of NA row copies) begins
     template <int NA>
-    __device__ __forceinline__ void first(int S) const {
+    __device__ __forceinline__ void first(int S) {
         slab(0);
-        copies<NA, 0, 6>(0, S, 0);
-        copies<NA, 0, 6>(1, S, kSlot);
-        copies<NA, 0, kEarly>(2, S, 2 * kSlot);
+        early(0, S, 0);
+        rest<NA>(0, S, 0);
+        early(1, S, kSlot);
+        rest<NA>(1, S, kSlot);
+        early(2, S, 2 * kSlot);
     }
-    __device__ __forceinline__ void first_stages(int valid, int S) const {
+    __device__ __forceinline__ void first_stages(int valid, int S) {
         if (valid <= 64) first<1>(S);
         else first<2>(S);
     }
 };
 
+// at most N and `stores` (0, 16, 32 or 48) of this wave's memory operations
+// outstanding
+template <int N>
+__device__ __forceinline__ void wait_vm_stores(int stores) {
+    switch (stores) {
+        case 0: wait_vm<N>(); break;
+        case 16: wait_vm<N + 16>(); break;
+        case 32: wait_vm<N + 32>(); break;
+        default: wait_vm<N + 48>(); break;
+    }
+}
+
 // One tile, whose first three stages are on their way into the ring; sends the
 // next tile's (if there are more) off before this one's results are written.
+// `stored`: stores of the tile before, which were issued behind this one's first
+// stages and need not have ended when those have landed.  All stores are
+// issued, those past the rows or columns with offsets past the resource, so
+// that their number is known.  Returns the stores of this tile.
 template <bool F32, int MB>
-__device__ __forceinline__ void run_tile(const Fp4GemmArgs& p, const Tile& t, const Tile& next_t,
-                                         bool more, int per, unsigned char* ring) {
+__device__ __forceinline__ int run_tile(const Fp4GemmArgs& p, const Tile& t, const Tile& next_t,
+                                        bool more, int per, int stored, unsigned char* ring) {
     // (the thread's place as a value of this variant's own: address terms
     // shared by the variants would be kept, or spilled, for all of them)
     int tid = threadIdx.x;
@@ -130,9 +160,7 @@ __device__ __forceinline__ void run_tile(const Fp4GemmArgs& p, const Tile& t, co
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     Fetch f;
     f.set(p, t);
-    // waves: WM along the rows x WN along the weight rows, each MI x NJ
-    // blocks of 32 x 32
-    constexpr int WM = MB == 4 ? 2 : 1, WN = 8 / WM, MI = MB / WM, NJ = 8 / WN, NT = MI * NJ;
+    constexpr int WN = Waves<MB>::WN, MI = Waves<MB>::MI, NJ = Waves<MB>::NJ, NT = MI * NJ;
     constexpr int NA = row_copies(MB), kCopies = 4 + NA;
     const int wm = wave / WN, wn = wave % WN;
     const int N = p.N, nb = p.K / 32;
@@ -141,63 +169,53 @@ __device__ __forceinline__ void run_tile(const Fp4GemmArgs& p, const Tile& t, co
 
     // LDS rows 32 apart share their swizzle, so the rest of an operand's
     // address is an immediate; the chunk index enters it by exclusive or
-    const int rd0 = l32 * BK + ((half ^ swz(l32)) << 4);
+    const int rd0 = l32 * BK + ((4 * half ^ swz(l32)) << 4);
     const int rdw = wn * NJ * 32 * BK + rd0;
     const int rda = kSlotW + wm * MI * 32 * BK + rd0;
-    const int rsw = kRing + (wn * NJ * 32 + l32) * 32;
+    auto wrow = [&](int n) { return wn * NJ * 32 + (NJ == 2 ? 2 * l32 + n : l32); };
+    const int rsw = kRing + wrow(0) * 32;
     const int rsa = kRing + (BN + wm * MI * 32 + l32) * 32;
-    // bits from the copied words' first byte to this half's first scale
+    // bytes of a row's copied words before its first scale
     const uint32_t wbase = (uint32_t)((uintptr_t)p.ws + ((size_t)t.g * N + t.n0) * nb);
     const uint32_t abase = (uint32_t)((uintptr_t)p.as + (size_t)t.row0 * nb);
-    int shw[NJ], sha[MI];
-#pragma unroll
-    for (int n = 0; n < NJ; ++n)
-        shw[n] = 8 * (int)((wbase + (uint32_t)((wn * NJ + n) * 32 + l32) * nb) & 3) + 8 * half;
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-        sha[i] = 8 * (int)((abase + (uint32_t)((wm * MI + i) * 32 + l32) * nb) & 3) + 8 * half;
-
-    // a slab's words; two are used up a stage
-    u32x4 qw[NJ][2], qa[MI][2];
+    // this half's words of the slab's stages, the next stage's first
+    u32x4 cw[NJ], ca[MI];
     auto read_slab = [&]() {
-#pragma unroll
-        for (int n = 0; n < NJ; ++n)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                qw[n][h] = *(const u32x4*)(ring + rsw + n * 32 * 32 + 16 * h);
-#pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                qa[i][h] = *(const u32x4*)(ring + rsa + i * 32 * 32 + 16 * h);
-    };
-    // The next stage's scales: bytes 0 and 2 of word 0 those of steps 0 and 1, of
-    // word 1 of 2 and 3
-    int cw[NJ][2], ca[MI][2];
-    auto scales = [&]() {
-        auto take = [](u32x4& x, u32x4& y, int by, int& c0, int& c1) {
-            c0 = (int)(uint32_t)((((uint64_t)x[1] << 32) | x[0]) >> by);
-            c1 = (int)(uint32_t)((((uint64_t)x[2] << 32) | x[1]) >> by);
-            x = u32x4{x[2], x[3], y[0], y[1]};
-            y = u32x4{y[2], y[3], 0u, 0u};
+        auto words = [&](int at, uint32_t mis, u32x4& c) {
+            u32x4 x = *(const u32x4*)(ring + at), y = *(const u32x4*)(ring + at + 16);
+            if (per == 3) {
+                x = u32x4{__builtin_amdgcn_alignbyte(x[1], x[0], mis),
+                          __builtin_amdgcn_alignbyte(x[2], x[1], mis),
+                          __builtin_amdgcn_alignbyte(x[3], x[2], mis),
+                          __builtin_amdgcn_alignbyte(y[0], x[3], mis)};
+                y = u32x4{__builtin_amdgcn_alignbyte(y[1], y[0], mis),
+                          __builtin_amdgcn_alignbyte(y[2], y[1], mis), 0u, 0u};
+            }
+            c = half ? u32x4{x[1], x[3], y[1], y[3]} : u32x4{x[0], x[2], y[0], y[2]};
         };
 #pragma unroll
-        for (int n = 0; n < NJ; ++n) take(qw[n][0], qw[n][1], shw[n], cw[n][0], cw[n][1]);
+        for (int n = 0; n < NJ; ++n)
+            words(rsw + n * 32, (wbase + (uint32_t)wrow(n) * nb) & 3, cw[n]);
 #pragma unroll
-        for (int i = 0; i < MI; ++i) take(qa[i][0], qa[i][1], sha[i], ca[i][0], ca[i][1]);
+        for (int i = 0; i < MI; ++i)
+            words(rsa + i * 32 * 32, (abase + (uint32_t)((wm * MI + i) * 32 + l32) * nb) & 3, ca[i]);
+    };
+    auto next_scales = [&]() {
+#pragma unroll
+        for (int n = 0; n < NJ; ++n) cw[n] = u32x4{cw[n][1], cw[n][2], cw[n][3], 0u};
+#pragma unroll
+        for (int i = 0; i < MI; ++i) ca[i] = u32x4{ca[i][1], ca[i][2], ca[i][3], 0u};
     };
     // the last stage's blocks past K: any finite scale
     auto finite = [&]() {
-        auto mask = [&](int& c0, int& c1) {
-            if (half >= tail) c0 = (c0 & ~0xff) | 127;
-            if (2 + half >= tail) c0 = (c0 & ~0xff0000) | 127 << 16;
-            if (4 + half >= tail) c1 = (c1 & ~0xff) | 127;
-            if (6 + half >= tail) c1 = (c1 & ~0xff0000) | 127 << 16;
-        };
+        uint32_t keep = 0;
 #pragma unroll
-        for (int n = 0; n < NJ; ++n) mask(cw[n][0], cw[n][1]);
+        for (int q = 0; q < 4; ++q)
+            if (4 * half + q < tail) keep |= 0xffu << (8 * q);
 #pragma unroll
-        for (int i = 0; i < MI; ++i) mask(ca[i][0], ca[i][1]);
+        for (int n = 0; n < NJ; ++n) cw[n][0] = (cw[n][0] & keep) | (0x7f7f7f7fu & ~keep);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) ca[i][0] = (ca[i][0] & keep) | (0x7f7f7f7fu & ~keep);
     };
 
     f32x16 acc[MI][NJ];
@@ -217,7 +235,7 @@ __device__ __forceinline__ void run_tile(const Fp4GemmArgs& p, const Tile& t, co
                 *(u32x4*)(ring + slot + q * 64 * BK + tid * 16) = u32x4{0u, 0u, 0u, 0u};
     };
     // stage 0 and the first slab have landed
-    wait_vm<kCopies + kEarly>();
+    wait_vm_stores<kCopies + kEarly>(stored);
     if (tail && S == 1) zeros(0);
     __syncthreads();
     // The middle of stage j: stage j + 1 has landed (the copies behind it are
@@ -226,7 +244,8 @@ __device__ __forceinline__ void run_tile(const Fp4GemmArgs& p, const Tile& t, co
     // slab if stage j is its first.
     bool sent = false;
     auto turn = [&](int j, int next) {
-        if (sent) wait_vm<kCopies + 2>();
+        if (j == 0) wait_vm_stores<kCopies>(stored);
+        else if (sent) wait_vm<kCopies + 2>();
         else wait_vm<kCopies>();
         if (tail && j == S - 2) zeros(next);
         __syncthreads();
@@ -237,23 +256,24 @@ __device__ __forceinline__ void run_tile(const Fp4GemmArgs& p, const Tile& t, co
         constexpr int q = decltype(step)::value, B = q & 1;
 #pragma unroll
         for (int n = 0; n < NJ; ++n)
-            rw[B][n] = *(const u32x4*)(ring + ((rdw + slot) ^ (q << 5)) + n * 32 * BK);
+            rw[B][n] = *(const u32x4*)(ring + ((rdw ^ (q << 4)) + slot) + n * 32 * BK);
 #pragma unroll
         for (int i = 0; i < MI; ++i)
-            ra[B][i] = *(const u32x4*)(ring + ((rda + slot) ^ (q << 5)) + i * 32 * BK);
+            ra[B][i] = *(const u32x4*)(ring + ((rda ^ (q << 4)) + slot) + i * 32 * BK);
     };
     auto wide = [](const u32x4& v) {
         return v8i{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
     };
-    // the products of a step, a copy (of up to four) behind each
+    // the products of a step, copies behind the first
     auto multiply = [&](auto step, auto copy) {
-        constexpr int q = decltype(step)::value, B = q & 1, W = q >> 1, O = 2 * (q & 1);
+        constexpr int q = decltype(step)::value, B = q & 1;
         static_for<0, 4>([&](auto index) {
             constexpr int x = decltype(index)::value, i = x / NJ, n = x % NJ;
             if constexpr (x < NT)
                 acc[i][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                    wide(rw[B][n]), wide(ra[B][i]), acc[i][n], 4, 4, O, cw[n][W], O, ca[i][W]);
-            copy(index);
+                    wide(ra[B][i]), wide(rw[B][n]), acc[i][n], 4, 4, q, (int)ca[i][0], q,
+                    (int)cw[n][0]);
+            if constexpr (x == 0) copy();
         });
         // (the products stay here: the compiler would take them all to the end of
         // the stage, behind its branches)
@@ -269,37 +289,28 @@ __device__ __forceinline__ void run_tile(const Fp4GemmArgs& p, const Tile& t, co
     using Q3 = std::integral_constant<int, 3>;
     read(0, Q0());
     read_slab();
-    scales();
     if (tail && S == 1) finite();
     int slot = 0, at = 0;                           // at: the stage's place in its slab
     for (int j = 0; j < S; ++j) {
         const int next = slot == 2 * kSlot ? 0 : slot + kSlot;
         const int last = next == 2 * kSlot ? 0 : next + kSlot;
         read(slot, Q1());
-        multiply(Q0(), [&](auto x) {
-            constexpr int c = 3 + decltype(x)::value;
-            if constexpr (c < 5) f.template copies<NA, c, c + 1>(j + 2, S, last);
-        });
+        multiply(Q0(), [&]() { f.template rest<NA>(j + 2, S, last); });
         read(slot, Q2());
-        multiply(Q1(), [&](auto x) {
-            constexpr int c = 5 + decltype(x)::value;
-            if constexpr (c < 6) f.template copies<NA, c, c + 1>(j + 2, S, last);
-        });
+        multiply(Q1(), []() {});
         read(slot, Q3());
-        multiply(Q2(), [](auto) {});
+        multiply(Q2(), []() {});
         turn(j, next);
         read(next, Q0());                           // (past the end: not used)
         sent = at == 0 && j + per < S;
         if (sent) f.slab(j + per);
+        multiply(Q3(), [&]() { f.early(j + 3, S, slot); });
         if (++at == per) {
             at = 0;
             read_slab();
+        } else {
+            next_scales();
         }
-        multiply(Q3(), [&](auto x) {
-            constexpr int c = decltype(x)::value;
-            if constexpr (c < kEarly) f.template copies<NA, c, c + 1>(j + 3, S, slot);
-        });
-        scales();
         if (tail && j == S - 2) finite();
         slot = next;
     }
@@ -310,39 +321,40 @@ __device__ __forceinline__ void run_tile(const Fp4GemmArgs& p, const Tile& t, co
         nf.first_stages(next_t.valid, S);
     }
 
-    // Lane l holds, of row l % 32 of its block, weight rows 8 q + 4 (l / 32) +
-    // (0 .. 3), q < 4.  The stores of a wave fill 32 to 64 bytes of a row each;
-    // the L2 joins them to lines.
+    // Lane l holds, of column l % 32 of its block (of columns 2 (l % 32) and the
+    // next of two blocks), rows 8 q + 4 (l / 32) + (0 .. 3), q < 4.  A store
+    // fills whole lines of two rows, or halves of them (bf16 of one block): with
+    // a lane along the rows its 32 bytes of each of 32 lines were what the L2
+    // took four times as long for.
+    constexpr int ES = F32 ? 4 : 2;
+    const uint64_t base = (uint64_t)(uintptr_t)p.out + ((size_t)t.row0 * N + t.n0) * ES;
+    const uint64_t first =
+        (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)base) |
+        (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(base >> 32)) << 32;
+    const uint32_t bytes = (uint32_t)(((size_t)(t.valid - 1) * N + (N - t.n0)) * ES);
+    const auto out = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(uintptr_t)first, 0, __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000);
+    const int col = wrow(0);
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-        const int r = (wm * MI + i) * 32 + l32;
-        const size_t at = (size_t)(t.row0 + r) * N + t.n0;
 #pragma unroll
-        for (int n = 0; n < NJ; ++n) {
-            const f32x16& v = acc[i][n];
-            if constexpr (F32) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int col = (wn * NJ + n) * 32 + 8 * q + 4 * half;
-                    if (r < t.valid && t.n0 + col < N)
-                        *(f32x4*)((float*)p.out + at + col) =
-                            f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-                }
-            } else {
-                // (the half-waves exchange, so that a lane holds 8 columns in a row)
-#pragma unroll
-                for (int q = 0; q < 4; q += 2) {
-                    const u32x2 x = swap_halves(bf16_pack2(v[4 * q], v[4 * q + 1]),
-                                                bf16_pack2(v[4 * q + 4], v[4 * q + 5]));
-                    const u32x2 y = swap_halves(bf16_pack2(v[4 * q + 2], v[4 * q + 3]),
-                                                bf16_pack2(v[4 * q + 6], v[4 * q + 7]));
-                    const int col = (wn * NJ + n) * 32 + 8 * (q + half);
-                    if (r < t.valid && t.n0 + col < N)
-                        *(u32x4*)((uint16_t*)p.out + at + col) = u32x4{x[0], y[0], x[1], y[1]};
-                }
-            }
+        for (int e = 0; e < 16; ++e) {
+            const int r = (wm * MI + i) * 32 + 8 * (e >> 2) + 4 * half + (e & 3);
+            const uint32_t in = ((uint32_t)r * (uint32_t)N + (uint32_t)col) * ES;
+            const int at = (int)(r < t.valid && t.n0 + col < N ? in : 0xfffffff0u);
+            const float x = acc[i][0][e], y = acc[i][NJ - 1][e];
+            if constexpr (F32 && NJ == 2)
+                __builtin_amdgcn_raw_buffer_store_b64(
+                    u32x2{__float_as_uint(x), __float_as_uint(y)}, out, at, 0, 0);
+            else if constexpr (F32)
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), out, at, 0, 0);
+            else if constexpr (NJ == 2)
+                __builtin_amdgcn_raw_buffer_store_b32(bf16_pack2(x, y), out, at, 0, 0);
+            else
+                __builtin_amdgcn_raw_buffer_store_b16((uint16_t)bf16_pack2(x, x), out, at, 0, 0);
         }
     }
+    return Waves<MB>::kStores;
 }
 
 // row tiles of a group of n rows, tiles of up to `blocks` blocks of 32 rows
@@ -431,15 +443,15 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_kernel(Fp4GemmArgs p) {
         f.set(p, t);
         f.first_stages(t.valid, S);
     }
-    for (;;) {
+    for (int stored = 0;;) {
         const bool more = q + step < end;
         Tile next = t;
         if (more) find(q + step, next);
         switch ((t.valid + 31) >> 5) {
-            case 1: run_tile<F32, 1>(p, t, next, more, per, smem); break;
-            case 2: run_tile<F32, 2>(p, t, next, more, per, smem); break;
-            case 3: run_tile<F32, 3>(p, t, next, more, per, smem); break;
-            default: run_tile<F32, 4>(p, t, next, more, per, smem); break;
+            case 1: stored = run_tile<F32, 1>(p, t, next, more, per, stored, smem); break;
+            case 2: stored = run_tile<F32, 2>(p, t, next, more, per, stored, smem); break;
+            case 3: stored = run_tile<F32, 3>(p, t, next, more, per, stored, smem); break;
+            default: stored = run_tile<F32, 4>(p, t, next, more, per, stored, smem); break;
         }
         if (!more) break;
         t = next;

@@ -28,6 +28,43 @@ __device__ __forceinline__ void copy16(u32x4 rsrc, int voffset, int soffset, int
         : "s"(at), "v"(voffset), "s"(rsrc), "s"(soffset)
         : "memory");
 }
+// Three such copies (N = 2: two) to places 8 KB apart, M0 saved once
+template <int N>
+__device__ __forceinline__ void copies16(u32x4 r0, int v0, u32x4 r1, int v1, u32x4 r2, int v2,
+                                         int soffset, int lds) {
+    const int at = __builtin_amdgcn_readfirstlane(lds);
+    soffset = __builtin_amdgcn_readfirstlane(soffset);
+    int saved;
+    if constexpr (N == 3)
+        asm volatile(
+            "s_mov_b32 %0, m0\n\t"
+            "s_mov_b32 m0, %1\n\t"
+            "s_nop 0\n\t"
+            "buffer_load_dwordx4 %2, %5, %8 offen lds\n\t"
+            "s_add_u32 m0, m0, 0x2000\n\t"
+            "s_nop 0\n\t"
+            "buffer_load_dwordx4 %3, %6, %8 offen lds\n\t"
+            "s_add_u32 m0, m0, 0x2000\n\t"
+            "s_nop 0\n\t"
+            "buffer_load_dwordx4 %4, %7, %8 offen lds\n\t"
+            "s_mov_b32 m0, %0"
+            : "=&s"(saved)
+            : "s"(at), "v"(v0), "v"(v1), "v"(v2), "s"(r0), "s"(r1), "s"(r2), "s"(soffset)
+            : "memory", "scc");
+    else
+        asm volatile(
+            "s_mov_b32 %0, m0\n\t"
+            "s_mov_b32 m0, %1\n\t"
+            "s_nop 0\n\t"
+            "buffer_load_dwordx4 %2, %4, %6 offen lds\n\t"
+            "s_add_u32 m0, m0, 0x2000\n\t"
+            "s_nop 0\n\t"
+            "buffer_load_dwordx4 %3, %5, %6 offen lds\n\t"
+            "s_mov_b32 m0, %0"
+            : "=&s"(saved)
+            : "s"(at), "v"(v0), "v"(v1), "s"(r0), "s"(r1), "s"(soffset)
+            : "memory", "scc");
+}
 __device__ __forceinline__ void copy4(const void* from, int lds) {
     const int at = __builtin_amdgcn_readfirstlane(lds);
     int saved;
