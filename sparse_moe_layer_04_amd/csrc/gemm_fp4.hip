@@ -44,8 +44,9 @@ struct Tile {
     int g, row0, valid, n0;                // n0: first weight row
 };
 
-// copies of codes a wave and stage: 4 of W, NA (one for each 64 rows) of A
-constexpr int row_copies(int blocks) { return (blocks + 1) / 2; }
+// copies of codes a wave and stage: 4 of W, 2 of A; 3 of them are issued after
+// the middle of a stage, the others before the middle of the next
+constexpr int kEarly = 3, kCopies = 6;
 // Waves of a tile of `blocks` blocks of 32 rows: along the rows x along the
 // weight rows, each MI x NJ blocks of 32 x 32.  With NJ = 2 the two blocks of
 // weight rows hold every other one of 64, so that a lane has neighbouring
@@ -56,19 +57,101 @@ struct Waves {
     static constexpr int kStores = 16 * MI;   // of a wave, whatever the output's type
 };
 __device__ __forceinline__ bool in_pairs(int valid) { return ((valid - 1) >> 5) & 1; }
-constexpr int kEarly = 3;                  // of them, issued in the stage before
 
-// The copies of a tile's operands into LDS, set up once per tile: buffer
-// resources over the tile's rows (wave-uniform base, 32-bit offsets; rows past
-// the tile's or the matrix's end lie past them and fetch nothing).
-struct Fetch {
+// row tiles of a group of n rows, tiles of up to `blocks` blocks of 32 rows
+__device__ __forceinline__ int row_tiles(int n, int blocks) {
+    const int c = (n + 31) >> 5;
+    return blocks == 1 ? c : blocks == 2 ? (c + 1) >> 1 : blocks == 3 ? (c + 2) / 3 : (c + 3) >> 2;
+}
+
+// Items are (group, band of kBand m-tiles, n-tile, m-tile), the 8 XCDs take
+// contiguous ranges, so that the m-tiles of a weight tile and the n-tiles of a
+// group's rows meet in one XCD's L2.  A group's rows split evenly over its
+// m-tiles.  The group of an item comes from a two-level sum that every wave
+// keeps in registers: lane l holds the items before run l of ceil(G / 64)
+// groups, and looks into the run that holds the item.
+constexpr int kBand = 8;
+constexpr int kTallest = BM / 32;
+static_assert(MOE_MAX_GROUPS <= 64 * 64, "one lane a run, one lane a group of a run");
+
+struct Schedule {
+    const int32_t* offsets;
+    int G, rows, NT, run, blocks;
+    int mine, upto;                        // of this lane's run
+
+    __device__ __forceinline__ int clamped(int v) const { return min(max(v, 0), rows); }
+    __device__ __forceinline__ void set(const Fp4GemmArgs& p, int lane) {
+        offsets = p.offsets;
+        G = p.G;
+        rows = p.rows;
+        NT = (p.N + BN - 1) / BN;
+        run = (G + 63) / 64;
+        // the row tiles of this lane's run, of up to 1 .. 4 blocks
+        int tiles[kTallest + 1] = {};
+        for (int i = 0; i < run; ++i) {
+            const int g = lane * run + i;
+            if (g < G) {
+                const int n = max(clamped(offsets[g + 1]) - clamped(offsets[g]), 0);
+#pragma unroll
+                for (int b = 1; b <= kTallest; ++b) tiles[b] += row_tiles(n, b);
+            }
+        }
+        blocks = kTallest;
+        mine = NT * tiles[kTallest];
+        upto = wave_scan(mine, lane);
+        // few tiles: the lowest of which every one still has a CU of its own
+        if ((long long)rows * NT <= 96ll * gridDim.x && items() < (int)gridDim.x) {
+#pragma unroll
+            for (int b = 1; b < kTallest; ++b) {
+                const int sum = wave_scan(NT * tiles[b], lane);
+                if (__builtin_amdgcn_readlane(sum, 63) > (int)gridDim.x) continue;
+                blocks = b;
+                mine = NT * tiles[b];
+                upto = sum;
+                break;
+            }
+        }
+    }
+    __device__ __forceinline__ int items() const { return __builtin_amdgcn_readlane(upto, 63); }
+    __device__ __forceinline__ void find(int q, Tile& t) const {
+        // the first lane whose sum passes q, then the groups of its run in
+        // turn (scalar loads: a vector load would wait for the copies that are
+        // on their way)
+        const int r = __builtin_ctzll(__builtin_amdgcn_ballot_w64(upto > q));
+        int local = q - __builtin_amdgcn_readlane(upto - mine, r);
+        t.g = r * run;
+        int r0 = clamped(scalar_load(offsets + t.g)), n, mt;
+        for (;; ++t.g) {                             // (ends: the run holds item q)
+            const int r1 = clamped(scalar_load(offsets + t.g + 1));
+            n = max(r1 - r0, 0);
+            mt = row_tiles(n, blocks);
+            if (local < NT * mt || t.g + 1 >= G) break;
+            local -= NT * mt;
+            r0 = r1;
+        }
+        const int per = ((n + mt - 1) / mt + 31) & ~31;
+        const int band = local / (kBand * NT) * kBand, high = min(kBand, mt - band);
+        local -= band * NT;
+        t.n0 = local / high * BN;
+        t.row0 = r0 + (band + local % high) * per;
+        t.valid = min(per, r0 + n - t.row0);
+    }
+};
+
+// What goes into LDS, stage after stage and tile after tile: the copies run two
+// and a half stages ahead of the products, across the ends of tiles.  Buffer
+// resources over a tile's rows (wave-uniform base, 32-bit offsets; rows past the
+// tile's or the matrix's end lie past them and fetch nothing).
+struct Feed {
+    Schedule sched;
+    Tile t;                                // the tile that is fetched
+    int q, step, end;                      // its item, the next one's distance, their end
+    int j, S;                              // its next stage, and its stages
     u32x4 wsrc, asrc, wscale, ascale;
-    int wo, ao, step, sw, sa;
+    int wo, ao, rows64, sw, sa;
 
-    __device__ __forceinline__ void set(const Fp4GemmArgs& p, const Tile& t) {
-        const int tid = threadIdx.x, lane = tid & 63;
-        const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-        const int Kb = p.K / 2, nb = p.K / 32;
+    __device__ __forceinline__ void set(const Fp4GemmArgs& p) {
+        const int tid = threadIdx.x, Kb = p.K / 2;
         const int lr = tid >> 3, c = (tid & 7) ^ swz(lr);   // chunk c of row lr + 64 q
         const size_t wfirst = (size_t)t.g * p.N + t.n0;
         const int wrows = min(p.N - t.n0, BN);
@@ -76,7 +159,15 @@ struct Fetch {
         asrc = uniform_rsrc(p.a + (size_t)t.row0 * Kb, (size_t)t.valid * Kb);
         wo = (in_pairs(t.valid) ? 2 * (lr & 31) + (lr >> 5) : lr) * Kb + 16 * c;
         ao = lr * Kb + 16 * c;
-        step = 64 * Kb;
+        rows64 = 64 * Kb;
+        set_scales(p, t);
+        j = 0;
+    }
+    __device__ __forceinline__ void set_scales(const Fp4GemmArgs& p, const Tile& t) {
+        const int lane = threadIdx.x & 63, nb = p.K / 32;
+        const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+        const size_t wfirst = (size_t)t.g * p.N + t.n0;
+        const int wrows = min(p.N - t.n0, BN);
         // scales: wave w the slab's weight rows 32 w + (0 .. 31) and rows 32 (w &
         // 3) + (0 .. 31) (half of them twice, so that every wave issues the same
         // number of copies), 16 bytes a lane; whole words from the one that
@@ -92,42 +183,36 @@ struct Fetch {
                scales(p.as + (size_t)t.row0 * nb, t.valid, ascale)) & ~3) + piece;
     }
 
-    // Stage j's copies into the slot at LDS byte `at`, in two parts.  (Every
-    // stage issues its copies: past the last stage with empty resources.  What
-    // the last stage holds past K is left out when it is multiplied.)
-    __device__ __forceinline__ int offset(int j, int S) const { return min(j, S - 1) * BK; }
-    __device__ __forceinline__ void early(int j, int S, int at) {
+    // The next stage's copies into the slot at LDS byte `at`, in two parts; the
+    // first goes on to the next tile where one ends (past the last with empty
+    // resources: every stage issues its copies).  What a tile's last stage holds
+    // past K is left out when it is multiplied.
+    __device__ __forceinline__ void early(const Fp4GemmArgs& p, int at) {
         const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-        if (j >= S) wsrc[2] = 0;
-        copies16<3>(wsrc, wo, wsrc, wo + step, wsrc, wo + 2 * step, offset(j, S),
-                    at + wave * 1024);
+        if (j == S) {
+            q += step;
+            j = 0;
+            if (q < end) {
+                sched.find(q, t);
+                set(p);
+            } else {
+                q = end;
+                wsrc[2] = asrc[2] = 0;
+            }
+        }
+        copies16<3>(wsrc, wo, wsrc, wo + rows64, wsrc, wo + 2 * rows64, j * BK, at + wave * 1024);
     }
-    template <int NA>
-    __device__ __forceinline__ void rest(int j, int S, int at) {
+    __device__ __forceinline__ void rest(int at) {
         const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-        if (j >= S) asrc[2] = 0;
-        copies16<1 + NA>(wsrc, wo + 3 * step, asrc, ao, asrc, ao + step, offset(j, S),
-                         at + 3 * 64 * BK + wave * 1024);
+        copies16<3>(wsrc, wo + 3 * rows64, asrc, ao, asrc, ao + rows64, j * BK,
+                    at + 3 * 64 * BK + wave * 1024);
+        ++j;
     }
     // the slab whose first stage is j: two copies
     __device__ __forceinline__ void slab(int j) const {
         const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
         copy16(wscale, sw, j * 8, kRing + wave * 1024);
         copy16(ascale, sa, j * 8, kRing + 32 * BN + (wave & 3) * 1024);
-    }
-    // what is on its way when a tile (of NA row copies) begins
-    template <int NA>
-    __device__ __forceinline__ void first(int S) {
-        slab(0);
-        early(0, S, 0);
-        rest<NA>(0, S, 0);
-        early(1, S, kSlot);
-        rest<NA>(1, S, kSlot);
-        early(2, S, 2 * kSlot);
-    }
-    __device__ __forceinline__ void first_stages(int valid, int S) {
-        if (valid <= 64) first<1>(S);
-        else first<2>(S);
     }
 };
 
@@ -143,29 +228,44 @@ __device__ __forceinline__ void wait_vm_stores(int stores) {
     }
 }
 
-// One tile, whose first three stages are on their way into the ring; sends the
-// next tile's (if there are more) off before this one's results are written.
-// `stored`: stores of the tile before, which were issued behind this one's first
-// stages and need not have ended when those have landed.  All stores are
-// issued, those past the rows or columns with offsets past the resource, so
-// that their number is known.  Returns the stores of this tile.
+// Of a tile's last stage, what this thread copied from past K (its blocks from
+// `tail` on) becomes zeros, in W alone: the products are then zero, as no code
+// is an infinity or NaN.
+__device__ __forceinline__ void zeros(unsigned char* ring, int slot, int tail) {
+    const int tid = threadIdx.x;
+    if (((tid & 7) ^ swz(tid >> 3)) >= tail)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            *(u32x4*)(ring + slot + q * 64 * BK + tid * 16) = u32x4{0u, 0u, 0u, 0u};
+}
+
+// What a workgroup's tiles have in common
+struct Run {
+    int S, tail;                           // stages, blocks of a short last one (0: none)
+    int per;                               // stages of a slab of scales
+    int slab_at;                           // the stage that sends the next tile's first slab
+    bool late;                             // which then lands only when that tile begins
+};
+
+// One tile, whose first stage has landed in the ring at `slot` and whose next
+// two are on their way (and its first slab; with fewer than three stages it is
+// fetched here).  `stored`: stores of the tile before, which were issued behind
+// those and need not have ended when they have landed.  All stores are issued,
+// those past the rows or columns with offsets past the resource, so that their
+// number is known.  Returns the stores of this tile.
 template <bool F32, int MB>
-__device__ __forceinline__ int run_tile(const Fp4GemmArgs& p, const Tile& t, const Tile& next_t,
-                                        bool more, int per, int stored, unsigned char* ring) {
+__device__ __forceinline__ int run_tile(const Fp4GemmArgs& p, const Tile& t, Feed& f, const Run& c,
+                                        int& slot, int stored, unsigned char* ring) {
     // (the thread's place as a value of this variant's own: address terms
     // shared by the variants would be kept, or spilled, for all of them)
     int tid = threadIdx.x;
     asm volatile("" : "+v"(tid));
     const int lane = tid & 63, half = lane >> 5, l32 = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    Fetch f;
-    f.set(p, t);
     constexpr int WN = Waves<MB>::WN, MI = Waves<MB>::MI, NJ = Waves<MB>::NJ, NT = MI * NJ;
-    constexpr int NA = row_copies(MB), kCopies = 4 + NA;
     const int wm = wave / WN, wn = wave % WN;
     const int N = p.N, nb = p.K / 32;
-    const int S = (p.K / 2 + BK - 1) / BK;
-    const int tail = nb & 7;               // blocks of a short last stage
+    const int S = c.S, tail = c.tail, per = c.per;
 
     // LDS rows 32 apart share their swizzle, so the rest of an operand's
     // address is an immediate; the chunk index enters it by exclusive or
@@ -226,28 +326,27 @@ __device__ __forceinline__ int run_tile(const Fp4GemmArgs& p, const Tile& t, con
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][n][e] = 0.0f;
 
-    // Of the last stage, what this thread copied from past K becomes zeros (in W
-    // alone: the products are then zero, as no code is an infinity or NaN).
-    auto zeros = [&](int slot) {
-        if (((tid & 7) ^ swz(tid >> 3)) >= tail)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                *(u32x4*)(ring + slot + q * 64 * BK + tid * 16) = u32x4{0u, 0u, 0u, 0u};
-    };
-    // stage 0 and the first slab have landed
-    wait_vm_stores<kCopies + kEarly>(stored);
-    if (tail && S == 1) zeros(0);
-    __syncthreads();
-    // The middle of stage j: stage j + 1 has landed (the copies behind it are
-    // stage j + 2's, and a slab that was sent off just before those) and every
-    // wave has read stage j's operands, whose slot takes stage j + 3's, and the
-    // slab if stage j is its first.
+    if (S < 3) {
+        // (the feed is past the next tile: this one's slab is not sent ahead)
+        __syncthreads();                            // (the last tile's has been read)
+        f.set_scales(p, t);
+        f.slab(0);
+        wait_vm<0>();
+        __syncthreads();
+    } else if (c.late && stored) {
+        wait_vm_stores<0>(stored);
+        __syncthreads();
+    }
+    // The middle of stage j: the next stage has landed (the copies behind it are
+    // those of the one after it, a slab that was sent off just before them, and
+    // the last tile's stores) and every wave has read stage j's operands, whose
+    // slot takes the next but two, and the slab if stage j is its first.
     bool sent = false;
     auto turn = [&](int j, int next) {
         if (j == 0) wait_vm_stores<kCopies>(stored);
-        else if (sent) wait_vm<kCopies + 2>();
+        else if (sent && j + 1 < S) wait_vm<kCopies + 2>();
         else wait_vm<kCopies>();
-        if (tail && j == S - 2) zeros(next);
+        if (tail && (j == S - 2 || S == 1)) zeros(ring, next, tail);
         __syncthreads();
     };
 
@@ -287,24 +386,25 @@ __device__ __forceinline__ int run_tile(const Fp4GemmArgs& p, const Tile& t, con
     using Q1 = std::integral_constant<int, 1>;
     using Q2 = std::integral_constant<int, 2>;
     using Q3 = std::integral_constant<int, 3>;
-    read(0, Q0());
+    read(slot, Q0());
     read_slab();
     if (tail && S == 1) finite();
-    int slot = 0, at = 0;                           // at: the stage's place in its slab
+    int at = 0;                                     // the stage's place in its slab
     for (int j = 0; j < S; ++j) {
         const int next = slot == 2 * kSlot ? 0 : slot + kSlot;
         const int last = next == 2 * kSlot ? 0 : next + kSlot;
         read(slot, Q1());
-        multiply(Q0(), [&]() { f.template rest<NA>(j + 2, S, last); });
+        multiply(Q0(), [&]() { f.rest(last); });
         read(slot, Q2());
         multiply(Q1(), []() {});
         read(slot, Q3());
         multiply(Q2(), []() {});
         turn(j, next);
-        read(next, Q0());                           // (past the end: not used)
-        sent = at == 0 && j + per < S;
-        if (sent) f.slab(j + per);
-        multiply(Q3(), [&]() { f.early(j + 3, S, slot); });
+        read(next, Q0());                           // (of the next tile: read again)
+        multiply(Q3(), [&]() { f.early(p, slot); });
+        const bool inner = at == 0 && j + per < S;
+        sent = inner || j == c.slab_at;
+        if (sent) f.slab(inner ? j + per : 0);
         if (++at == per) {
             at = 0;
             read_slab();
@@ -313,12 +413,6 @@ __device__ __forceinline__ int run_tile(const Fp4GemmArgs& p, const Tile& t, con
         }
         if (tail && j == S - 2) finite();
         slot = next;
-    }
-    // (every wave has read the last stage; what the ring still holds is unused)
-    if (more) {
-        Fetch nf;
-        nf.set(p, next_t);
-        nf.first_stages(next_t.valid, S);
     }
 
     // Lane l holds, of column l % 32 of its block (of columns 2 (l % 32) and the
@@ -357,105 +451,52 @@ __device__ __forceinline__ int run_tile(const Fp4GemmArgs& p, const Tile& t, con
     return Waves<MB>::kStores;
 }
 
-// row tiles of a group of n rows, tiles of up to `blocks` blocks of 32 rows
-__device__ __forceinline__ int row_tiles(int n, int blocks) {
-    const int c = (n + 31) >> 5;
-    return blocks == 1 ? c : blocks == 2 ? (c + 1) >> 1 : blocks == 3 ? (c + 2) / 3 : (c + 3) >> 2;
-}
-
-// Persistent grid, one workgroup a CU.  Items are (group, band of kBand
-// m-tiles, n-tile, m-tile), the 8 XCDs take contiguous ranges, so that the
-// m-tiles of a weight tile and the n-tiles of a group's rows meet in one XCD's
-// L2.  A group's rows split evenly over its m-tiles.  The group of an item
-// comes from a two-level sum that every wave keeps in registers: lane l holds
-// the items before run l of ceil(G / 64) groups, and looks into the run that
-// holds the item.
-constexpr int kBand = 8;
-constexpr int kTallest = BM / 32;
-static_assert(MOE_MAX_GROUPS <= 64 * 64, "one lane a run, one lane a group of a run");
-
+// Persistent grid, one workgroup a CU
 template <bool F32>
 __global__ __launch_bounds__(kThreads) void gemm_mxfp4_kernel(Fp4GemmArgs p) {
     extern __shared__ __align__(16) unsigned char smem[];
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int G = p.G, rows = p.rows, Kb = p.K / 2, S = (Kb + BK - 1) / BK;
-    const int NT = (p.N + BN - 1) / BN;
-    auto clamped = [&](int v) { return min(max(v, 0), rows); };
-    const int run = (G + 63) / 64;
-    // the row tiles of this lane's run, of up to 1 .. 4 blocks
-    int tiles[kTallest + 1] = {};
-    for (int i = 0; i < run; ++i) {
-        const int g = lane * run + i;
-        if (g < G) {
-            const int n = max(clamped(p.offsets[g + 1]) - clamped(p.offsets[g]), 0);
-#pragma unroll
-            for (int b = 1; b <= kTallest; ++b) tiles[b] += row_tiles(n, b);
-        }
-    }
-    int blocks = kTallest, mine = NT * tiles[kTallest], upto = wave_scan(mine, lane);
-    // few tiles: the lowest of which every one still has a CU of its own
-    if ((long long)rows * NT <= 96ll * gridDim.x &&
-        __builtin_amdgcn_readlane(upto, 63) < (int)gridDim.x) {
-#pragma unroll
-        for (int b = 1; b < kTallest; ++b) {
-            const int sum = wave_scan(NT * tiles[b], lane);
-            if (__builtin_amdgcn_readlane(sum, 63) > (int)gridDim.x) continue;
-            blocks = b;
-            mine = NT * tiles[b];
-            upto = sum;
-            break;
-        }
-    }
-    const long long Q = __builtin_amdgcn_readlane(upto, 63);
-    const int xcd = blockIdx.x & 7, step = gridDim.x >> 3;
-    const int end = (int)(Q * (xcd + 1) / 8);
-    auto find = [&](int q, Tile& t) {
-        // the first lane whose sum passes q, then the groups of its run in
-        // turn (scalar loads: a vector load would wait for the copies that are
-        // on their way)
-        const int r = __builtin_ctzll(__builtin_amdgcn_ballot_w64(upto > q));
-        int local = q - __builtin_amdgcn_readlane(upto - mine, r);
-        t.g = r * run;
-        int r0 = clamped(scalar_load(p.offsets + t.g)), n, mt;
-        for (;; ++t.g) {                             // (ends: the run holds item q)
-            const int r1 = clamped(scalar_load(p.offsets + t.g + 1));
-            n = max(r1 - r0, 0);
-            mt = row_tiles(n, blocks);
-            if (local < NT * mt || t.g + 1 >= G) break;
-            local -= NT * mt;
-            r0 = r1;
-        }
-        const int per = ((n + mt - 1) / mt + 31) & ~31;
-        const int band = local / (kBand * NT) * kBand, high = min(kBand, mt - band);
-        local -= band * NT;
-        t.n0 = local / high * BN;
-        t.row0 = r0 + (band + local % high) * per;
-        t.valid = min(per, r0 + n - t.row0);
-    };
-    // stages of a slab of scales
-    const int per = (p.K & 127) || (((uintptr_t)p.as | (uintptr_t)p.ws) & 3) ? 3 : 4;
+    const int nb = p.K / 32;
+    Run c;
+    c.S = (nb + 7) / 8;
+    c.tail = nb & 7;
+    c.per = (nb & 3) || (((uintptr_t)p.as | (uintptr_t)p.ws) & 3) ? 3 : 4;
+    // the next tile's first slab: once this one's last has been read and the feed
+    // is at that tile
+    c.slab_at = c.S < 3 ? -1 : max((c.S - 1) / c.per * c.per, c.S - 3);
+    c.late = c.slab_at == c.S - 1;
+    Feed f;
+    f.sched.set(p, threadIdx.x & 63);
+    const long long Q = f.sched.items();
+    const int xcd = blockIdx.x & 7;
+    f.step = gridDim.x >> 3;
+    f.end = (int)(Q * (xcd + 1) / 8);
+    f.S = c.S;
     int q = (int)(Q * xcd / 8) + (int)(blockIdx.x >> 3);
-    if (q >= end) return;
-    Tile t;
-    find(q, t);
-    {
-        Fetch f;
-        f.set(p, t);
-        f.first_stages(t.valid, S);
-    }
-    for (int stored = 0;;) {
-        const bool more = q + step < end;
-        Tile next = t;
-        if (more) find(q + step, next);
+    if (q >= f.end) return;
+    f.q = q;
+    f.sched.find(q, f.t);
+    f.set(p);
+    Tile t = f.t;
+    if (c.S >= 3) f.slab(0);
+    f.early(p, 0);
+    f.rest(0);
+    f.early(p, kSlot);
+    f.rest(kSlot);
+    f.early(p, 2 * kSlot);
+    wait_vm<kCopies + kEarly>();
+    if (c.tail && c.S == 1) zeros(smem, 0, c.tail);
+    __syncthreads();
+    for (int slot = 0, stored = 0;;) {
         switch ((t.valid + 31) >> 5) {
-            case 1: stored = run_tile<F32, 1>(p, t, next, more, per, stored, smem); break;
-            case 2: stored = run_tile<F32, 2>(p, t, next, more, per, stored, smem); break;
-            case 3: stored = run_tile<F32, 3>(p, t, next, more, per, stored, smem); break;
-            default: stored = run_tile<F32, 4>(p, t, next, more, per, stored, smem); break;
+            case 1: stored = run_tile<F32, 1>(p, t, f, c, slot, stored, smem); break;
+            case 2: stored = run_tile<F32, 2>(p, t, f, c, slot, stored, smem); break;
+            case 3: stored = run_tile<F32, 3>(p, t, f, c, slot, stored, smem); break;
+            default: stored = run_tile<F32, 4>(p, t, f, c, slot, stored, smem); break;
         }
-        if (!more) break;
-        t = next;
-        q += step;
+        q += f.step;
+        if (q >= f.end) break;
+        if (c.S >= 3) t = f.t;
+        else f.sched.find(q, t);
     }
 }
 
