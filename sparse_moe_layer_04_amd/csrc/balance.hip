@@ -95,17 +95,17 @@ struct Token {
     }
 };
 
-// ---- first pass: a workgroup of four waves takes a chunk of p.chunk tokens,
-// each wave every fourth token of a piece.  Lane l holds experts l + 64 i.
-template <int NPL>
-__global__ __launch_bounds__(256) void balance_pieces_kernel(BalanceArgs p) {
-    __shared__ float sums[4][2][NPL * 64];
+// ---- first pass: a workgroup of W waves takes a chunk of p.chunk tokens, each
+// wave every W'th token of a piece.  Lane l holds experts l + 64 i.
+template <int NPL, int W>
+__global__ __launch_bounds__(64 * W) void balance_pieces_kernel(BalanceArgs p) {
+    __shared__ float sums[W][2][NPL * 64];
     __shared__ int hist[2][NPL * 64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int E = p.E, k = p.k;
     const int t0 = blockIdx.x * p.chunk, t1 = min(p.T, t0 + p.chunk);
     if (blockIdx.x == 0)
-        for (int s = threadIdx.x; s < p.S; s += 256) p.ticket[s] = 0;
+        for (int s = threadIdx.x; s < p.S; s += 64 * W) p.ticket[s] = 0;
     for (int tb = t0; tb < t1;) {
         const int s = sequence_of(p, tb, lane);
         if (s >= p.S) break;
@@ -114,16 +114,16 @@ __global__ __launch_bounds__(256) void balance_pieces_kernel(BalanceArgs p) {
             tb = max(te, tb + 1);            // with offsets in order)
             continue;
         }
-        for (int i = threadIdx.x; i < 2 * NPL * 64; i += 256) (&hist[0][0])[i] = 0;
+        for (int i = threadIdx.x; i < 2 * NPL * 64; i += 64 * W) (&hist[0][0])[i] = 0;
         __syncthreads();
         float m0[NPL], m1[NPL];
 #pragma unroll
         for (int i = 0; i < NPL; ++i) m0[i] = m1[i] = 0.0f;
         Token<NPL> next;
         next.load(p, min(tb + wave, te - 1), lane);
-        for (int t = tb + wave; t < te; t += 4) {
+        for (int t = tb + wave; t < te; t += W) {
             Token<NPL> a = next;
-            next.load(p, min(t + 4, te - 1), lane);
+            next.load(p, min(t + W, te - 1), lane);
             const int c = a.mod ? 1 : 0;
             const bool bad = a.bad(p);
             if (!a.mask || bad) {
@@ -152,9 +152,12 @@ __global__ __launch_bounds__(256) void balance_pieces_kernel(BalanceArgs p) {
         }
         __syncthreads();
         const size_t to = ((size_t)blockIdx.x + s) * p.C * E;
-        for (int x = threadIdx.x; x < p.C * E; x += 256) {
+        for (int x = threadIdx.x; x < p.C * E; x += 64 * W) {
             const int c = x >= E ? 1 : 0, e = x - c * E;
-            p.piece_sum[to + x] = (sums[0][c][e] + sums[1][c][e]) + (sums[2][c][e] + sums[3][c][e]);
+            float v = sums[0][c][e];
+#pragma unroll
+            for (int w = 1; w < W; ++w) v += sums[w][c][e];
+            p.piece_sum[to + x] = v;
             p.piece_num[to + x] = hist[c][e];
         }
         __syncthreads();
@@ -246,8 +249,13 @@ struct Group {
     int s = -2;                            // the sequence (none yet)
     int end = -1;                          // first token behind it
     float c0[NPL], c1[NPL];
-    float n0, n1;                          // tokens
+    float a0, a1;                          // d_loss / T_g * E / (k T_g)
 
+    // (0 for a group of no pairs, which no token is in)
+    __device__ __forceinline__ static float factor(const BalanceArgs& p, int g, double pairs) {
+        const double n = pairs / p.k;
+        return pairs > 0.0 ? (float)((double)p.d_loss[g] * p.E / (p.k * n * n)) : 0.0f;
+    }
     __device__ __forceinline__ void load(const BalanceArgs& p, int seq, int lane) {
         s = seq;
         if (seq < 0 || seq >= p.S) {
@@ -267,8 +275,8 @@ struct Group {
             sum0 += a;
             sum1 += b;
         }
-        n0 = (float)(wave_sum(sum0) / p.k);
-        n1 = (float)(wave_sum(sum1) / p.k);
+        a0 = factor(p, seq * p.C, wave_sum(sum0));
+        a1 = p.C == 2 ? factor(p, seq * p.C + 1, wave_sum(sum1)) : 0.0f;
     }
 };
 
@@ -298,11 +306,8 @@ __global__ __launch_bounds__(256) void balance_gradient_kernel(BalanceArgs p, in
         }
         sum = wave_sum_f32(sum);
         cs = wave_sum_f32(cs);
-        const float q = cs / sum;
-        const float n = second ? g.n1 : g.n0;
-        const float up = part ? p.d_loss[g.s * p.C + second] / n *
-                                    ((float)p.E / ((float)p.k * n)) / sum
-                              : 0.0f;
+        const float inv = 1.0f / sum, q = cs * inv;
+        const float up = (second ? g.a1 : g.a0) * inv;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
             const int x = lane + 64 * i;
@@ -316,10 +321,10 @@ __global__ __launch_bounds__(256) void balance_gradient_kernel(BalanceArgs p, in
 }
 
 // Tokens of a chunk: enough chunks for every CU, the pieces a small part of
-// what is read, and at most 2^18 chunks.  8192 tokens x 384 experts, loss and
-// gradient: 27.8 us with 32, 28.2 with 16, 31.7 with 64; 32767 x 330: 46 us with
-// 32, 49 with 16 and with 64.
-int chunk_of(int T) { return T <= 65536 ? 32 : T <= 1 << 24 ? 64 : 2 * (1 + (T >> 19)); }
+// what is read, and at most 2^18 chunks.  The loss, 8192 tokens x 384 experts:
+// 14.6 us with 32 (four waves a workgroup 16.5), 17.1 with 16, 16.4 with 64;
+// 32767 x 330: 24.3 us with 32, 22.6 with 64; 131072 x 384: 73 and 61.
+int chunk_of(int T) { return T <= 16384 ? 32 : T <= 1 << 24 ? 64 : 2 * (1 + (T >> 19)); }
 int slices_of(const BalanceArgs& p) { return (p.C * p.E + 63) / 64; }
 
 #define MOE_BY_EXPERTS(E, CALL)        \
@@ -355,8 +360,10 @@ hipError_t launch_balance_loss(const BalanceArgs& p, hipStream_t stream) {
     // (a workgroup with T = 0 too: it clears the tickets)
     const unsigned chunks = (unsigned)(((long long)p.T + p.chunk - 1) / p.chunk);
     const dim3 grid(chunks ? chunks : 1);
-#define MOE_PIECES(N) \
-    hipLaunchKernelGGL((balance_pieces_kernel<N>), grid, dim3(256), 0, stream, p)
+    // (eight waves a workgroup; four where their sums pass 64 KB of LDS)
+#define MOE_PIECES(N)                                                                       \
+    hipLaunchKernelGGL((balance_pieces_kernel<N, N <= 8 ? 8 : 4>), grid,                    \
+                       dim3(64 * (N <= 8 ? 8 : 4)), 0, stream, p)
     MOE_BY_EXPERTS(p.E, MOE_PIECES)
 #undef MOE_PIECES
     const unsigned x = (unsigned)(p.S < 32768 ? p.S : 32768);

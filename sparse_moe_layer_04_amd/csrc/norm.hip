@@ -307,9 +307,11 @@ int backward_parts(long long rows, const Shape& s) {
 
 hipError_t launch_add_rms_norm(const NormArgs& p, hipStream_t stream) {
     if (p.rows == 0) return hipSuccess;
-    // two chunks a lane where there are rows for every CU (8191 x 4096 bf16 24.4
-    // -> 21.8 us), one where a row's chain of waits is what counts
-    const Shape s = shape_of(p.d, p.rows < 1024 ? 1 : 2);
+    // Two loads in flight a lane: of x and the residual, or of two chunks of x
+    // (8192 x 4096 bf16: with a residual 54.6 us, with two chunks 58.4; without
+    // one 24.4 with one chunk, 21.8 with two).  One chunk where a row's chain of
+    // waits is what counts.
+    const Shape s = shape_of(p.d, p.rows < 1024 || p.res ? 1 : 2);
     const dim3 grid = grid_of(s.one ? (p.rows + 3) / 4 : p.rows);
     const int res = !p.res ? RES_NONE : p.res_f32 ? RES_F32 : RES_BF16;
     if (p.x_f32) {
