@@ -397,9 +397,9 @@ int moe_expert_ffn_fp8_block(const uint8_t* a8, const float* a_scale, const int3
  *   x [rows, d], residual [rows, d] or NULL, w [d]: each bf16 (MOE_IN_BF16) or
  *   fp32 (MOE_IN_F32); res_out [rows, d]; y [rows, d] bf16 or NULL; codes
  *   [rows, d] and scales [rows, ceil(d / 128)] fp32, or both NULL; y or codes
- *   is given.  eps >= 0 and finite.  d a multiple of 8 (with codes of 16), up
- *   to 16384; all 16-byte aligned but scales (4).  y, codes and scales overlap
- *   no input.
+ *   is given.  eps >= 0 and finite (a row of zeros with eps = 0 gives NaN).
+ *   d a multiple of 8 (with codes of 16), up to 16384; all 16-byte aligned but
+ *   scales (4).  y, codes and scales overlap no input.
  */
 int moe_add_rms_norm(const void* x, int x_dtype, const void* residual, int res_dtype,
                      const void* w, int w_dtype, long long rows, int d, double eps,
@@ -680,8 +680,8 @@ size_t moe_forward_workspace_size(const moe_cfg* cfg);
 size_t moe_workspace_size(const moe_cfg* cfg);
 
 /* Reads the device error-flag word (the MOE_FLAG_* bits that moe_route,
- * moe_permute, moe_route_backward, moe_forward and moe_forward_few OR into
- * *d_flags) into *out after all work queued on `stream` so far has completed.  Unlike every
+ * moe_permute, moe_route_backward, moe_balance_loss, moe_forward and
+ * moe_forward_few OR into *d_flags) into *out after all work queued on `stream` so far has completed.  Unlike every
  * other entry point it synchronises the host with the stream (a checking or
  * test call, not a per-step one).  d_flags is a device uint32; out a host
  * pointer.  MOE_ERR_NULL if either is NULL, MOE_ERR_HIP if the copy or the

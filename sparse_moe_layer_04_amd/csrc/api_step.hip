@@ -4,7 +4,6 @@
 #include <math.h>
 
 #include <algorithm>
-#include <new>
 #include <vector>
 
 #include "fp4.h"
@@ -234,7 +233,7 @@ int moe_grad_plan(const moe_grad_tensor* tensors, int count, void* host_plan, si
             if (x.lo < outs || (x.out && x.lo < grads)) return MOE_ERR_UNSUPPORTED;
             (x.out ? outs : grads) = std::max(x.out ? outs : grads, x.hi);
         }
-    } catch (const std::bad_alloc&) {
+    } catch (...) {                        // (no memory for the ranges)
         return MOE_ERR_WORKSPACE;
     }
     GradChunk* c = (GradChunk*)host_plan;

@@ -5,8 +5,16 @@
 // y to bf16, and to E4M3 codes with a power-of-two scale for each 128 values
 // (the rule of moe_quantize_fp8_block, on the fp32 y).  The sum of squares,
 // the root and s / root are held in 64 bits: no sum overflows or vanishes
-// (|s| up to the type's largest), and y comes out the same bits for any order
-// of the sum, so that codes and scales next to a border do too.
+// (|s| up to the type's largest), and n depends on the order of the sum only
+// where s / root lies within 2^-52 of a border of fp32 (one value in 2^28), so
+// that codes and scales next to a border do not either.
+//
+// Bound: HBM, each value read and written once, 9 bytes a value with a bf16
+// residual, bf16 and 8-bit output: 8192 x 4096 54.6 us, 5.6 TB/s (a large copy:
+// 6.0); without the residual and the codes, 8191 x 4096, 21.8 us (6.2, half of
+// it from the cache).  Loads behind a branch on the type, which the compiler
+// waits for one by one, took 93 us: types are template arguments.  Stores or
+// loads past the caches: none or slower.  Four rows of 2048: 2.7 us, a launch.
 #include <type_traits>
 
 #include "step.h"
@@ -132,8 +140,11 @@ __global__ __launch_bounds__(ONE ? 256 : 1024) void add_rms_norm_kernel(NormArgs
 // One pass over a row: the sums of s^2 and of g s together (64 bits, as is the
 // last line, whose terms cancel), the row held in registers.  A wave or a
 // workgroup takes rows t, t + stride, ... and keeps its columns' dw in
-// registers (fp32, at most a few dozen terms each); its sums go to a row of
-// `part`, which the second kernel adds up (64 bits), always in the same order.
+// registers (fp32); its sums go to a row of `part`, which the second kernel
+// adds up (64 bits), always in the same order.
+//
+// Bound: HBM, 14 bytes a value with fp32 gradients: 8192 x 4096 84 us + 4.5 for
+// the sums of dw, 5.3 TB/s over both.  The last line in 32 bits: the same time.
 template <bool SF32, bool GF32, int RES, int NC, bool ONE>
 __global__ __launch_bounds__(ONE ? 256 : 1024) void rms_norm_backward_kernel(NormBwdArgs p) {
     __shared__ double part[2][ONE ? 1 : 16][2];

@@ -58,6 +58,7 @@ WEIGHTS_FP8_BLOCK = 5
 # scaled block of the 8-bit operators, largest T of forward_few
 FP8_BLOCK = 128
 FEW_MAX_T = 64
+ERR_UNSUPPORTED = -3
 # workspace of the gradients' norm and clipping
 GRAD_WORKSPACE_BYTES = 16384
 IN_BF16 = 0
@@ -935,8 +936,10 @@ class GradClip:
         self.device = self.grads[0].device
         size = int(lib().moe_grad_plan_size(entries, len(entries)))
         host = torch.empty(size, dtype=torch.uint8)
-        _check(lib().moe_grad_plan(entries, len(entries), host.data_ptr() if size else None, size),
-               "moe_grad_plan")
+        st = lib().moe_grad_plan(entries, len(entries), host.data_ptr() if size else None, size)
+        if st == ERR_UNSUPPORTED:
+            raise MoeError("grads and out: a tensor overlaps another's out (or is listed twice)")
+        _check(st, "moe_grad_plan")
         self.plan = host.to(self.device)
         self.workspace = torch.empty(GRAD_WORKSPACE_BYTES, dtype=torch.uint8, device=self.device)
 

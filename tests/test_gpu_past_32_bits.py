@@ -1,0 +1,74 @@
+"""The operators around the layer and the MXFP4 ones on tensors of more than
+2^31 values: a block of rows repeated, whose last copy has to come out as the
+first."""
+import pytest
+import torch
+
+from sparse_moe_layer_04_amd import ops
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def free_memory():
+    yield
+    torch.cuda.empty_cache()
+
+
+def same_ends(t, rows):
+    assert torch.equal(t[:rows], t[-rows:]) and t.numel() > 2 ** 31
+
+
+def test_norm_and_backward():
+    x = torch.randn(1000, 4096, device="cuda").bfloat16().repeat(530, 1)
+    w = torch.randn(4096, device="cuda")
+    _, y, codes, scales = ops.add_rms_norm(x, w, fp8=True)
+    same_ends(y, 1000)
+    same_ends(codes, 1000)
+    assert torch.equal(scales[:1000], scales[-1000:])
+    del codes
+    dx, dw = ops.rms_norm_backward(x, w, y, dx_dtype=ops.OUT_BF16)
+    same_ends(dx, 1000)
+    one = ops.rms_norm_backward(x[:1000], w, y[:1000])[1].double() * 530
+    # sums of 1036 rows a part in fp32
+    assert ((dw.double() - one).abs() <= 1036 * 2.0 ** -24 *
+            (y[:1000].double().abs() * 530 * 6).sum(0)).all()
+
+
+def test_balance():
+    lg = torch.randn(10000, 384, device="cuda").repeat(600, 1)
+    ids = torch.rand(10000, 384, device="cuda").argsort(1)[:, :6].to(torch.int32).repeat(600, 1)
+    off = (torch.arange(601) * 10000).to(torch.int32).cuda()
+    loss, counts = ops.balance_loss(lg, ids, off)
+    assert (counts == counts[:1]).all()
+    assert ((loss / loss[0] - 1).abs() <= 64 * 2.0 ** -24).all()
+    d = ops.balance_loss_backward(lg, ids, counts, torch.ones_like(loss), off)
+    same_ends(d, 10000)
+    assert d[-10000:].any()
+
+
+def test_mxfp4():
+    a = torch.randn(1000, 4096, device="cuda").bfloat16().repeat(530, 1)
+    codes, scales = ops.quantize_mxfp4(a)
+    assert a.numel() > 2 ** 31
+    assert torch.equal(codes[:1000], codes[-1000:]) and torch.equal(scales[:1000], scales[-1000:])
+    assert codes[-1000:].any()
+    del a, codes
+    a4 = torch.randint(0, 256, (1000, 32), dtype=torch.uint8, device="cuda").repeat(1100, 1)
+    sa = torch.randint(120, 130, (1000, 2), dtype=torch.uint8, device="cuda").repeat(1100, 1)
+    w4 = torch.randint(0, 256, (1, 2048, 32), dtype=torch.uint8, device="cuda")
+    sw = torch.randint(120, 130, (1, 2048, 2), dtype=torch.uint8, device="cuda")
+    off = torch.tensor([0, 1100000], dtype=torch.int32, device="cuda")
+    out = ops.grouped_gemm_mxfp4(a4, sa, off, w4, sw, out_dtype=ops.OUT_F32)
+    same_ends(out, 1000)
+    assert out[-1000:].any()
+
+
+def test_clip():
+    n = 2 ** 31 + 4097
+    g = torch.full((n,), 0.5, device="cuda")
+    norm = ops.GradClip([g]).clip(1.0)
+    assert abs(float(norm) / (0.5 * n ** 0.5) - 1) <= 1e-6
+    want = 1.0 / n ** 0.5
+    for part in (g[:5], g[2 ** 31 - 3:2 ** 31 + 5], g[-5:]):
+        assert ((part.double() / want - 1).abs() <= 1e-6).all()
