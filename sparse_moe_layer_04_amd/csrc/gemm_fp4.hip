@@ -12,56 +12,76 @@
 // Tile: up to 128 rows x 256 weight rows, 8 waves of 64 x 64 or (rows of the
 // tile) x 32 outputs, 256 of K (128 bytes a row) a stage, four steps.  The
 // codes of both operands go to a ring of three LDS slots by copies that pass
-// no register, two stages ahead (a wave's copy covers 8 rows x 128 bytes; LDS
-// row r holds its 16-byte chunk c at c ^ ((r >> 1) & 7), so that the lanes of
-// an operand read spread over the banks).
+// no register, two and a half stages ahead (a wave's copy covers 8 rows x 128
+// bytes; LDS row r holds its 16-byte chunk c at c ^ ((r >> 1) & 7), so that the
+// lanes of an operand read spread over the banks).  Where it saves enough
+// rounds the tiles have up to 256 rows, 8 waves of up to 128 x 64, in a ring of
+// two slots, each refilled as soon as its last step has been read.
 //
 // Scales: a row's 8 bytes of a stage, but fetched 32 at a time: the 16 bytes of
 // one stage for each of 384 rows are 384 lines touched, as many as its codes
-// (384 groups x 128 rows x 4096 x 2048: 560 us; without any scales 448).  A
-// slab of 32 bytes a row from the word that holds the first one is four stages
-// (K / 32 and the scales' address multiples of 4) or three (any others, the
-// bytes shifted out of the words).  Its place in LDS is read into registers at
-// the slab's first stage and takes the next slab from then on.
+// (384 groups x 128 rows x 4096 x 2048 with an earlier order of the stores: 560
+// us fetched so, 448 without any scales, 492 now).  A slab of 32 bytes a row
+// from the word that holds the first one is four stages (K / 32 and the scales'
+// address multiples of 4) or three (any others, the bytes shifted out of the
+// words).  Its place in LDS is read into registers at the slab's first stage and
+// takes the next slab from then on.
+//
+// Bound and measured (us):
+//   64 groups, 192 rows in all, 2048 x 1024, bf16 out        15  the weights' 70 MB (10 at
+//     6.8 TB/s) and the start of the reads: one round, 8 stages
+//   384 uneven groups, 49152 rows, 4096 x 2048, fp32 out    465  HBM: weights, rows and
+//     outputs are 2.2 GB, what tiles fetch again from memory 0.3 GB: 5.35 TB/s
+//   8191 x 4064 x 2032, bf16 out                             49  copies into LDS and reads
+//     out of it beside the matrix cores: 2.8 PFLOP/s of the 8 that the instructions
+//     reach from registers
+//   8192 x 4096 x 2048, bf16 out                             45  the same, 3.0 PFLOP/s
 #include "fp4.h"
 #include "lds_ring.h"
 
 namespace moe {
 namespace {
 
-constexpr int BM = 128;                    // rows a tile, at most
 constexpr int BN = 256;                    // weight rows a tile
 constexpr int BK = 128;                    // bytes of a row a stage: 256 of K
 constexpr int kThreads = 512;
 constexpr int kSlotW = BN * BK;
-constexpr int kSlot = kSlotW + BM * BK;
-constexpr int kRing = 3 * kSlot;
-constexpr int kSlab = 32 * (BN + BM);      // scales: 32 bytes a row, W's first
-constexpr int kLds = kRing + kSlab;
-static_assert(kLds <= 160 * 1024 && kSlot % 128 == 0, "three slots of LDS");
+// tiles of up to 128 rows and three slots, or of up to 256 and two
+template <bool TALL>
+struct Ring {
+    static constexpr int BM = TALL ? 256 : 128;
+    static constexpr int kSlot = kSlotW + BM * BK, kSlots = TALL ? 2 : 3;
+    static constexpr int kSlabs = kSlots * kSlot;  // scales: 32 bytes a row, W's first
+    static constexpr int kBytes = kSlabs + 32 * (BN + BM);
+    static_assert(kSlot % 128 == 0, "the chunks' places within a row");
+};
+constexpr int kLds = Ring<false>::kBytes;
+static_assert(kLds <= 160 * 1024 && Ring<true>::kBytes <= kLds, "the LDS of a CU");
 
 struct Tile {
     int g, row0, valid, n0;                // n0: first weight row
 };
 
-// copies of codes a wave and stage: 4 of W, 2 of A; 3 of them are issued after
-// the middle of a stage, the others before the middle of the next
-constexpr int kEarly = 3, kCopies = 6;
-// Waves of a tile of `blocks` blocks of 32 rows: along the rows x along the
-// weight rows, each MI x NJ blocks of 32 x 32.  With NJ = 2 the two blocks of
-// weight rows hold every other one of 64, so that a lane has neighbouring
-// columns of the output.
-template <int MB>
+// Waves of a tile of MB blocks of 32 rows (tall tiles: 4, 6 or 8): along the rows
+// x along the weight rows, each MI x NJ blocks of 32 x 32.  With NJ = 2 the two
+// blocks of weight rows hold every other one of 64, so that a lane has
+// neighbouring columns of the output.
+template <int MB, bool TALL>
 struct Waves {
-    static constexpr int WM = MB == 4 || MB == 2 ? 2 : 1, WN = 8 / WM, MI = MB / WM, NJ = 8 / WN;
+    static constexpr int WM = TALL || MB == 4 || MB == 2 ? 2 : 1, WN = 8 / WM, MI = MB / WM;
+    static constexpr int NJ = 8 / WN;
     static constexpr int kStores = 16 * MI;   // of a wave, whatever the output's type
 };
-__device__ __forceinline__ bool in_pairs(int valid) { return ((valid - 1) >> 5) & 1; }
+template <bool TALL>
+__device__ __forceinline__ bool in_pairs(int valid) {
+    return TALL || ((valid - 1) >> 5) & 1;
+}
 
 // row tiles of a group of n rows, tiles of up to `blocks` blocks of 32 rows
 __device__ __forceinline__ int row_tiles(int n, int blocks) {
     const int c = (n + 31) >> 5;
-    return blocks == 1 ? c : blocks == 2 ? (c + 1) >> 1 : blocks == 3 ? (c + 2) / 3 : (c + 3) >> 2;
+    return blocks == 1 ? c : blocks == 2 ? (c + 1) >> 1 : blocks == 3 ? (c + 2) / 3
+           : blocks == 4 ? (c + 3) >> 2 : (c + 7) >> 3;
 }
 
 // Items are (group, band of kBand m-tiles, n-tile, m-tile), the 8 XCDs take
@@ -71,13 +91,14 @@ __device__ __forceinline__ int row_tiles(int n, int blocks) {
 // keeps in registers: lane l holds the items before run l of ceil(G / 64)
 // groups, and looks into the run that holds the item.
 constexpr int kBand = 8;
-constexpr int kTallest = BM / 32;
+constexpr int kUsual = 4, kTall = 8;
 static_assert(MOE_MAX_GROUPS <= 64 * 64, "one lane a run, one lane a group of a run");
 
 struct Schedule {
     const int32_t* offsets;
     int G, rows, NT, run, blocks;
     int mine, upto;                        // of this lane's run
+    bool tall;
 
     __device__ __forceinline__ int clamped(int v) const { return min(max(v, 0), rows); }
     __device__ __forceinline__ void set(const Fp4GemmArgs& p, int lane) {
@@ -86,25 +107,43 @@ struct Schedule {
         rows = p.rows;
         NT = (p.N + BN - 1) / BN;
         run = (G + 63) / 64;
-        // the row tiles of this lane's run, of up to 1 .. 4 blocks
-        int tiles[kTallest + 1] = {};
+        // the row tiles of this lane's run, of up to 1 .. 4 and 8 blocks
+        int tiles[kUsual + 1] = {}, talls = 0;
         for (int i = 0; i < run; ++i) {
             const int g = lane * run + i;
             if (g < G) {
                 const int n = max(clamped(offsets[g + 1]) - clamped(offsets[g]), 0);
 #pragma unroll
-                for (int b = 1; b <= kTallest; ++b) tiles[b] += row_tiles(n, b);
+                for (int b = 1; b <= kUsual; ++b) tiles[b] += row_tiles(n, b);
+                talls += row_tiles(n, kTall);
             }
         }
-        blocks = kTallest;
-        mine = NT * tiles[kTallest];
+        blocks = kUsual;
+        mine = NT * tiles[kUsual];
         upto = wave_scan(mine, lane);
+        const int cus = (int)gridDim.x, usual = items();
+        // Tall tiles where their rounds on the CUs, of up to twice the products
+        // and 3/4 of the bytes into LDS for each, are fewer than 2/3: 8191 x 4064
+        // x 2032 then takes 49 us instead of 57, 8192 x 4096 x 2048 45 instead of
+        // 50; 384 uneven groups of 128 rows on the average x 4096 x 2048, all in
+        // tall tiles, 505 instead of 465
+        tall = false;
+        if (usual > cus) {
+            const int sum = wave_scan(NT * talls, lane);
+            const int rounds = (usual + cus - 1) / cus;
+            if (3 * ((__builtin_amdgcn_readlane(sum, 63) + cus - 1) / cus) < 2 * rounds) {
+                tall = true;
+                blocks = kTall;
+                mine = NT * talls;
+                upto = sum;
+            }
+        }
         // few tiles: the lowest of which every one still has a CU of its own
-        if ((long long)rows * NT <= 96ll * gridDim.x && items() < (int)gridDim.x) {
+        if ((long long)rows * NT <= 96ll * cus && usual < cus) {
 #pragma unroll
-            for (int b = 1; b < kTallest; ++b) {
+            for (int b = 1; b < kUsual; ++b) {
                 const int sum = wave_scan(NT * tiles[b], lane);
-                if (__builtin_amdgcn_readlane(sum, 63) > (int)gridDim.x) continue;
+                if (__builtin_amdgcn_readlane(sum, 63) > cus) continue;
                 blocks = b;
                 mine = NT * tiles[b];
                 upto = sum;
@@ -142,8 +181,10 @@ struct Schedule {
 // and a half stages ahead of the products, across the ends of tiles.  Buffer
 // resources over a tile's rows (wave-uniform base, 32-bit offsets; rows past the
 // tile's or the matrix's end lie past them and fetch nothing).
+template <bool TALL>
 struct Feed {
-    Schedule sched;
+    using R = Ring<TALL>;
+    const Schedule& sched;
     Tile t;                                // the tile that is fetched
     int q, step, end;                      // its item, the next one's distance, their end
     int j, S;                              // its next stage, and its stages
@@ -157,7 +198,7 @@ struct Feed {
         const int wrows = min(p.N - t.n0, BN);
         wsrc = uniform_rsrc(p.w + wfirst * Kb, (size_t)wrows * Kb);
         asrc = uniform_rsrc(p.a + (size_t)t.row0 * Kb, (size_t)t.valid * Kb);
-        wo = (in_pairs(t.valid) ? 2 * (lr & 31) + (lr >> 5) : lr) * Kb + 16 * c;
+        wo = (in_pairs<TALL>(t.valid) ? 2 * (lr & 31) + (lr >> 5) : lr) * Kb + 16 * c;
         ao = lr * Kb + 16 * c;
         rows64 = 64 * Kb;
         set_scales(p, t);
@@ -168,10 +209,10 @@ struct Feed {
         const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
         const size_t wfirst = (size_t)t.g * p.N + t.n0;
         const int wrows = min(p.N - t.n0, BN);
-        // scales: wave w the slab's weight rows 32 w + (0 .. 31) and rows 32 (w &
-        // 3) + (0 .. 31) (half of them twice, so that every wave issues the same
-        // number of copies), 16 bytes a lane; whole words from the one that
-        // holds the first byte on
+        // scales: wave w the slab's weight rows 32 w + (0 .. 31) and rows 32 w +
+        // (0 .. 31) (of 128 rows modulo 4, half of them twice, so that every wave
+        // issues the same number of copies), 16 bytes a lane; whole words from
+        // the one that holds the first byte on
         auto scales = [&](const uint8_t* first, int rows, u32x4& src) {
             const int mis = (int)((uintptr_t)first & 3);
             src = uniform_rsrc(first - mis, ((size_t)rows * nb + mis + 3) & ~size_t(3));
@@ -179,52 +220,66 @@ struct Feed {
         };
         const int r = lane >> 1, piece = 16 * (lane & 1);
         sw = (((32 * wave + r) * nb + scales(p.ws + wfirst * nb, wrows, wscale)) & ~3) + piece;
-        sa = (((32 * (wave & 3) + r) * nb +
+        sa = (((32 * (TALL ? wave : wave & 3) + r) * nb +
                scales(p.as + (size_t)t.row0 * nb, t.valid, ascale)) & ~3) + piece;
     }
 
-    // The next stage's copies into the slot at LDS byte `at`, in two parts; the
-    // first goes on to the next tile where one ends (past the last with empty
-    // resources: every stage issues its copies).  What a tile's last stage holds
-    // past K is left out when it is multiplied.
-    __device__ __forceinline__ void early(const Fp4GemmArgs& p, int at) {
+    // The next stage's copies into the slot at LDS byte `at`, in parts 0 and 1
+    // (three copies each; tall tiles have a part 2 of two more); part 0 goes on
+    // to the next tile where one ends (past the last with empty resources: every
+    // stage issues its copies).  What a tile's last stage holds past K is left
+    // out when it is multiplied.
+    static constexpr int kCopies = TALL ? 8 : 6;
+    template <int PART>
+    __device__ __forceinline__ void copy(const Fp4GemmArgs& p, int at) {
         const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-        if (j == S) {
-            q += step;
-            j = 0;
-            if (q < end) {
-                sched.find(q, t);
-                set(p);
-            } else {
-                q = end;
-                wsrc[2] = asrc[2] = 0;
+        at += wave * 1024;
+        if constexpr (PART == 0) {
+            if (j == S) {
+                q += step;
+                j = 0;
+                if (q < end) {
+                    sched.find(q, t);
+                    set(p);
+                } else {
+                    q = end;
+                    wsrc[2] = asrc[2] = 0;
+                }
             }
+            copies16<3>(wsrc, wo, wsrc, wo + rows64, wsrc, wo + 2 * rows64, j * BK, at);
+        } else if constexpr (PART == 1) {
+            copies16<3>(wsrc, wo + 3 * rows64, asrc, ao, asrc, ao + rows64, j * BK,
+                        at + 3 * 64 * BK);
+            if (!TALL) ++j;
+        } else {
+            copies16<2>(asrc, ao + 2 * rows64, asrc, ao + 3 * rows64, asrc, 0, j * BK,
+                        at + 6 * 64 * BK);
+            ++j;
         }
-        copies16<3>(wsrc, wo, wsrc, wo + rows64, wsrc, wo + 2 * rows64, j * BK, at + wave * 1024);
     }
-    __device__ __forceinline__ void rest(int at) {
-        const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-        copies16<3>(wsrc, wo + 3 * rows64, asrc, ao, asrc, ao + rows64, j * BK,
-                    at + 3 * 64 * BK + wave * 1024);
-        ++j;
+    __device__ __forceinline__ void stage(const Fp4GemmArgs& p, int at) {
+        copy<0>(p, at);
+        copy<1>(p, at);
+        if constexpr (TALL) copy<2>(p, at);
     }
     // the slab whose first stage is j: two copies
     __device__ __forceinline__ void slab(int j) const {
         const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-        copy16(wscale, sw, j * 8, kRing + wave * 1024);
-        copy16(ascale, sa, j * 8, kRing + 32 * BN + (wave & 3) * 1024);
+        copy16(wscale, sw, j * 8, R::kSlabs + wave * 1024);
+        copy16(ascale, sa, j * 8, R::kSlabs + 32 * BN + (TALL ? wave : wave & 3) * 1024);
     }
 };
 
-// at most N and `stores` (0, 16, 32 or 48) of this wave's memory operations
-// outstanding
+// at most N and `stores` (0, 16, 32, 48 or 64) of this wave's memory operations
+// outstanding (the counter goes to 63)
 template <int N>
 __device__ __forceinline__ void wait_vm_stores(int stores) {
     switch (stores) {
         case 0: wait_vm<N>(); break;
         case 16: wait_vm<N + 16>(); break;
         case 32: wait_vm<N + 32>(); break;
-        default: wait_vm<N + 48>(); break;
+        case 48: wait_vm<N + 48>(); break;
+        default: wait_vm<63>(); break;
     }
 }
 
@@ -253,16 +308,21 @@ struct Run {
 // those and need not have ended when they have landed.  All stores are issued,
 // those past the rows or columns with offsets past the resource, so that their
 // number is known.  Returns the stores of this tile.
-template <bool F32, int MB>
-__device__ __forceinline__ int run_tile(const Fp4GemmArgs& p, const Tile& t, Feed& f, const Run& c,
-                                        int& slot, int stored, unsigned char* ring) {
+template <bool F32, int MB, bool TALL>
+__device__ __forceinline__ int run_tile(const Fp4GemmArgs& p, const Tile& t, Feed<TALL>& f,
+                                        const Run& c, int& slot, int stored,
+                                        unsigned char* ring) {
     // (the thread's place as a value of this variant's own: address terms
     // shared by the variants would be kept, or spilled, for all of them)
     int tid = threadIdx.x;
     asm volatile("" : "+v"(tid));
     const int lane = tid & 63, half = lane >> 5, l32 = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    constexpr int WN = Waves<MB>::WN, MI = Waves<MB>::MI, NJ = Waves<MB>::NJ, NT = MI * NJ;
+    using W = Waves<MB, TALL>;
+    constexpr int WN = W::WN, MI = W::MI, NJ = W::NJ, NT = MI * NJ;
+    constexpr int kSlot = Ring<TALL>::kSlot, kSlabs = Ring<TALL>::kSlabs;
+    // copies behind the next stage's at a turn
+    constexpr int kBehind = TALL ? 0 : Feed<TALL>::kCopies;
     const int wm = wave / WN, wn = wave % WN;
     const int N = p.N, nb = p.K / 32;
     const int S = c.S, tail = c.tail, per = c.per;
@@ -273,8 +333,8 @@ __device__ __forceinline__ int run_tile(const Fp4GemmArgs& p, const Tile& t, Fee
     const int rdw = wn * NJ * 32 * BK + rd0;
     const int rda = kSlotW + wm * MI * 32 * BK + rd0;
     auto wrow = [&](int n) { return wn * NJ * 32 + (NJ == 2 ? 2 * l32 + n : l32); };
-    const int rsw = kRing + wrow(0) * 32;
-    const int rsa = kRing + (BN + wm * MI * 32 + l32) * 32;
+    const int rsw = kSlabs + wrow(0) * 32;
+    const int rsa = kSlabs + (BN + wm * MI * 32 + l32) * 32;
     // bytes of a row's copied words before its first scale
     const uint32_t wbase = (uint32_t)((uintptr_t)p.ws + ((size_t)t.g * N + t.n0) * nb);
     const uint32_t abase = (uint32_t)((uintptr_t)p.as + (size_t)t.row0 * nb);
@@ -337,15 +397,15 @@ __device__ __forceinline__ int run_tile(const Fp4GemmArgs& p, const Tile& t, Fee
         wait_vm_stores<0>(stored);
         __syncthreads();
     }
-    // The middle of stage j: the next stage has landed (the copies behind it are
-    // those of the one after it, a slab that was sent off just before them, and
-    // the last tile's stores) and every wave has read stage j's operands, whose
-    // slot takes the next but two, and the slab if stage j is its first.
+    // The middle of stage j: the next stage has landed (the copies behind it are,
+    // of three slots, those of the one after it, a slab that was sent off just
+    // before them, and the last tile's stores) and every wave has read stage j's
+    // operands, whose slot is free, and the slab if stage j is its first.
     bool sent = false;
     auto turn = [&](int j, int next) {
-        if (j == 0) wait_vm_stores<kCopies>(stored);
-        else if (sent && j + 1 < S) wait_vm<kCopies + 2>();
-        else wait_vm<kCopies>();
+        if (j == 0) wait_vm_stores<kBehind>(stored);
+        else if (sent && j + 1 < S) wait_vm<kBehind + 2>();
+        else wait_vm<kBehind>();
         if (tail && (j == S - 2 || S == 1)) zeros(ring, next, tail);
         __syncthreads();
     };
@@ -363,16 +423,16 @@ __device__ __forceinline__ int run_tile(const Fp4GemmArgs& p, const Tile& t, Fee
     auto wide = [](const u32x4& v) {
         return v8i{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
     };
-    // the products of a step, copies behind the first
+    // the products of a step, copies behind the first ones
     auto multiply = [&](auto step, auto copy) {
         constexpr int q = decltype(step)::value, B = q & 1;
-        static_for<0, 4>([&](auto index) {
+        static_for<0, NT < 4 ? 4 : NT>([&](auto index) {
             constexpr int x = decltype(index)::value, i = x / NJ, n = x % NJ;
             if constexpr (x < NT)
                 acc[i][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
                     wide(ra[B][i]), wide(rw[B][n]), acc[i][n], 4, 4, q, (int)ca[i][0], q,
                     (int)cw[n][0]);
-            if constexpr (x == 0) copy();
+            copy(index);
         });
         // (the products stay here: the compiler would take them all to the end of
         // the stage, behind its branches)
@@ -391,17 +451,21 @@ __device__ __forceinline__ int run_tile(const Fp4GemmArgs& p, const Tile& t, Fee
     if (tail && S == 1) finite();
     int at = 0;                                     // the stage's place in its slab
     for (int j = 0; j < S; ++j) {
-        const int next = slot == 2 * kSlot ? 0 : slot + kSlot;
+        const int next = slot == (Ring<TALL>::kSlots - 1) * kSlot ? 0 : slot + kSlot;
         const int last = next == 2 * kSlot ? 0 : next + kSlot;
         read(slot, Q1());
-        multiply(Q0(), [&]() { f.rest(last); });
+        multiply(Q0(), [&](auto x) {
+            if constexpr (!TALL && x == 0) f.template copy<1>(p, last);
+        });
         read(slot, Q2());
-        multiply(Q1(), []() {});
+        multiply(Q1(), [](auto) {});
         read(slot, Q3());
-        multiply(Q2(), []() {});
+        multiply(Q2(), [](auto) {});
         turn(j, next);
         read(next, Q0());                           // (of the next tile: read again)
-        multiply(Q3(), [&]() { f.early(p, slot); });
+        multiply(Q3(), [&](auto x) {
+            if constexpr (x == 0 || (TALL && x < 3)) f.template copy<decltype(x)::value>(p, slot);
+        });
         const bool inner = at == 0 && j + per < S;
         sent = inner || j == c.slab_at;
         if (sent) f.slab(inner ? j + per : 0);
@@ -448,13 +512,13 @@ __device__ __forceinline__ int run_tile(const Fp4GemmArgs& p, const Tile& t, Fee
                 __builtin_amdgcn_raw_buffer_store_b16((uint16_t)bf16_pack2(x, x), out, at, 0, 0);
         }
     }
-    return Waves<MB>::kStores;
+    return W::kStores;
 }
 
-// Persistent grid, one workgroup a CU
-template <bool F32>
-__global__ __launch_bounds__(kThreads) void gemm_mxfp4_kernel(Fp4GemmArgs p) {
-    extern __shared__ __align__(16) unsigned char smem[];
+template <bool F32, bool TALL>
+__device__ __forceinline__ void run_tiles(const Fp4GemmArgs& p, const Schedule& sched,
+                                          unsigned char* smem) {
+    constexpr int kSlot = Ring<TALL>::kSlot, kAhead = TALL ? 2 : 3;   // stages
     const int nb = p.K / 32;
     Run c;
     c.S = (nb + 7) / 8;
@@ -462,42 +526,60 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_kernel(Fp4GemmArgs p) {
     c.per = (nb & 3) || (((uintptr_t)p.as | (uintptr_t)p.ws) & 3) ? 3 : 4;
     // the next tile's first slab: once this one's last has been read and the feed
     // is at that tile
-    c.slab_at = c.S < 3 ? -1 : max((c.S - 1) / c.per * c.per, c.S - 3);
+    c.slab_at = c.S < 3 ? -1 : max((c.S - 1) / c.per * c.per, c.S - kAhead);
     c.late = c.slab_at == c.S - 1;
-    Feed f;
-    f.sched.set(p, threadIdx.x & 63);
-    const long long Q = f.sched.items();
-    const int xcd = blockIdx.x & 7;
-    f.step = gridDim.x >> 3;
-    f.end = (int)(Q * (xcd + 1) / 8);
-    f.S = c.S;
+    const long long Q = sched.items();
+    const int xcd = blockIdx.x & 7, step = gridDim.x >> 3, end = (int)(Q * (xcd + 1) / 8);
     int q = (int)(Q * xcd / 8) + (int)(blockIdx.x >> 3);
-    if (q >= f.end) return;
+    if (q >= end) return;
+    Feed<TALL> f{sched};
+    f.step = step;
+    f.end = end;
+    f.S = c.S;
     f.q = q;
-    f.sched.find(q, f.t);
+    sched.find(q, f.t);
     f.set(p);
     Tile t = f.t;
     if (c.S >= 3) f.slab(0);
-    f.early(p, 0);
-    f.rest(0);
-    f.early(p, kSlot);
-    f.rest(kSlot);
-    f.early(p, 2 * kSlot);
-    wait_vm<kCopies + kEarly>();
+    f.stage(p, 0);
+    f.stage(p, kSlot);
+    if constexpr (TALL) {
+        wait_vm<Feed<TALL>::kCopies>();
+    } else {
+        f.template copy<0>(p, 2 * kSlot);
+        wait_vm<Feed<TALL>::kCopies + 3>();
+    }
     if (c.tail && c.S == 1) zeros(smem, 0, c.tail);
     __syncthreads();
     for (int slot = 0, stored = 0;;) {
-        switch ((t.valid + 31) >> 5) {
-            case 1: stored = run_tile<F32, 1>(p, t, f, c, slot, stored, smem); break;
-            case 2: stored = run_tile<F32, 2>(p, t, f, c, slot, stored, smem); break;
-            case 3: stored = run_tile<F32, 3>(p, t, f, c, slot, stored, smem); break;
-            default: stored = run_tile<F32, 4>(p, t, f, c, slot, stored, smem); break;
+        const int blocks = (t.valid + 31) >> 5;
+        if constexpr (TALL) {
+            if (blocks <= 4) stored = run_tile<F32, 4, true>(p, t, f, c, slot, stored, smem);
+            else if (blocks <= 6) stored = run_tile<F32, 6, true>(p, t, f, c, slot, stored, smem);
+            else stored = run_tile<F32, 8, true>(p, t, f, c, slot, stored, smem);
+        } else {
+            switch (blocks) {
+                case 1: stored = run_tile<F32, 1, false>(p, t, f, c, slot, stored, smem); break;
+                case 2: stored = run_tile<F32, 2, false>(p, t, f, c, slot, stored, smem); break;
+                case 3: stored = run_tile<F32, 3, false>(p, t, f, c, slot, stored, smem); break;
+                default: stored = run_tile<F32, 4, false>(p, t, f, c, slot, stored, smem); break;
+            }
         }
-        q += f.step;
-        if (q >= f.end) break;
+        q += step;
+        if (q >= end) break;
         if (c.S >= 3) t = f.t;
-        else f.sched.find(q, t);
+        else sched.find(q, t);
     }
+}
+
+// Persistent grid, one workgroup a CU
+template <bool F32>
+__global__ __launch_bounds__(kThreads) void gemm_mxfp4_kernel(Fp4GemmArgs p) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    Schedule sched;
+    sched.set(p, threadIdx.x & 63);
+    if (sched.tall) run_tiles<F32, true>(p, sched, smem);
+    else run_tiles<F32, false>(p, sched, smem);
 }
 
 template <bool F32>

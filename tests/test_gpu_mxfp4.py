@@ -158,8 +158,24 @@ def test_rows(dt, rows):
 def test_several_tiles_a_workgroup(dt, K):
     """More tiles than CUs, of every height, over every count of stages modulo
     the ring's slots and a slab's stages, with short last stages and without."""
-    args = [v.cuda() for v in make(40, 12000, K, 1552)]
+    check_on_gpu([v.cuda() for v in make(40, 12000, K, 1552)], dt)
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("K", [32, 64, 224, 256, 288, 480, 512, 544, 736, 768, 800, 1024, 1056, 1280,
+                               1312, 2272, 2304, 2336])
+def test_several_tall_tiles_a_workgroup(dt, K):
+    """Groups that fill tiles of 256 rows (and a few of other heights), more of
+    them than CUs, over the same counts of stages."""
+    sizes = torch.tensor([256] * 35 + [1, 255, 33, 100, 129, 0, 161, 193, 225] + [256] * 35)
+    a4, sa, off, w4, sw = make(79, int(sizes.sum()), K, 1552)
+    off[1:] = sizes.cumsum(0)
+    check_on_gpu([v.cuda() for v in (a4, sa, off, w4, sw)], dt)
+
+
+def check_on_gpu(args, dt):
     a4, sa, off, w4, sw = args
+    K = 2 * a4.shape[1]
     out = ops.grouped_gemm_mxfp4(*args, out_dtype=ops.OUT_F32 if dt == F32 else ops.OUT_BF16)
     v = VALUES.cuda()
 
@@ -167,7 +183,7 @@ def test_several_tiles_a_workgroup(dt, K):
         c = torch.stack((c & 15, c >> 4), -1).view(c.shape[0], -1)
         return v[c.long()] * torch.exp2(s.to(D) - 127).repeat_interleave(32, 1)
     a, o = of(a4, sa), off.tolist()
-    for g in range(40):
+    for g in range(w4.shape[0]):
         w, r = of(w4[g], sw[g]), a[o[g]:o[g + 1]]
         want, mag = r @ w.t(), r.abs() @ w.abs().t()
         tol = K * 2.0 ** -24 * mag + (want.abs() * 2.0 ** -8 if dt == BF16 else 0)
