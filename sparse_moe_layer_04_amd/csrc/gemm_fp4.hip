@@ -30,8 +30,8 @@
 // Bound and measured (us):
 //   64 groups, 192 rows in all, 2048 x 1024, bf16 out        15  the weights' 70 MB (10 at
 //     6.8 TB/s) and the start of the reads: one round, 8 stages
-//   384 uneven groups, 49152 rows, 4096 x 2048, fp32 out    465  HBM: weights, rows and
-//     outputs are 2.2 GB, what tiles fetch again from memory 0.3 GB: 5.35 TB/s
+//   384 uneven groups, 49152 rows, 4096 x 2048, fp32 out    455  HBM: weights, rows and
+//     outputs are 2.2 GB, what tiles fetch again from memory 0.3 GB: 5.5 TB/s
 //   8191 x 4064 x 2032, bf16 out                             49  copies into LDS and reads
 //     out of it beside the matrix cores: 2.8 PFLOP/s of the 8 that the instructions
 //     reach from registers
@@ -308,7 +308,7 @@ struct Run {
 // those and need not have ended when they have landed.  All stores are issued,
 // those past the rows or columns with offsets past the resource, so that their
 // number is known.  Returns the stores of this tile.
-template <bool F32, int MB, bool TALL>
+template <bool F32, bool PAST, int MB, bool TALL>
 __device__ __forceinline__ int run_tile(const Fp4GemmArgs& p, const Tile& t, Feed<TALL>& f,
                                         const Run& c, int& slot, int stored,
                                         unsigned char* ring) {
@@ -493,6 +493,7 @@ __device__ __forceinline__ int run_tile(const Fp4GemmArgs& p, const Tile& t, Fee
     const auto out = __builtin_amdgcn_make_buffer_rsrc(
         (void*)(uintptr_t)first, 0, __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000);
     const int col = wrow(0);
+    constexpr int kAux = PAST ? 2 : 0;              // (2: nontemporal)
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
 #pragma unroll
@@ -503,19 +504,19 @@ __device__ __forceinline__ int run_tile(const Fp4GemmArgs& p, const Tile& t, Fee
             const float x = acc[i][0][e], y = acc[i][NJ - 1][e];
             if constexpr (F32 && NJ == 2)
                 __builtin_amdgcn_raw_buffer_store_b64(
-                    u32x2{__float_as_uint(x), __float_as_uint(y)}, out, at, 0, 0);
+                    u32x2{__float_as_uint(x), __float_as_uint(y)}, out, at, 0, kAux);
             else if constexpr (F32)
-                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), out, at, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), out, at, 0, kAux);
             else if constexpr (NJ == 2)
-                __builtin_amdgcn_raw_buffer_store_b32(bf16_pack2(x, y), out, at, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b32(bf16_pack2(x, y), out, at, 0, kAux);
             else
-                __builtin_amdgcn_raw_buffer_store_b16((uint16_t)bf16_pack2(x, x), out, at, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b16((uint16_t)bf16_pack2(x, x), out, at, 0, kAux);
         }
     }
     return W::kStores;
 }
 
-template <bool F32, bool TALL>
+template <bool F32, bool PAST, bool TALL>
 __device__ __forceinline__ void run_tiles(const Fp4GemmArgs& p, const Schedule& sched,
                                           unsigned char* smem) {
     constexpr int kSlot = Ring<TALL>::kSlot, kAhead = TALL ? 2 : 3;   // stages
@@ -553,16 +554,19 @@ __device__ __forceinline__ void run_tiles(const Fp4GemmArgs& p, const Schedule& 
     __syncthreads();
     for (int slot = 0, stored = 0;;) {
         const int blocks = (t.valid + 31) >> 5;
+        auto tile = [&](auto mb) {
+            stored = run_tile<F32, PAST, decltype(mb)::value, TALL>(p, t, f, c, slot, stored, smem);
+        };
         if constexpr (TALL) {
-            if (blocks <= 4) stored = run_tile<F32, 4, true>(p, t, f, c, slot, stored, smem);
-            else if (blocks <= 6) stored = run_tile<F32, 6, true>(p, t, f, c, slot, stored, smem);
-            else stored = run_tile<F32, 8, true>(p, t, f, c, slot, stored, smem);
+            if (blocks <= 4) tile(std::integral_constant<int, 4>());
+            else if (blocks <= 6) tile(std::integral_constant<int, 6>());
+            else tile(std::integral_constant<int, 8>());
         } else {
             switch (blocks) {
-                case 1: stored = run_tile<F32, 1, false>(p, t, f, c, slot, stored, smem); break;
-                case 2: stored = run_tile<F32, 2, false>(p, t, f, c, slot, stored, smem); break;
-                case 3: stored = run_tile<F32, 3, false>(p, t, f, c, slot, stored, smem); break;
-                default: stored = run_tile<F32, 4, false>(p, t, f, c, slot, stored, smem); break;
+                case 1: tile(std::integral_constant<int, 1>()); break;
+                case 2: tile(std::integral_constant<int, 2>()); break;
+                case 3: tile(std::integral_constant<int, 3>()); break;
+                default: tile(std::integral_constant<int, 4>()); break;
             }
         }
         q += step;
@@ -573,28 +577,37 @@ __device__ __forceinline__ void run_tiles(const Fp4GemmArgs& p, const Schedule& 
 }
 
 // Persistent grid, one workgroup a CU
-template <bool F32>
+template <bool F32, bool PAST>
 __global__ __launch_bounds__(kThreads) void gemm_mxfp4_kernel(Fp4GemmArgs p) {
     extern __shared__ __align__(16) unsigned char smem[];
     Schedule sched;
     sched.set(p, threadIdx.x & 63);
-    if (sched.tall) run_tiles<F32, true>(p, sched, smem);
-    else run_tiles<F32, false>(p, sched, smem);
+    if (sched.tall) run_tiles<F32, PAST, true>(p, sched, smem);
+    else run_tiles<F32, PAST, false>(p, sched, smem);
 }
 
-template <bool F32>
+// Outputs above this are stored past the caches (nontemporal), which the operands
+// then have for themselves: with a kernel behind that reads them (quantise) 384
+// groups x 128 rows x 4096 x 2048 490 -> 484 us with bf16 outputs (201 MB), 548
+// -> 532 fp32 (403), 32768 x 1024 x 4096 fp32 (537) 285 -> 260; but 65.1 -> 72.6
+// for 8192 x 1024 x 4096 (134), 63.8 -> 65.2 for 64 groups of 24576 rows x 2048 x
+// 1024 bf16 (50), where it finds them in the 256 MB of cache otherwise, though
+// the product alone took 60 -> 46 us in 64 groups of 16384 rows x 1024 x 2048.
+constexpr size_t kKept = size_t(160) << 20;
+
+template <bool F32, bool PAST>
 hipError_t launch(const Fp4GemmArgs& g, hipStream_t stream) {
     static DeviceSetup setup;
     long long grid = 0, unused = 0;
     const hipError_t err =
         device_setup(setup, grid, unused, [](int, long long& gr, long long&) {
             gr = (device_cu_count() + 7) & ~7;
-            return hipFuncSetAttribute((const void*)gemm_mxfp4_kernel<F32>,
+            return hipFuncSetAttribute((const void*)gemm_mxfp4_kernel<F32, PAST>,
                                        hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
         });
     if (err != hipSuccess) return err;
-    hipLaunchKernelGGL((gemm_mxfp4_kernel<F32>), dim3((unsigned)grid), dim3(kThreads), kLds, stream,
-                       g);
+    hipLaunchKernelGGL((gemm_mxfp4_kernel<F32, PAST>), dim3((unsigned)grid), dim3(kThreads), kLds,
+                       stream, g);
     return hipGetLastError();
 }
 
@@ -602,7 +615,9 @@ hipError_t launch(const Fp4GemmArgs& g, hipStream_t stream) {
 
 hipError_t launch_grouped_gemm_mxfp4(bool f32, const Fp4GemmArgs& g, hipStream_t stream) {
     if (g.K < 32 || g.K % 32 || g.N < 16 || g.N % 16 || g.G < 1) return hipErrorInvalidValue;
-    return f32 ? launch<true>(g, stream) : launch<false>(g, stream);
+    const bool past = (size_t)g.rows * g.N * (f32 ? 4 : 2) > kKept;
+    return f32 ? past ? launch<true, true>(g, stream) : launch<true, false>(g, stream)
+               : past ? launch<false, true>(g, stream) : launch<false, false>(g, stream);
 }
 
 }  // namespace moe

@@ -173,6 +173,28 @@ def test_several_tall_tiles_a_workgroup(dt, K):
     check_on_gpu([v.cuda() for v in (a4, sa, off, w4, sw)], dt)
 
 
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("G", [1, 24])
+def test_outputs_beyond_the_caches(dt, G):
+    """Outputs of more than 160 MiB (another way of storing them) against the
+    same product in four parts, whose outputs are below that: the same bits, and
+    nothing outside the groups' rows and the columns."""
+    rows, K, N = (24000 if dt == F32 else 48000) + 7, 96, 1936
+    a4, sa, off, w4, sw = (v.cuda() for v in make(G, rows, K, N))
+    off = off - 3 if G > 1 else off                    # three rows behind the last group
+    od = ops.OUT_F32 if dt == F32 else ops.OUT_BF16
+    space = torch.full((rows + 2, N), -77.0, dtype=dt, device="cuda")
+    assert space.numel() * space.element_size() > 170 << 20
+    ops.grouped_gemm_mxfp4(a4, sa, off, w4, sw, out_dtype=od, out=space[1:-1])
+    parts = torch.full((rows, N), -77.0, dtype=dt, device="cuda")
+    for i in range(4):
+        lo, hi = rows * i // 4, rows * (i + 1) // 4
+        ops.grouped_gemm_mxfp4(a4[lo:hi].clone(), sa[lo:hi].clone(), (off - lo).clamp(0, hi - lo), w4,
+                               sw, out_dtype=od, out=parts[lo:hi])
+    assert torch.equal(space[1:-1], parts)
+    assert (space[0] == -77.0).all() and (space[-1] == -77.0).all()
+
+
 def check_on_gpu(args, dt):
     a4, sa, off, w4, sw = args
     K = 2 * a4.shape[1]
