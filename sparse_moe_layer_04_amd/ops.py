@@ -929,10 +929,16 @@ class GradClip:
         entries = (MoeGradTensor * len(self.grads))()
         dev = _device(self.grads[0], "grads[0]")
         for i, (g, o) in enumerate(zip(self.grads, self.out)):
-            dt = _in_dtype(g, f"grads[{i}]")
-            _on(g, dev, g.dtype, f"grads[{i}]", g.shape)
-            _on(o, dev, g.dtype, f"out[{i}]", g.shape)
-            entries[i] = MoeGradTensor(_ptr(g) or None, _ptr(o) or None, g.numel(), dt)
+            # (names are made for what fails: there may be thousands of tensors)
+            dt = None if g is None else _IN_TYPES.get(g.dtype)
+            if dt is None or g.get_device() != dev or not g.is_contiguous():
+                _in_dtype(g, f"grads[{i}]")
+                _on(g, dev, g.dtype, f"grads[{i}]", g.shape)
+            at = to = g.data_ptr()
+            if o is not g:
+                _on(o, dev, g.dtype, f"out[{i}]", g.shape)
+                to = o.data_ptr()
+            entries[i] = MoeGradTensor(at or None, to or None, g.numel(), dt)
         self.device = self.grads[0].device
         size = int(lib().moe_grad_plan_size(entries, len(entries)))
         host = torch.empty(size, dtype=torch.uint8)
