@@ -18,8 +18,11 @@
 // 201 (what it leaves in the cache is then lost).
 //
 // Bound: HBM, 12 bytes an fp32 value (the second read is real where the
-// gradients pass the cache's 256 MB): 409 M values 820 us, 6.0 TB/s, the rate
-// of a large copy; 40 M 75 us (6.4).
+// gradients pass the cache's 256 MB): 409 M values 815 us, 6.0 TB/s, the rate
+// of a large copy; 100 M 181 us; 40 M 79 (6.1).  400 tensors of 3 M values in
+// all 11.6 us, two launches of 3 and 6 and the host's call; with loops over a
+// short chunk's pieces and the norm added before the first values were asked
+// for 14.0.
 #include "step.h"
 
 namespace moe {
@@ -60,27 +63,43 @@ __device__ __forceinline__ double square_sum(const u32x4& w, bool f32) {
 
 constexpr int kU = kGradChunk / 4 / kT;    // 16-byte pieces a thread, of an fp32 chunk
 
-// A whole chunk's values on their way (pieces threadIdx.x + 256 u; of a short
-// chunk nothing).  ONCE: they are not read again soon.
+// A chunk's values on their way: pieces threadIdx.x + 256 u, the last one again
+// beyond it, and of the values behind the pieces one a thread.  (In a loop over
+// the pieces of short chunks each load would wait for the one before.)
+// ONCE: they are not read again soon.
 template <bool ONCE>
 struct Load {
     GradChunk c;
     u32x4 w[kU];
-    int pieces;                            // whole ones of 16 bytes
+    uint32_t value;                        // the one behind the pieces
+    int pieces, rest;                      // whole ones of 16 bytes; the value's place
 
     __device__ __forceinline__ void issue(const GradChunk& chunk) {
         c = chunk;
         pieces = c.n / (c.f32 ? 4 : 8);
-        if (c.n == kGradChunk) {
-            const u32x4* g = (const u32x4*)c.grad + threadIdx.x;
+        const int inside = pieces * (c.f32 ? 4 : 8);
+        rest = inside + (int)threadIdx.x;
+        const u32x4* g = (const u32x4*)c.grad;
+        auto load = [&](int u) {
+            const u32x4* at = g + min(u * kT + (int)threadIdx.x, pieces - 1);
+            w[u] = ONCE ? __builtin_nontemporal_load(at) : *at;
+        };
+        if (pieces > 0)
 #pragma unroll
-            for (int u = 0; u < kU / 2; ++u)
-                w[u] = ONCE ? __builtin_nontemporal_load(g + u * kT) : g[u * kT];
-            if (c.f32)
+            for (int u = 0; u < kU / 2; ++u) load(u);
+        if (pieces > kU / 2 * kT)
 #pragma unroll
-                for (int u = kU / 2; u < kU; ++u)
-                    w[u] = ONCE ? __builtin_nontemporal_load(g + u * kT) : g[u * kT];
-        }
+            for (int u = kU / 2; u < kU; ++u) load(u);
+        if (inside < c.n && rest < c.n)
+            value = c.f32 ? ((const uint32_t*)c.grad)[rest]
+                          : (uint32_t)((const uint16_t*)c.grad)[rest] << 16;
+    }
+    // f(u, place) for this thread's pieces
+    template <class F>
+    __device__ __forceinline__ void each(const F& f) const {
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+            if (u * kT + (int)threadIdx.x < pieces) f(u, u * kT + (int)threadIdx.x);
     }
 };
 
@@ -99,23 +118,11 @@ __global__ __launch_bounds__(kT) void grad_square_kernel(const GradChunk* __rest
             next.issue(after);
             after = plan[at + gridDim.x < chunks ? at + gridDim.x : at];
         }
-        if (l.c.n == kGradChunk) {
-            if (l.c.f32) {
-#pragma unroll
-                for (int u = 0; u < kU; ++u) sum += square_sum(l.w[u], true);
-            } else {
-#pragma unroll
-                for (int u = 0; u < kU / 2; ++u) sum += square_sum(l.w[u], false);
-            }
-        } else {
-            const u32x4* g = (const u32x4*)l.c.grad;
-            for (int i = threadIdx.x; i < l.pieces; i += kT) sum += square_sum(g[i], l.c.f32);
-            const int rest = l.pieces * (l.c.f32 ? 4 : 8) + (int)threadIdx.x;
-            if (rest < l.c.n) {
-                const double v = l.c.f32 ? ((const float*)l.c.grad)[rest]
-                                         : bf16_to_f32(((const uint16_t*)l.c.grad)[rest]);
-                sum = __builtin_fma(v, v, sum);
-            }
+        if (l.c.f32) l.each([&](int u, int) { sum += square_sum(l.w[u], true); });
+        else l.each([&](int u, int) { sum += square_sum(l.w[u], false); });
+        if (l.rest < l.c.n) {
+            const double v = __uint_as_float(l.value);
+            sum = __builtin_fma(v, v, sum);
         }
     }
     sum = group_sum(sum);
@@ -124,8 +131,14 @@ __global__ __launch_bounds__(kT) void grad_square_kernel(const GradChunk* __rest
 
 // the norm from the partial sums, in every thread
 __device__ __forceinline__ double norm_of(const double* part, int parts) {
-    double v = 0.0;
-    for (int i = threadIdx.x; i < parts; i += kT) v += part[i];
+    constexpr int kN = kGradParts / kT;
+    double p[kN], v = 0.0;
+    if (parts > 0)
+#pragma unroll
+        for (int i = 0; i < kN; ++i) p[i] = part[min(i * kT + (int)threadIdx.x, parts - 1)];
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+        if (i * kT + (int)threadIdx.x < parts) v += p[i];
     return __builtin_sqrt(group_sum(v));
 }
 
@@ -151,17 +164,20 @@ __global__ __launch_bounds__(kT) void grad_scale_kernel(const GradChunk* __restr
                                                         long long chunks, double max_norm,
                                                         const double* __restrict__ part, int parts,
                                                         float* __restrict__ norm) {
+    // (the first chunk's values are on their way while the sums are added)
+    long long at = chunks - 1 - blockIdx.x;
+    auto plan_at = [&](long long i) { return plan[i >= 0 ? i : 0]; };
+    Load<true> next;
+    GradChunk after;
+    if (chunks > 0) {
+        next.issue(plan_at(at));
+        after = plan_at(at - gridDim.x);
+    }
     const double total = norm_of(part, parts);
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)total;
     const bool clip = total > max_norm && total < __builtin_inf();
     const double f = clip ? max_norm / total : 1.0;
-    if (chunks == 0) return;
     // (in place and within the norm there is nothing to write)
-    long long at = chunks - 1 - blockIdx.x;
-    auto plan_at = [&](long long i) { return plan[i >= 0 ? i : 0]; };
-    Load<true> next;
-    next.issue(plan_at(at));
-    GradChunk after = plan_at(at - gridDim.x);
     while (at >= 0) {
         const Load<true> l = next;
         at -= gridDim.x;
@@ -171,33 +187,18 @@ __global__ __launch_bounds__(kT) void grad_scale_kernel(const GradChunk* __restr
         }
         if (!clip && l.c.out == l.c.grad) continue;
         u32x4* o = (u32x4*)l.c.out;
-        if (l.c.n == kGradChunk) {
-            if (l.c.f32) {
-#pragma unroll
-                for (int u = 0; u < kU; ++u)
-                    __builtin_nontemporal_store(clip ? scaled16(l.w[u], true, f) : l.w[u],
-                                                o + u * kT + threadIdx.x);
-            } else {
-#pragma unroll
-                for (int u = 0; u < kU / 2; ++u)
-                    __builtin_nontemporal_store(clip ? scaled16(l.w[u], false, f) : l.w[u],
-                                                o + u * kT + threadIdx.x);
-            }
-        } else {
-            const u32x4* g = (const u32x4*)l.c.grad;
-            for (int i = threadIdx.x; i < l.pieces; i += kT)
-                o[i] = clip ? scaled16(g[i], l.c.f32, f) : g[i];
-            const int rest = l.pieces * (l.c.f32 ? 4 : 8) + (int)threadIdx.x;
-            if (rest < l.c.n) {
-                if (l.c.f32) {
-                    const float v = ((const float*)l.c.grad)[rest];
-                    ((float*)l.c.out)[rest] = clip ? scaled(v, f) : v;
-                } else {
-                    const uint16_t v = ((const uint16_t*)l.c.grad)[rest];
-                    ((uint16_t*)l.c.out)[rest] =
-                        clip ? (uint16_t)bf16_pack2(scaled(bf16_to_f32(v), f), 0.0f) : v;
-                }
-            }
+        auto store = [&](bool f32) {
+            l.each([&](int u, int i) {
+                __builtin_nontemporal_store(clip ? scaled16(l.w[u], f32, f) : l.w[u], o + i);
+            });
+        };
+        if (l.c.f32) store(true);
+        else store(false);
+        if (l.rest < l.c.n) {
+            const float v = clip ? scaled(__uint_as_float(l.value), f) : __uint_as_float(l.value);
+            if (l.c.f32) ((float*)l.c.out)[l.rest] = v;
+            else ((uint16_t*)l.c.out)[l.rest] =
+                (uint16_t)(clip ? bf16_pack2(v, 0.0f) : l.value >> 16);
         }
     }
 }
@@ -213,7 +214,8 @@ hipError_t launch_grad_norm(const GradChunk* plan, long long chunks, double* par
                             hipStream_t stream) {
     const int parts = parts_of(chunks);
     if (parts > 0)
-        hipLaunchKernelGGL(grad_square_kernel, dim3(parts), dim3(kT), 0, stream, plan, chunks, part);
+        hipLaunchKernelGGL(grad_square_kernel, dim3(parts), dim3(kT), 0, stream, plan, chunks,
+                           part);
     hipLaunchKernelGGL(grad_norm_kernel, dim3(1), dim3(kT), 0, stream, part, parts, norm);
     return hipGetLastError();
 }
@@ -222,9 +224,10 @@ hipError_t launch_clip_grad_norm(const GradChunk* plan, long long chunks, double
                                  double* part, float* norm, hipStream_t stream) {
     const int parts = parts_of(chunks);
     if (parts > 0)
-        hipLaunchKernelGGL(grad_square_kernel, dim3(parts), dim3(kT), 0, stream, plan, chunks, part);
-    hipLaunchKernelGGL(grad_scale_kernel, dim3(parts > 0 ? scalers_of(chunks) : 1), dim3(kT), 0, stream, plan,
-                       chunks, max_norm, part, parts, norm);
+        hipLaunchKernelGGL(grad_square_kernel, dim3(parts), dim3(kT), 0, stream, plan, chunks,
+                           part);
+    hipLaunchKernelGGL(grad_scale_kernel, dim3(parts > 0 ? scalers_of(chunks) : 1), dim3(kT), 0,
+                       stream, plan, chunks, max_norm, part, parts, norm);
     return hipGetLastError();
 }
 
