@@ -45,7 +45,7 @@ __device__ __forceinline__ int offset_at(const BalanceArgs& p, int i) {
 // there are more).
 __device__ __forceinline__ int sequence_of(const BalanceArgs& p, int t, int lane) {
     if (!p.offsets) return 0;
-    if (t < offset_at(p, 0)) return -1;
+    const int first = offset_at(p, 0);     // (looked at last: its load with the others')
     int lo = 0, n = p.S;                   // the answer is in [lo, lo + n]
     while (n > 64) {
         const int mid = n >> 1;
@@ -57,7 +57,8 @@ __device__ __forceinline__ int sequence_of(const BalanceArgs& p, int t, int lane
         }
     }
     const bool before = lane < n && offset_at(p, lo + 1 + min(lane, n - 1)) <= t;
-    return lo + __popcll(__builtin_amdgcn_ballot_w64(before));
+    const int s = lo + __popcll(__builtin_amdgcn_ballot_w64(before));
+    return t < first ? -1 : s;
 }
 
 // e = exp(-x) and S(x) = 1 / (1 + e), within 4 steps of the router's scores
@@ -252,9 +253,10 @@ struct Group {
     float a0, a1;                          // d_loss / T_g * E / (k T_g)
 
     // (0 for a group of no pairs, which no token is in)
-    __device__ __forceinline__ static float factor(const BalanceArgs& p, int g, double pairs) {
+    __device__ __forceinline__ static float factor(const BalanceArgs& p, float d_loss,
+                                                   double pairs) {
         const double n = pairs / p.k;
-        return pairs > 0.0 ? (float)((double)p.d_loss[g] * p.E / (p.k * n * n)) : 0.0f;
+        return pairs > 0.0 ? (float)((double)d_loss * p.E / (p.k * n * n)) : 0.0f;
     }
     __device__ __forceinline__ void load(const BalanceArgs& p, int seq, int lane) {
         s = seq;
@@ -264,6 +266,7 @@ struct Group {
         }
         end = offset_at(p, seq + 1);
         const int32_t* c = p.counts + (size_t)seq * p.C * p.E;
+        const float u0 = p.d_loss[seq * p.C], u1 = p.d_loss[seq * p.C + p.C - 1];
         double sum0 = 0.0, sum1 = 0.0;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
@@ -275,8 +278,8 @@ struct Group {
             sum0 += a;
             sum1 += b;
         }
-        a0 = factor(p, seq * p.C, wave_sum(sum0));
-        a1 = p.C == 2 ? factor(p, seq * p.C + 1, wave_sum(sum1)) : 0.0f;
+        a0 = factor(p, u0, wave_sum(sum0));
+        a1 = p.C == 2 ? factor(p, u1, wave_sum(sum1)) : 0.0f;
     }
 };
 

@@ -358,7 +358,8 @@ __device__ __forceinline__ int run_tile(const Fp4GemmArgs& p, const Tile& t, Fee
             words(rsw + n * 32, (wbase + (uint32_t)wrow(n) * nb) & 3, cw[n]);
 #pragma unroll
         for (int i = 0; i < MI; ++i)
-            words(rsa + i * 32 * 32, (abase + (uint32_t)((wm * MI + i) * 32 + l32) * nb) & 3, ca[i]);
+            words(rsa + i * 32 * 32, (abase + (uint32_t)((wm * MI + i) * 32 + l32) * nb) & 3,
+                  ca[i]);
     };
     auto next_scales = [&]() {
 #pragma unroll

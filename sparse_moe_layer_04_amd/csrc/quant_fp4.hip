@@ -46,7 +46,8 @@ __global__ __launch_bounds__(256) void quant_mxfp4_kernel(const void* __restrict
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if constexpr (F32) v[i] = __uint_as_float(w[u][i >> 2][i & 3]);
-            else v[i] = __uint_as_float(i & 1 ? w[u][0][i >> 1] & 0xffff0000u : w[u][0][i >> 1] << 16);
+            else v[i] = __uint_as_float(i & 1 ? w[u][0][i >> 1] & 0xffff0000u
+                                              : w[u][0][i >> 1] << 16);
         }
         uint32_t top = 0;                  // |v| as bits: infinities and NaN are the largest
 #pragma unroll
