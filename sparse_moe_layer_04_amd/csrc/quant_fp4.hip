@@ -9,6 +9,12 @@
 // The rows are one run of blocks (K is a multiple of 32), whatever K is.  Four
 // lanes take a block, eight values each (so that a wave's loads cover whole
 // lines), a thread kU blocks with their loads in flight together.
+//
+// Bound: HBM, 2.53 bytes a bf16 value: 49152 x 4096 84 us, 6.1 TB/s; 8191 x
+// 4064 fp32 25 us (6.0, half of it from the cache).  A lane a block (16 bytes
+// of each of 64 lines a load) and a conversion in software took 103 and 29.
+// Loads past the caches: 78 where nothing is found there, but 32 for 25 and 55
+// for 48 behind a kernel that wrote the rows.
 #include "fp4.h"
 
 namespace moe {
