@@ -490,7 +490,8 @@ __device__ __forceinline__ int run_tile(const Fp4GemmArgs& p, const Tile& t, Fee
     const uint64_t first =
         (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)base) |
         (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(base >> 32)) << 32;
-    const uint32_t bytes = (uint32_t)(((size_t)(t.valid - 1) * N + (N - t.n0)) * ES);
+    // (to the tile's last column: below 2^32 for any N)
+    const uint32_t bytes = (uint32_t)(((size_t)(t.valid - 1) * N + min(N - t.n0, BN)) * ES);
     const auto out = __builtin_amdgcn_make_buffer_rsrc(
         (void*)(uintptr_t)first, 0, __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000);
     const int col = wrow(0);

@@ -64,6 +64,24 @@ def test_mxfp4():
     assert out[-1000:].any()
 
 
+def test_mxfp4_widest():
+    """The most columns there may be, in tiles of 256 rows whose outputs end at
+    2^32 bytes: the halves' products have the same bits."""
+    N = 1 << 22
+    draw = lambda lo, hi, *s: torch.randint(lo, hi, s, dtype=torch.uint8, device="cuda")  # noqa: E731
+    a4, sa = draw(0, 256, 512, 16), draw(120, 130, 512, 1)
+    w4, sw = draw(0, 256, 1, N, 16), draw(120, 130, 1, N, 1)
+    off = torch.tensor([0, 512], dtype=torch.int32, device="cuda")
+    out = torch.full((512, N), -77.0, device="cuda")
+    ops.grouped_gemm_mxfp4(a4, sa, off, w4, sw, out_dtype=ops.OUT_F32, out=out)
+    for i in range(2):
+        cols = slice(i * N // 2, (i + 1) * N // 2)
+        half = ops.grouped_gemm_mxfp4(a4, sa, off, w4[:, cols].contiguous(),
+                                      sw[:, cols].contiguous(), out_dtype=ops.OUT_F32)
+        assert torch.equal(out[:, cols], half)
+    assert out[-1].any()
+
+
 def test_clip():
     n = 2 ** 31 + 4097
     g = torch.full((n,), 0.5, device="cuda")
