@@ -432,7 +432,8 @@ int moe_rms_norm_backward(const void* s, int s_dtype, const void* w, int w_dtype
  *   f_e = E counts[g, e] / (k T_g),  p_te = s_te / sum_e s_te, s = S(logits)
  *   (moe_route's scores),
  *   loss[g] = 1 / T_g sum_t sum_e f_e p_te  (1 for even load; 0 if T_g = 0).
- * Sums over tokens are held in 64 bits.
+ * Sums over tokens are held in fp32 within a piece of a sequence (up to 64
+ * tokens, more beyond 2^24 tokens in all) and in 64 bits over the pieces.
  *   logits [T, E] fp32, topk_ids [T, k] int32; offsets [S + 1] int32 in DEVICE
  *   memory, non-decreasing within [0, T] (entries outside are clamped; NULL
  *   with S = 1: all tokens); modality, mask [T] u8 or NULL; loss [S, C] fp32,
