@@ -145,6 +145,12 @@ __global__ __launch_bounds__(ONE ? 256 : 1024) void add_rms_norm_kernel(NormArgs
 //
 // Bound: HBM, 14 bytes a value with fp32 gradients: 8192 x 4096 84 us + 4.5 for
 // the sums of dw, 5.3 TB/s over both.  The last line in 32 bits: the same time.
+// AHEAD: the next row's loads before this row's sums, where two rows of bf16
+// gradients fit the registers: 8191 x 4096 58 us instead of 63, 16383 x 512 21
+// instead of 23; with fp32 ones, spilled, 93 instead of 90.
+// Two chunks a lane (rows past 8192): the values are converted to 64 bits a
+// second time, not kept so in registers that there are not: 2047 x 16384 bf16
+// 75 us instead of 127 (with one chunk, where they fit, 68 instead of 63).
 template <bool SF32, bool GF32, int RES, int NC, bool ONE>
 __global__ __launch_bounds__(ONE ? 256 : 1024) void rms_norm_backward_kernel(NormBwdArgs p) {
     __shared__ double part[2][ONE ? 1 : 16][2];
@@ -160,15 +166,16 @@ __global__ __launch_bounds__(ONE ? 256 : 1024) void rms_norm_backward_kernel(Nor
         in[c] = first + c * step < d;
         at[c] = in[c] ? first + c * step : 0;
     }
-    Raw8<SF32> s[NC];
-    Raw8<GF32> g[NC];
-    Raw8<RES == RES_F32> r[NC];
+    constexpr bool AHEAD = NC == 1 && !GF32 && RES != RES_F32;
+    Raw8<SF32> s[NC], s1[NC];
+    Raw8<GF32> g[NC], g1[NC];
+    Raw8<RES == RES_F32> r[NC], r1[NC];
     auto load = [&](long long t) {
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            s[c].load(p.s, (size_t)t * d + at[c]);
-            g[c].load(p.dy, (size_t)t * d + at[c]);
-            if constexpr (RES != RES_NONE) r[c].load(p.d_res, (size_t)t * d + at[c]);
+            s1[c].load(p.s, (size_t)t * d + at[c]);
+            g1[c].load(p.dy, (size_t)t * d + at[c]);
+            if constexpr (RES != RES_NONE) r1[c].load(p.d_res, (size_t)t * d + at[c]);
         }
     };
     if (slot < p.rows) load(slot);
@@ -185,6 +192,13 @@ __global__ __launch_bounds__(ONE ? 256 : 1024) void rms_norm_backward_kernel(Nor
     int turn = 0;
     for (long long row = slot; row < p.rows; row += stride, turn ^= 1) {
         double ss = 0.0, gs = 0.0;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            s[c] = s1[c];
+            g[c] = g1[c];
+            if constexpr (RES != RES_NONE) r[c] = r1[c];
+        }
+        if (AHEAD && row + stride < p.rows) load(row + stride);
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -203,6 +217,17 @@ __global__ __launch_bounds__(ONE ? 256 : 1024) void rms_norm_backward_kernel(Nor
             gs = part[turn][0][1];
             for (int v = 1; v < W; ++v) ss += part[turn][v][0], gs += part[turn][v][1];
         }
+        if constexpr (NC > 1) {                  // (converted again from here on)
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+#pragma unroll
+                for (int i = 0; i < (SF32 ? 2 : 1); ++i) asm volatile("" : "+v"(s[c].v[i]));
+#pragma unroll
+                for (int i = 0; i < (GF32 ? 2 : 1); ++i) asm volatile("" : "+v"(g[c].v[i]));
+#pragma unroll
+                for (int j = 0; j < 8; ++j) asm volatile("" : "+v"(w[c][j]));
+            }
+        }
         const double rstd = 1.0 / __builtin_sqrt(ss / d + p.eps);
         const double along = gs / d * rstd * rstd * rstd;
 #pragma unroll
@@ -219,7 +244,7 @@ __global__ __launch_bounds__(ONE ? 256 : 1024) void rms_norm_backward_kernel(Nor
             }
             if (in[c]) store8(p.dx, (size_t)row * d + at[c], p.dx_f32, out);
         }
-        if (row + stride < p.rows) load(row + stride);
+        if (!AHEAD && row + stride < p.rows) load(row + stride);
     }
 #pragma unroll
     for (int c = 0; c < NC; ++c)
