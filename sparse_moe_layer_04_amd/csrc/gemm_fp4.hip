@@ -178,7 +178,8 @@ struct Schedule {
 };
 
 // What goes into LDS, stage after stage and tile after tile: the copies run two
-// and a half stages ahead of the products, across the ends of tiles.  Buffer
+// and a half stages ahead of the products (two slots: one and a quarter), across
+// the ends of tiles.  Buffer
 // resources over a tile's rows (wave-uniform base, 32-bit offsets; rows past the
 // tile's or the matrix's end lie past them and fetch nothing).
 template <bool TALL>
@@ -303,7 +304,7 @@ struct Run {
 };
 
 // One tile, whose first stage has landed in the ring at `slot` and whose next
-// two are on their way (and its first slab; with fewer than three stages it is
+// two (one) are on their way (and its first slab; with fewer than three stages it is
 // fetched here).  `stored`: stores of the tile before, which were issued behind
 // those and need not have ended when they have landed.  All stores are issued,
 // those past the rows or columns with offsets past the resource, so that their
