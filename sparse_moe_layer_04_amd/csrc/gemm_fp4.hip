@@ -37,6 +37,7 @@
 //     reach from registers
 //   8192 x 4096 x 2048, bf16 out                             45  the same, 3.0 PFLOP/s
 #include "fp4.h"
+#include "fp4_order.h"
 #include "lds_ring.h"
 
 namespace moe {
@@ -230,7 +231,7 @@ struct Feed {
     // to the next tile where one ends (past the last with empty resources: every
     // stage issues its copies).  What a tile's last stage holds past K is left
     // out when it is multiplied.
-    static constexpr int kCopies = TALL ? 8 : 6;
+    static constexpr int kCopies = stage_copies(TALL);
     template <int PART>
     __device__ __forceinline__ void copy(const Fp4GemmArgs& p, int at) {
         const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -298,9 +299,7 @@ __device__ __forceinline__ void zeros(unsigned char* ring, int slot, int tail) {
 // What a workgroup's tiles have in common
 struct Run {
     int S, tail;                           // stages, blocks of a short last one (0: none)
-    int per;                               // stages of a slab of scales
-    int slab_at;                           // the stage that sends the next tile's first slab
-    bool late;                             // which then lands only when that tile begins
+    SlabPlan slabs;
 };
 
 // One tile, whose first stage has landed in the ring at `slot` and whose next
@@ -322,11 +321,9 @@ __device__ __forceinline__ int run_tile(const Fp4GemmArgs& p, const Tile& t, Fee
     using W = Waves<MB, TALL>;
     constexpr int WN = W::WN, MI = W::MI, NJ = W::NJ, NT = MI * NJ;
     constexpr int kSlot = Ring<TALL>::kSlot, kSlabs = Ring<TALL>::kSlabs;
-    // copies behind the next stage's at a turn
-    constexpr int kBehind = TALL ? 0 : Feed<TALL>::kCopies;
     const int wm = wave / WN, wn = wave % WN;
     const int N = p.N, nb = p.K / 32;
-    const int S = c.S, tail = c.tail, per = c.per;
+    const int S = c.S, tail = c.tail, per = c.slabs.per;
 
     // LDS rows 32 apart share their swizzle, so the rest of an operand's
     // address is an immediate; the chunk index enters it by exclusive or
@@ -395,19 +392,21 @@ __device__ __forceinline__ int run_tile(const Fp4GemmArgs& p, const Tile& t, Fee
         f.slab(0);
         wait_vm<0>();
         __syncthreads();
-    } else if (c.late && stored) {
+    } else if (c.slabs.late && stored) {
         wait_vm_stores<0>(stored);
         __syncthreads();
     }
-    // The middle of stage j: the next stage has landed (the copies behind it are,
-    // of three slots, those of the one after it, a slab that was sent off just
-    // before them, and the last tile's stores) and every wave has read stage j's
-    // operands, whose slot is free, and the slab if stage j is its first.
+    // The middle of stage j: the next stage has landed (behind its copies are, of
+    // three slots, those of the one after it, a slab between their halves, and the
+    // last tile's stores) and every wave has read stage j's operands, whose slot is
+    // free, and the slab if stage j is its first.  The next tile's first slab, if it
+    // was sent before this tile's last stage, has landed at this tile's last turn.
     bool sent = false;
     auto turn = [&](int j, int next) {
-        if (j == 0) wait_vm_stores<kBehind>(stored);
-        else if (sent && j + 1 < S) wait_vm<kBehind + 2>();
-        else wait_vm<kBehind>();
+        if (j == 0) wait_vm_stores<on_their_way(TALL, NO_SLAB)>(stored);
+        else if (!sent) wait_vm<on_their_way(TALL, NO_SLAB)>();
+        else if (j + 1 < S) wait_vm<on_their_way(TALL, SLAB)>();
+        else wait_vm<on_their_way(TALL, NEXT_SLAB)>();
         if (tail && (j == S - 2 || S == 1)) zeros(ring, next, tail);
         __syncthreads();
     };
@@ -469,7 +468,7 @@ __device__ __forceinline__ int run_tile(const Fp4GemmArgs& p, const Tile& t, Fee
             if constexpr (x == 0 || (TALL && x < 3)) f.template copy<decltype(x)::value>(p, slot);
         });
         const bool inner = at == 0 && j + per < S;
-        sent = inner || j == c.slab_at;
+        sent = inner || j == c.slabs.next_at;
         if (sent) f.slab(inner ? j + per : 0);
         if (++at == per) {
             at = 0;
@@ -522,16 +521,12 @@ __device__ __forceinline__ int run_tile(const Fp4GemmArgs& p, const Tile& t, Fee
 template <bool F32, bool PAST, bool TALL>
 __device__ __forceinline__ void run_tiles(const Fp4GemmArgs& p, const Schedule& sched,
                                           unsigned char* smem) {
-    constexpr int kSlot = Ring<TALL>::kSlot, kAhead = TALL ? 2 : 3;   // stages
+    constexpr int kSlot = Ring<TALL>::kSlot;
     const int nb = p.K / 32;
     Run c;
     c.S = (nb + 7) / 8;
     c.tail = nb & 7;
-    c.per = (nb & 3) || (((uintptr_t)p.as | (uintptr_t)p.ws) & 3) ? 3 : 4;
-    // the next tile's first slab: once this one's last has been read and the feed
-    // is at that tile
-    c.slab_at = c.S < 3 ? -1 : max((c.S - 1) / c.per * c.per, c.S - kAhead);
-    c.late = c.slab_at == c.S - 1;
+    c.slabs = slab_plan(c.S, !(nb & 3) && !(((uintptr_t)p.as | (uintptr_t)p.ws) & 3), TALL);
     const long long Q = sched.items();
     const int xcd = blockIdx.x & 7, step = gridDim.x >> 3, end = (int)(Q * (xcd + 1) / 8);
     int q = (int)(Q * xcd / 8) + (int)(blockIdx.x >> 3);
@@ -551,7 +546,7 @@ __device__ __forceinline__ void run_tiles(const Fp4GemmArgs& p, const Schedule& 
         wait_vm<Feed<TALL>::kCopies>();
     } else {
         f.template copy<0>(p, 2 * kSlot);
-        wait_vm<Feed<TALL>::kCopies + 3>();
+        wait_vm<Feed<TALL>::kCopies + half_copies()>();
     }
     if (c.tail && c.S == 1) zeros(smem, 0, c.tail);
     __syncthreads();

@@ -1,0 +1,17 @@
+"""The MXFP4 product's copies, waits and reads, replayed on the CPU for every
+count of stages, both kinds of slabs and both rings, with the numbers that the
+kernel takes from csrc/fp4_order.h: nothing is read before it has landed behind
+a barrier, and nothing is overwritten before it has been read."""
+import os
+import subprocess
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def test_replay(tmp_path):
+    exe = str(tmp_path / "fp4_order")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror",
+                    "-I" + os.path.join(ROOT, "sparse_moe_layer_04_amd", "csrc"),
+                    os.path.join(ROOT, "tests", "c", "fp4_order.cpp"), "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0, r.stdout[-2000:]

@@ -274,3 +274,43 @@ def test_quantised_product():
     a4, sa = ops.quantize_mxfp4(a.cuda())
     w4, sw = ops.quantize_mxfp4(w.cuda())
     check((a4.cpu(), sa.cpu(), off, w4.cpu(), sw.cpu()), F32)
+
+
+def unaligned(t):
+    """t in memory that begins one byte behind a word."""
+    space = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)
+    space[1:] = t.reshape(-1)
+    return space[1:].view(t.shape)
+
+
+@pytest.mark.parametrize("K,word", [(1184, 1), (1408, 1), (1536, 1), (1824, 1), (2016, 1), (2048, 0),
+                                    (2048, 1), (2560, 1), (2720, 1), (3584, 1)])
+def test_scales_across_tiles(K, word):
+    """Tiles of up to 128 rows, three and more a workgroup, over the counts of
+    stages S whose next tile's scales are sent one stage before a tile's last
+    (S % 4 = 2 with K a multiple of 128 and the scales in whole words, S % 3 = 2
+    with any others), and two with other counts: the 64-bit values, and the bits
+    of a group's product alone, which is one tile a workgroup."""
+    G, N = 160, 784
+    g = torch.Generator(device="cuda").manual_seed(K + word)
+    sizes = torch.randint(0, 129, (G,), generator=g, device="cuda")
+    off = torch.cat([sizes.new_zeros(1), sizes.cumsum(0)]).to(torch.int32)
+    rows = int(off[-1])
+
+    def draw(lo, hi, *s):
+        return torch.randint(lo, hi, s, generator=g, dtype=torch.uint8, device="cuda")
+    a4, w4 = draw(0, 256, rows, K // 2), draw(0, 256, G, N, K // 2)
+    sa, sw = draw(122, 133, rows, K // 32), draw(115, 126, G, N, K // 32)
+    if not word:
+        sa, sw = unaligned(sa), unaligned(sw)
+    for dt in (F32, BF16):
+        check_on_gpu((a4, sa, off, w4, sw), dt)
+    whole = ops.grouped_gemm_mxfp4(a4, sa, off, w4, sw, out_dtype=ops.OUT_F32)
+    o = off.tolist()
+    for i in range(0, G, 3):
+        lo, hi = o[i], o[i + 1]
+        alone = ops.grouped_gemm_mxfp4(a4[lo:hi].clone(), sa[lo:hi].clone(),
+                                       torch.tensor([0, hi - lo], dtype=torch.int32, device="cuda"),
+                                       w4[i:i + 1].clone(), sw[i:i + 1].clone(),
+                                       out_dtype=ops.OUT_F32)
+        assert torch.equal(alone, whole[lo:hi]), i
