@@ -1,7 +1,19 @@
-// The order in which a wave of the MXFP4 product sends off its copies into LDS,
-// as numbers: what the kernel waits for, and what a replay on the host checks.
-// Plain C++.
-//
+// What the MXFP4 product's kernel shares with checks on the host: how a group's
+// rows split into tiles, and the order in which a wave sends off its copies into
+// LDS, as numbers that the kernel waits for.  Plain C++.
+#pragma once
+
+#include "row_tiles.h"
+
+namespace moe {
+
+// row tiles of a group of n rows, tiles of up to `blocks` blocks of 32 rows
+constexpr int row_tiles(int n, int blocks) {
+    const int c = row_blocks(n);
+    return blocks == 1 ? c : blocks == 2 ? (c + 1) >> 1 : blocks == 3 ? (c + 2) / 3
+           : blocks == 4 ? (c + 3) >> 2 : (c + 7) >> 3;
+}
+
 // A stage j of a tile of S stages, in a ring of three slots:
 //   the second half of the copies of stage j + 2 | turn | the first half of those
 //   of stage j + 3, a slab of scales;
@@ -10,10 +22,6 @@
 // Stages behind S are the next tile's.  The turn is a wait and a barrier, behind
 // which the next stage's operands are read.  A wave's operations end in order, so
 // a wait names how many of the last ones may still be on their way.
-#pragma once
-
-namespace moe {
-
 constexpr int kSlabCopies = 2;                             // of a slab
 constexpr int stage_copies(bool tall) { return tall ? 8 : 6; }
 constexpr int half_copies() { return 3; }

@@ -78,13 +78,6 @@ __device__ __forceinline__ bool in_pairs(int valid) {
     return TALL || ((valid - 1) >> 5) & 1;
 }
 
-// row tiles of a group of n rows, tiles of up to `blocks` blocks of 32 rows
-__device__ __forceinline__ int row_tiles(int n, int blocks) {
-    const int c = (n + 31) >> 5;
-    return blocks == 1 ? c : blocks == 2 ? (c + 1) >> 1 : blocks == 3 ? (c + 2) / 3
-           : blocks == 4 ? (c + 3) >> 2 : (c + 7) >> 3;
-}
-
 // Items are (group, band of kBand m-tiles, n-tile, m-tile), the 8 XCDs take
 // contiguous ranges, so that the m-tiles of a weight tile and the n-tiles of a
 // group's rows meet in one XCD's L2.  A group's rows split evenly over its
@@ -169,7 +162,7 @@ struct Schedule {
             local -= NT * mt;
             r0 = r1;
         }
-        const int per = ((n + mt - 1) / mt + 31) & ~31;
+        const int per = tile_rows(n, mt);
         const int band = local / (kBand * NT) * kBand, high = min(kBand, mt - band);
         local -= band * NT;
         t.n0 = local / high * BN;

@@ -1,6 +1,7 @@
-// Test helper: replays the order in which a wave of the MXFP4 product sends off
-// its copies into LDS, waits and reads, with the numbers that the kernel takes
-// from csrc/fp4_order.h, and checks that nothing is read before it has landed
+// Test helper: how a group's rows split into tiles of the MXFP4 product, against
+// 64-bit arithmetic up to the largest groups; and a replay of the order in which a
+// wave of it sends off its copies into LDS, waits and reads, with the numbers that
+// the kernel takes from csrc/fp4_order.h: nothing is read before it has landed
 // behind a barrier and nothing is overwritten before a barrier follows its last
 // read.  All waves take the same steps, so one stands for all.
 #include <cstdio>
@@ -100,10 +101,28 @@ bool replay(int S, bool words, bool tall, int stores) {
     return w.ok;
 }
 
+bool tiles_right(int n, int blocks) {
+    const long long c = ((long long)n + 31) / 32, mt = (c + blocks - 1) / blocks;
+    if (row_tiles(n, blocks) != mt) return false;
+    if (n == 0) return true;
+    const long long per = (((long long)n + mt - 1) / mt + 31) / 32 * 32;
+    return tile_rows(n, (int)mt) == per && per <= 32 * blocks && (mt - 1) * per < n &&
+           mt * per >= n;
+}
+
 }  // namespace
 
 int main() {
     int bad = 0;
+    for (int blocks : {1, 2, 3, 4, 8}) {
+        auto check = [&](int n) {
+            if (tiles_right(n, blocks)) return;
+            printf("n=%d blocks=%d\n", n, blocks);
+            ++bad;
+        };
+        for (int n = 0; n < 70000; ++n) check(n);
+        for (int n = 0; n < 70000; ++n) check(0x7fffffff - n), check(0x7fffffff - 331 * n);
+    }
     for (int tall = 0; tall < 2; ++tall)
         for (int words = 0; words < 2; ++words)
             for (int S = 1; S <= 200; ++S)

@@ -1,7 +1,8 @@
 """The MXFP4 product's copies, waits and reads, replayed on the CPU for every
 count of stages, both kinds of slabs and both rings, with the numbers that the
 kernel takes from csrc/fp4_order.h: nothing is read before it has landed behind
-a barrier, and nothing is overwritten before it has been read."""
+a barrier, and nothing is overwritten before it has been read.  And how a
+group's rows split into tiles, up to 2^31 - 1 of them."""
 import os
 import subprocess
 

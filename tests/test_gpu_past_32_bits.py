@@ -90,3 +90,34 @@ def test_clip():
     want = 1.0 / n ** 0.5
     for part in (g[:5], g[2 ** 31 - 3:2 ** 31 + 5], g[-5:]):
         assert ((part.double() / want - 1).abs() <= 1e-6).all()
+
+
+def test_mxfp4_most_rows():
+    """As many rows as there may be, in one group: every 2^20 of them as the
+    first ones, which are the 64-bit values, in bf16 what rounding leaves."""
+    rows, part = (1 << 31) - 1, 1 << 20
+    draw = lambda lo, hi, *s: torch.randint(lo, hi, s, dtype=torch.uint8, device="cuda")  # noqa: E731
+    first, scale = draw(0, 256, part, 16), draw(120, 130, part, 1)
+    a4 = torch.empty(rows, 16, dtype=torch.uint8, device="cuda")
+    sa = torch.empty(rows, 1, dtype=torch.uint8, device="cuda")
+    for lo in range(0, rows, part):
+        n = min(part, rows - lo)
+        a4[lo:lo + n], sa[lo:lo + n] = first[:n], scale[:n]
+    w4, sw = draw(0, 256, 1, 16, 16), draw(120, 130, 1, 16, 1)
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    out = torch.full((rows, 16), -77.0, dtype=torch.bfloat16, device="cuda")
+    ops.grouped_gemm_mxfp4(a4, sa, off, w4, sw, out=out)
+    assert out.numel() > 2 ** 31
+    value = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6, -0., -.5, -1, -1.5, -2, -3, -4, -6],
+                         dtype=torch.float64, device="cuda")
+
+    def of(c, s):
+        v = value[torch.stack((c & 15, c >> 4), -1).flatten(-2).long()]
+        return v * torch.exp2(s.double() - 127)
+    a, w = of(first, scale), of(w4[0], sw[0])
+    want, mag = a @ w.t(), a.abs() @ w.abs().t()
+    got = out[:part].double()
+    assert ((got - want).abs() <= 32 * 2.0 ** -24 * mag + want.abs() * 2.0 ** -8).all()
+    for lo in range(0, rows, part):
+        n = min(part, rows - lo)
+        assert torch.equal(out[lo:lo + n], out[:n]), lo
