@@ -58,6 +58,7 @@
 // memory, 5.5 TB/s.  One row of each of few groups: the chain of K's blocks on
 // few CUs (12 groups x 4096 x 544: 36 tiles, 16 us with bf16, 25 with fp32).
 #include "lds_ring.h"
+#include "row_tiles.h"
 
 namespace moe {
 namespace {
@@ -654,7 +655,7 @@ __device__ __forceinline__ void run_tile(const Fp8GemmArgs& p, const Tile& t, co
 // (fp32 output; bf16 35 and 18).
 constexpr int kTallest = BM / 32;
 __device__ __forceinline__ int row_tiles(int n, int blocks) {
-    const int c = (n + 31) >> 5;
+    const int c = row_blocks(n);
     if (blocks >= 4) return c <= kTallest ? c > 0 : blocks == 4 ? (c + 3) >> 2 : (c + 4) / 5;
     return blocks == 1 ? c : blocks == 2 ? (c + 1) >> 1 : (c + 2) / 3;
 }
@@ -743,7 +744,7 @@ __global__ __launch_bounds__(kThreads) void gemm_fp8_block_kernel(Fp8GemmArgs p)
             local -= NT * mt;
             r0 = r1;
         }
-        const int per = ((n + mt - 1) / mt + 31) & ~31;
+        const int per = tile_rows(n, mt);
         const int band = local / (kBand * NT) * kBand, high = min(kBand, mt - band);
         local -= band * NT;
         t.n0 = local / high * TN;

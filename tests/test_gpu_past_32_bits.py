@@ -121,3 +121,29 @@ def test_mxfp4_most_rows():
     for lo in range(0, rows, part):
         n = min(part, rows - lo)
         assert torch.equal(out[lo:lo + n], out[:n]), lo
+
+
+def test_fp8_block_most_rows():
+    """The 8-bit product in the same way."""
+    rows, part = (1 << 31) - 1, 1 << 20
+    first = torch.randint(0, 0x7f, (part, 16), dtype=torch.uint8, device="cuda")
+    scale = torch.rand(part, 1, device="cuda") + 0.5
+    a8 = torch.empty(rows, 16, dtype=torch.uint8, device="cuda")
+    sa = torch.empty(rows, 1, device="cuda")
+    for lo in range(0, rows, part):
+        n = min(part, rows - lo)
+        a8[lo:lo + n], sa[lo:lo + n] = first[:n], scale[:n]
+    w8 = torch.randint(0, 0x7f, (1, 16, 16), dtype=torch.uint8, device="cuda")
+    sw = torch.rand(1, 1, 1, device="cuda") + 0.5
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    out = torch.full((rows, 16), -77.0, dtype=torch.bfloat16, device="cuda")
+    ops.grouped_gemm_fp8_block(a8, sa, off, w8, sw, out=out)
+    of = lambda c, s: c.view(torch.float8_e4m3fn).double() * s.double()  # noqa: E731
+    want = of(first, scale) @ of(w8[0], sw[0]).t()
+    got = out[:part].double()
+    # values of one sign: 7 * 2^-13 of their sum at most is left out of a bf16
+    # output's products, then one rounding
+    assert ((got - want).abs() <= want * (2.0 ** -8 + 8 * 2.0 ** -13)).all()
+    for lo in range(0, rows, part):
+        n = min(part, rows - lo)
+        assert torch.equal(out[lo:lo + n], out[:n]), lo
