@@ -112,13 +112,15 @@ __global__ __launch_bounds__(64 * W) void balance_pieces_kernel(BalanceArgs p) {
     __shared__ int hist[2][NPL * 64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int E = p.E, k = p.k;
-    const int t0 = blockIdx.x * p.chunk, t1 = min(p.T, t0 + p.chunk);
+    // (places beyond a wave's last token may pass 2^31: unsigned)
+    const unsigned t0 = blockIdx.x * (unsigned)p.chunk;
+    const unsigned t1 = min((unsigned)p.T, t0 + (unsigned)p.chunk);
     if (blockIdx.x == 0)
         for (int s = threadIdx.x; s < p.S; s += 64 * W) p.ticket[s] = 0;
-    for (int tb = t0; tb < t1;) {
-        const int s = sequence_of(p, tb, lane);
+    for (unsigned tb = t0; tb < t1;) {
+        const int s = sequence_of(p, (int)tb, lane);
         if (s >= p.S) break;
-        const int te = min(t1, s < 0 ? offset_at(p, 0) : offset_at(p, s + 1));
+        const unsigned te = min(t1, (unsigned)offset_at(p, s < 0 ? 0 : s + 1));
         if (s < 0 || te <= tb) {             // (before the first sequence; never te <= tb
             tb = max(te, tb + 1);            // with offsets in order)
             continue;
@@ -129,10 +131,10 @@ __global__ __launch_bounds__(64 * W) void balance_pieces_kernel(BalanceArgs p) {
 #pragma unroll
         for (int i = 0; i < NPL; ++i) m0[i] = m1[i] = 0.0f;
         Token<NPL> next;
-        next.load(p, min(tb + wave, te - 1), lane);
-        for (int t = tb + wave; t < te; t += W) {
+        next.load(p, (int)min(tb + wave, te - 1), lane);
+        for (unsigned t = tb + wave; t < te; t += W) {
             Token<NPL> a = next;
-            next.load(p, min(t + W, te - 1), lane);
+            next.load(p, (int)min(t + W, te - 1), lane);
             const int c = a.mod ? 1 : 0;
             const bool bad = a.bad(p);
             if (!a.mask || bad) {

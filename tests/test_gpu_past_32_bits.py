@@ -147,3 +147,35 @@ def test_fp8_block_most_rows():
     for lo in range(0, rows, part):
         n = min(part, rows - lo)
         assert torch.equal(out[lo:lo + n], out[:n]), lo
+
+
+def test_balance_most_tokens():
+    """As many tokens as there may be, 2047 times the same 2^20 and all but the
+    last of them again as a second sequence, against 64 bits."""
+    T, part, E = (1 << 31) - 1, 1 << 20, 2
+    first = torch.randn(part, E, device="cuda")
+    chosen = torch.randint(0, E, (part, 1), device="cuda").to(torch.int32)
+    lg = torch.empty(T, E, device="cuda")
+    ids = torch.empty(T, 1, dtype=torch.int32, device="cuda")
+    for lo in range(0, T, part):
+        n = min(part, T - lo)
+        lg[lo:lo + n], ids[lo:lo + n] = first[:n], chosen[:n]
+    off = torch.tensor([0, 2047 * part, T], dtype=torch.int32, device="cuda")
+    loss, counts = ops.balance_loss(lg, ids, off)
+    d = ops.balance_loss_backward(lg, ids, counts, torch.ones_like(loss), off)
+    s = torch.sigmoid(first.double())
+    p = s / s.sum(1, keepdim=True)
+    for seq, n in ((0, part), (1, part - 1)):
+        times = 2047 if seq == 0 else 1
+        c = torch.bincount(chosen[:n, 0].long(), minlength=E)
+        assert torch.equal(counts[seq, 0].long(), c * times)
+        f = c.double() * E / n
+        q = p[:n] @ f
+        # 64 steps of a row's sums and quotients, fp32 sums of 1024 tokens a wave
+        assert abs(float(loss[seq, 0]) / float(q.mean()) - 1) <= (64 + 1024 + 8) * 2.0 ** -24
+        up = p[:n] * (1 - s[:n]) / (n * times)
+        at = seq * 2047 * part
+        got = d[at:at + n].double()
+        assert ((got - (f - q[:, None]) * up).abs() <= 64 * 2.0 ** -24 * (f + q[:, None]) * up).all()
+    for i in range(1, 2047):
+        assert torch.equal(d[i * part:(i + 1) * part], d[:part]), i
