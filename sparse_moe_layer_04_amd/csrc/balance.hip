@@ -319,13 +319,16 @@ __global__ __launch_bounds__(256) void balance_gradient_kernel(BalanceArgs p, in
         }
         sum = wave_sum_f32(sum);
         cs = wave_sum_f32(cs);
+        // (the scores are divided by their sum before they meet d_loss: 1 / sum is
+        // up to 5e34, and their product would pass fp32)
         const float inv = 1.0f / sum, q = cs * inv;
-        const float up = (second ? g.a1 : g.a0) * inv;
+        const float up = second ? g.a1 : g.a0;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
             const int x = lane + 64 * i;
             if (x >= p.E) continue;
-            float d = part ? up * ((second ? g.c1[i] : g.c0[i]) - q) * s[i] * (e[i] * s[i]) : 0.0f;
+            const float v = up * ((second ? g.c1[i] : g.c0[i]) - q);
+            float d = part ? v * (s[i] * inv) * (e[i] * s[i]) : 0.0f;
             const size_t at = (size_t)t * p.E + x;
             if (p.add) d += p.add[at];
             p.d_logits[at] = d;

@@ -604,3 +604,18 @@ def test_another_stream():
     _, want = norm_ref(xs, None, torch.ones(1024), 1e-6)
     near(y, want, rounded(want, BF16, want.abs() * 2.0 ** -22), "y")
     assert abs(float(n) / float(xs.to(D).norm()) - 1) < 1e-6
+
+
+@pytest.mark.parametrize("E,k", [(1, 1), (8, 1), (100, 3)])
+@pytest.mark.parametrize("d_loss", [1.0, 65536.0, 1e8])
+def test_balance_gradient_of_small_scores(E, k, d_loss):
+    """Logits at the clamp's lower end, where a row's scores add up to 1e-33, with
+    a scaled loss: the gradient is of the order of d_loss / T_g all the same."""
+    g = torch.Generator().manual_seed(E)
+    lg = -81 + 3 * torch.rand(3, E, generator=g)
+    ids = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(3)]).to(torch.int32)
+    off = torch.tensor([0, 1, 3], dtype=torch.int32)
+    dl = torch.full((2, 1), d_loss)
+    _, counts, d, mag = balance_ref(lg, ids, off, None, None, dl)
+    got = ops.balance_loss_backward(lg.cuda(), ids.cuda(), counts.cuda(), dl.cuda(), off.cuda())
+    near(got, d, mag * STEPS + TINY[F32] * 4, "d_logits")
