@@ -186,7 +186,7 @@ __global__ __launch_bounds__(ONE ? 256 : 1024) void rms_norm_backward_kernel(Nor
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             dw[c][j] = 0.0f;
-            w[c][j] = in[c] ? w[c][j] : 0.0f;    // (lanes past d add nothing)
+            w[c][j] = in[c] ? w[c][j] : 0.0f;
         }
     }
     int turn = 0;
@@ -196,6 +196,11 @@ __global__ __launch_bounds__(ONE ? 256 : 1024) void rms_norm_backward_kernel(Nor
         for (int c = 0; c < NC; ++c) {
             s[c] = s1[c];
             g[c] = g1[c];
+            // (lanes past d add nothing, whatever the row's start holds)
+#pragma unroll
+            for (int i = 0; i < (GF32 ? 2 : 1); ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) g[c].v[i][j] = in[c] ? g[c].v[i][j] : 0u;
             if constexpr (RES != RES_NONE) r[c] = r1[c];
         }
         if (AHEAD && row + stride < p.rows) load(row + stride);

@@ -619,3 +619,18 @@ def test_balance_gradient_of_small_scores(E, k, d_loss):
     _, counts, d, mag = balance_ref(lg, ids, off, None, None, dl)
     got = ops.balance_loss_backward(lg.cuda(), ids.cuda(), counts.cuda(), dl.cuda(), off.cuda())
     near(got, d, mag * STEPS + TINY[F32] * 4, "d_logits")
+
+
+@pytest.mark.parametrize("d", [8, 520, 1024, 4104, 9000])
+@pytest.mark.parametrize("gt", [BF16, F32])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_backward_not_finite(d, gt, value):
+    """An infinity or NaN in a row's first gradients: what the formula makes of
+    it, whatever the row's width, in its row alone."""
+    s, _, w = norm_inputs(6, d, F32, None, F32)
+    dy = torch.randn(6, d, generator=torch.Generator().manual_seed(d)).to(gt)
+    dy[1, 0], dy[4, 5] = value, -value
+    dx, dw, mag, dmag = backward_ref(s, w, dy, None, 1e-6)
+    got, gw = ops.rms_norm_backward(s.cuda(), w.cuda(), dy.cuda())
+    near(got, dx, rounded(dx, F32, mag * 2.0 ** -40), "dx")
+    near(gw, dw, 8 * 2.0 ** -24 * dmag + TINY[F32], "dw")
