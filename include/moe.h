@@ -409,7 +409,8 @@ int moe_add_rms_norm(const void* x, int x_dtype, const void* residual, int res_d
  * residual), dy the gradient of y, d_res (or NULL) that of res_out from
  * elsewhere.  With r = 1 / sqrt(mean(s^2) + eps), n = s r and g = dy w:
  *   dx = r (g - n mean(g n)) + d_res, the gradient of x and of the residual;
- *   dw[c] = sum_t dy[t, c] n[t, c], fp32.
+ *   dw[c] = sum_t dy[t, c] n[t, c], fp32 (sums of up to 512 rows in fp32, added
+ *   in 64 bits).
  *   s, w, dy, d_res, dx: each bf16 or fp32 (MOE_IN_*); dx may be dy or d_res
  *   of the same type.  dw [d] is written (zeros with rows = 0).  ws:
  *   moe_rms_norm_backward_workspace_size(rows, d) bytes, 256-byte aligned (0

@@ -15,6 +15,7 @@
 // it from the cache).  Loads behind a branch on the type, which the compiler
 // waits for one by one, took 93 us: types are template arguments.  Stores or
 // loads past the caches: none or slower.  Four rows of 2048: 2.7 us, a launch.
+#include <algorithm>
 #include <type_traits>
 
 #include "step.h"
@@ -141,7 +142,10 @@ __global__ __launch_bounds__(ONE ? 256 : 1024) void add_rms_norm_kernel(NormArgs
 // last line, whose terms cancel), the row held in registers.  A wave or a
 // workgroup takes rows t, t + stride, ... and keeps its columns' dw in
 // registers (fp32); its sums go to a row of `part`, which the second kernel
-// adds up (64 bits), always in the same order.
+// adds up (64 bits), always in the same order.  A launch gives each at most
+// kNormRun rows, so that no fp32 sum is longer (16384 equal terms were off by
+// 2^-12): one launch up to 262144 rows, 524288 of up to 2048 values.  (Runs in a
+// loop of the kernel's own cost registers: 8191 x 4104 bf16 73 -> 79 us.)
 //
 // Bound: HBM, 14 bytes a value with fp32 gradients: 8192 x 4096 84 us + 4.5 for
 // the sums of dw, 5.3 TB/s over both.  The last line in 32 bits: the same time.
@@ -331,17 +335,25 @@ void launch_backward(const NormBwdArgs& p, const Shape& s, dim3 grid, hipStream_
 #undef MOE_NORM
 }
 
-// Rows of the backward's `part`: as many workgroups as are resident at once, 8
-// waves for each of 512.  8192 x 4096, fp32: 92 us with 512, 97 with 1024 (half
+// Rows of the backward's `part` (of a launch): as many workgroups as are resident at
+// once, 8 waves for each of 512.  8192 x 4096, fp32: 92 us with 512, 97 with 1024 (half
 // of them wait), 101 with 256; 8191 x 1024 (a wave a row): 28.5 us with 1024
 // waves, 38 with 2048 (more partial sums).
 constexpr int kNormParts = 512;
 
+constexpr int kNormRun = 512;
+
 Shape backward_shape(int d) { return shape_of(d, 1); }
-int backward_parts(long long rows, const Shape& s) {
+// rows of `part` of a launch
+int backward_slots(long long rows, const Shape& s) {
     const long long most = s.one ? (rows + 3) / 4 * 4 : rows;
-    const long long parts = s.one ? 2 * kNormParts : s.threads <= 256 ? 2 * kNormParts : kNormParts;
-    return (int)(most < parts ? most : parts);
+    const long long slots = s.one ? 2 * kNormParts : s.threads <= 256 ? 2 * kNormParts : kNormParts;
+    return (int)(most < slots ? most : slots);
+}
+// and of all launches
+int backward_parts(long long rows, int slots) {
+    const long long each = (long long)slots * kNormRun;
+    return slots ? (int)((rows + each - 1) / each * slots) : 0;
 }
 
 }  // namespace
@@ -367,13 +379,26 @@ hipError_t launch_add_rms_norm(const NormArgs& p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-int norm_backward_parts(long long rows, int d) { return backward_parts(rows, backward_shape(d)); }
+int norm_backward_parts(long long rows, int d) {
+    return backward_parts(rows, backward_slots(rows, backward_shape(d)));
+}
 
-hipError_t launch_rms_norm_backward(const NormBwdArgs& p, hipStream_t stream) {
-    const Shape s = backward_shape(p.d);
-    const int parts = backward_parts(p.rows, s);
-    if (parts > 0) {
-        const dim3 grid((unsigned)(s.one ? parts / 4 : parts));
+hipError_t launch_rms_norm_backward(const NormBwdArgs& args, hipStream_t stream) {
+    const Shape s = backward_shape(args.d);
+    const int slots = backward_slots(args.rows, s), parts = backward_parts(args.rows, slots);
+    const long long each = (long long)slots * kNormRun;
+    for (long long row = 0; row < args.rows; row += each) {
+        NormBwdArgs p = args;
+        auto behind = [&](const void* q, int f32) {
+            return (const char*)q + (size_t)row * p.d * (f32 ? 4 : 2);
+        };
+        p.rows = std::min(each, args.rows - row);
+        p.s = behind(args.s, p.s_f32);
+        p.dy = behind(args.dy, p.dy_f32);
+        if (p.d_res) p.d_res = behind(args.d_res, p.res_f32);
+        p.dx = const_cast<char*>(behind(args.dx, p.dx_f32));
+        p.part = args.part + (size_t)(row / kNormRun) * p.d;
+        const dim3 grid((unsigned)(s.one ? slots / 4 : slots));
         const int res = !p.d_res ? RES_NONE : p.res_f32 ? RES_F32 : RES_BF16;
         auto by_res = [&](auto sf, auto gf) {
             constexpr bool S = decltype(sf)::value, G = decltype(gf)::value;
@@ -388,8 +413,8 @@ hipError_t launch_rms_norm_backward(const NormBwdArgs& p, hipStream_t stream) {
         else if (p.dy_f32) by_res(false_type(), true_type());
         else by_res(false_type(), false_type());
     }
-    hipLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)((p.d + 15) / 16)), dim3(256), 0, stream,
-                       p.part, parts, p.d, p.dw);
+    hipLaunchKernelGGL(norm_dw_kernel, dim3((unsigned)((args.d + 15) / 16)), dim3(256), 0, stream,
+                       args.part, parts, args.d, args.dw);
     return hipGetLastError();
 }
 

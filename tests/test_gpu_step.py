@@ -634,3 +634,15 @@ def test_backward_not_finite(d, gt, value):
     got, gw = ops.rms_norm_backward(s.cuda(), w.cuda(), dy.cuda())
     near(got, dx, rounded(dx, F32, mag * 2.0 ** -40), "dx")
     near(gw, dw, 8 * 2.0 ** -24 * dmag + TINY[F32], "dw")
+
+
+@pytest.mark.parametrize("rows,d", [(1 << 24, 8), (1 << 21, 520)])
+def test_backward_many_rows(rows, d):
+    """dw of many rows of one sign, whose terms end in bits that a long fp32 sum
+    does not hold: fp32 sums of 512 rows at most, the rest in 64 bits."""
+    s = torch.ones(1, d, dtype=BF16, device="cuda").expand(rows, d).contiguous()
+    dy = torch.full((rows, d), 1 + 0.4 * 2.0 ** -10, device="cuda")
+    dw = ops.rms_norm_backward(s, torch.ones(d, device="cuda"), dy, eps=0.0,
+                               dx_dtype=ops.OUT_BF16)[1]
+    want = torch.full((d,), float(dy[0, 0].double()) * rows, dtype=D)
+    near(dw, want, want * (512 + 1) * 2.0 ** -24, "dw")
