@@ -701,6 +701,7 @@ def expert_ffn_fp8_block(a8, a_scale, offsets, w_gate, w_up, w_down, clamp_limit
 
 
 _IN_TYPES = {torch.bfloat16: IN_BF16, torch.float32: IN_F32}
+_OUT_TYPES = {OUT_BF16: torch.bfloat16, OUT_F32: torch.float32}
 
 
 def _device(t, name):
@@ -808,6 +809,9 @@ def rms_norm_backward(s, w, dy, eps=1e-6, d_res=None, dx_dtype=OUT_F32, dx=None,
     (its first result), dy the gradient of y, d_res that of s from elsewhere
     (or None); bf16 or fp32 each.  Returns (dx [rows, d] of dx_dtype, the
     gradient of x and of the residual, dw [d] fp32)."""
+    dt = _OUT_TYPES.get(dx_dtype)
+    if dt is None:
+        raise MoeError(f"dx_dtype must be OUT_F32 or OUT_BF16, got {dx_dtype}")
     dev = _device(s, "s")
     shape = rows, d = _two_dims(s, "s")
     st = _typed(s, dev, "s", shape)
@@ -816,7 +820,6 @@ def rms_norm_backward(s, w, dy, eps=1e-6, d_res=None, dx_dtype=OUT_F32, dx=None,
     rt = rp = 0
     if d_res is not None:
         rt, rp = _typed(d_res, dev, "d_res", shape), d_res.data_ptr()
-    dt = torch.float32 if dx_dtype == OUT_F32 else torch.bfloat16
     if dx is None:
         dx = torch.empty_like(s, dtype=dt, memory_format=torch.contiguous_format)
     else:

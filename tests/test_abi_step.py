@@ -231,3 +231,11 @@ def test_binding_refuses_host_tensors():
                  lambda: ops.GradClip([None]), lambda: ops.grouped_gemm_mxfp4(None, u8, off, u8, u8)):
         with pytest.raises(ops.MoeError, match="is required"):
             call()
+
+
+@pytest.mark.parametrize("dx_dtype", [torch.float32, torch.bfloat16, 2, -1, None, "fp32"])
+def test_binding_refuses_types_of_dx(dx_dtype):
+    """What is neither OUT_F32 nor OUT_BF16 is no bf16 either."""
+    x, w = torch.zeros(4, 128), torch.ones(128)
+    with pytest.raises(ops.MoeError, match="dx_dtype"):
+        ops.rms_norm_backward(x, w, x, dx_dtype=dx_dtype)
