@@ -44,6 +44,7 @@ class Block:
         self.grads = dict(dx=torch.empty((w.T, w.d), device=dev),
                           norm=torch.empty(w.d, device=dev),
                           **{"d" + n: like(n) for n in self.weights})
+        self.flags = torch.zeros(1, dtype=torch.int32, device=dev)     # of all steps
         self.clip = ops.GradClip([self.grads["norm"]] + [self.grads["d" + n] for n in self.weights])
         self.load()
 
@@ -51,6 +52,7 @@ class Block:
         """The layouts of the layer's kernels, after a weight update."""
         self.layer = ops.MoeLayer.from_workload(self.w, self.inputs, out_dtype=ops.OUT_F32,
                                                 packed=True)
+        self.layer.flags = self.flags
         self.w_g_t = ops.pack_weights(self.inputs["w_g"].t().contiguous(), 256)
 
     def forward(self, x, stream):
@@ -63,7 +65,7 @@ class Block:
         self.ids = torch.empty((w.T, w.k), dtype=torch.int32, device=dev)
         out = self.layer.forward(self.y, modality=self.modality, logits=self.logits, ids=self.ids)
         loss, self.counts = ops.balance_loss(self.logits, self.ids, self.offsets, self.modality,
-                                             flags=self.layer.flags)
+                                             flags=self.flags)
         return out, self.s, loss
 
     def backward(self, d_out, d_stream=None):
@@ -113,8 +115,8 @@ def main():
         print(f"step {step}: error {float(error.square().mean()):.4f}, balance "
               f"{float(balance.mean()):.4f}, gradients' norm {float(norm):.3f}, "
               f"{(time.perf_counter() - t) * 1e3:.1f} ms")
-    if ops.read_error_flags(block.layer.flags):
-        raise ops.MoeError("the layer raised its error flags")
+    if ops.read_error_flags(block.flags):
+        raise ops.MoeError("a step raised the error flags")
 
 
 if __name__ == "__main__":

@@ -154,3 +154,16 @@ def test_low_precision_forward():
     want = torch.cat([a[:40] @ m[0].t(), a[40:] @ m[1].t()])
     mag = torch.cat([a[:40].abs() @ m[0].abs().t(), a[40:].abs() @ m[1].abs().t()])
     assert ((got - want).abs() <= d * 2.0 ** -24 * mag).all()
+
+
+def test_flags_of_earlier_steps():
+    """What a step's kernels flagged is still there behind the weight update,
+    which makes a new layer."""
+    w = workloads.small(64, 128, 64, 2, 64, 3, scale=2.5, F_shared=64)
+    block = example.Block(w, workloads.make_inputs(w, "cuda"),
+                          torch.tensor([0, w.T], dtype=torch.int32, device="cuda"))
+    for v in block.grads.values():
+        v.zero_()
+    block.layer.flags.fill_(ops.FLAG_BAD_EXPERT_ID)
+    block.update(0.1, 1.0)
+    assert ops.read_error_flags(block.layer.flags) == ops.FLAG_BAD_EXPERT_ID
