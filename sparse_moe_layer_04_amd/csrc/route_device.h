@@ -15,7 +15,7 @@ namespace {
 // C2 = fl32(ln2 - C1); exp(r) by the degree-7 Taylor polynomial (Horner, fma)
 // with binary32 coefficients 1/j!; e = p * 2^n; S = 1 / (1 + e), correctly
 // rounded division.
-__device__ __forceinline__ float score_exp(float x) {
+__device__ __forceinline__ float score_fn(float x) {
     x = __builtin_fminf(__builtin_fmaxf(x, -80.0f), 80.0f);  // maxNum: NaN -> -80
     const float log2e = 0x1.715476p+0f;
     const float c1 = 0x1.62e4p-1f;
@@ -33,11 +33,7 @@ __device__ __forceinline__ float score_exp(float x) {
     p = __builtin_fmaf(p, r, 0.5f);
     p = __builtin_fmaf(p, r, 1.0f);
     p = __builtin_fmaf(p, r, 1.0f);
-    return __builtin_ldexpf(p, (int)n);
-}
-// S alone, and e of it for 1 - S = e S
-__device__ __forceinline__ float score_fn(float x) {
-    const float e = score_exp(x);
+    float e = __builtin_ldexpf(p, (int)n);
     float den = 1.0f + e;
     return 1.0f / den;
 }
