@@ -31,11 +31,14 @@
 //   64 groups, 192 rows in all, 2048 x 1024, bf16 out        15  the weights' 70 MB (10 at
 //     6.8 TB/s) and the start of the reads: one round, 8 stages
 //   384 uneven groups, 49152 rows, 4096 x 2048, fp32 out    455  HBM: weights, rows and
-//     outputs are 2.2 GB, what tiles fetch again from memory 0.3 GB: 5.5 TB/s
-//   8191 x 4064 x 2032, bf16 out                             49  copies into LDS and reads
-//     out of it beside the matrix cores: 2.8 PFLOP/s of the 8 that the instructions
-//     reach from registers
-//   8192 x 4096 x 2048, bf16 out                             45  the same, 3.0 PFLOP/s
+//     outputs are 2.2 GB, what tiles fetch again from memory 0.3 GB: 5.5 TB/s (under the
+//     profiler 480 on the average, 440 at least)
+//   8191 x 4064 x 2032, bf16 out                          47-51  waits: the matrix cores are
+//     busy 29% of the time, the LDS with reads 16% (2.8 PFLOP/s of the 8 that the
+//     instructions reach from registers): all waves of a CU meet at each stage's
+//     barrier, and a step's products stand behind its reads
+//   8192 x 4096 x 2048, bf16 out                             47  the same, 2.9 PFLOP/s
+//   one matrix, 1 to 16 rows x 4096 x 2048                   15  one tile's 16 stages, on 8 CUs
 #include "fp4.h"
 #include "fp4_order.h"
 #include "lds_ring.h"
@@ -118,7 +121,7 @@ struct Schedule {
         const int cus = (int)gridDim.x, usual = items();
         // Tall tiles where their rounds on the CUs, of up to twice the products
         // and 3/4 of the bytes into LDS for each, are fewer than 2/3: 8191 x 4064
-        // x 2032 then takes 49 us instead of 57, 8192 x 4096 x 2048 45 instead of
+        // x 2032 then takes 49 us instead of 57, 8192 x 4096 x 2048 47 instead of
         // 50; 384 uneven groups of 128 rows on the average x 4096 x 2048, all in
         // tall tiles, 505 instead of 465
         tall = false;

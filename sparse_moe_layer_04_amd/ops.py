@@ -918,8 +918,12 @@ class GradClip:
     moe_clip_grad_norm): bf16 or fp32 tensors of any shapes on one device, laid
     out once and kept (the plan holds them), as a program keeps its gradient
     buffers.  out: tensors of the same shapes and types for the clipped
-    gradients; None: in place.  A tensor listed twice, or one that overlaps
-    another's out, is refused.  A GradClip serves one call at a time (its
+    gradients; None: in place.  Every tensor begins at a multiple of 16 bytes
+    (what torch allocates does; views of a flat buffer may not, and are refused).
+    A tensor listed twice, or one that overlaps another's out, is refused.  Laying
+    out takes 0.3 ms of host time for 400 tensors, 1.5 ms for 2000, and waits for
+    the current stream: a program whose gradients are new tensors in every step
+    pays that in every step.  A GradClip serves one call at a time (its
     workspace)."""
 
     def __init__(self, grads, out=None):
