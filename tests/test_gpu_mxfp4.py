@@ -314,3 +314,26 @@ def test_scales_across_tiles(K, word):
                                        w4[i:i + 1].clone(), sw[i:i + 1].clone(),
                                        out_dtype=ops.OUT_F32)
         assert torch.equal(alone, whole[lo:hi]), i
+
+
+@pytest.mark.parametrize("K,word", [(640, 1), (1408, 1), (1536, 1), (1824, 1), (2048, 0), (2560, 1)])
+def test_scales_across_tall_tiles(K, word):
+    """The same of tiles of 256 rows, three a workgroup."""
+    G, N, n = 80, 1552, 256
+    g = torch.Generator(device="cuda").manual_seed(K + word)
+
+    def draw(lo, hi, *s):
+        return torch.randint(lo, hi, s, generator=g, dtype=torch.uint8, device="cuda")
+    a4, w4 = draw(0, 256, G * n, K // 2), draw(0, 256, G, N, K // 2)
+    sa, sw = draw(122, 133, G * n, K // 32), draw(115, 126, G, N, K // 32)
+    if not word:
+        sa, sw = unaligned(sa), unaligned(sw)
+    off = (torch.arange(G + 1, device="cuda") * n).to(torch.int32)
+    check_on_gpu((a4, sa, off, w4, sw), F32)
+    whole = ops.grouped_gemm_mxfp4(a4, sa, off, w4, sw, out_dtype=ops.OUT_F32)
+    for i in range(0, G, 3):
+        rows = slice(i * n, (i + 1) * n)
+        alone = ops.grouped_gemm_mxfp4(a4[rows].clone(), sa[rows].clone(), off[:2].clone(),
+                                       w4[i:i + 1].clone(), sw[i:i + 1].clone(),
+                                       out_dtype=ops.OUT_F32)
+        assert torch.equal(alone, whole[rows]), i

@@ -646,3 +646,26 @@ def test_backward_many_rows(rows, d):
                                dx_dtype=ops.OUT_BF16)[1]
     want = torch.full((d,), float(dy[0, 0].double()) * rows, dtype=D)
     near(dw, want, want * (512 + 1) * 2.0 ** -24, "dw")
+
+
+@pytest.mark.parametrize("rows,d", [(524288 + 1, 8), (262144 + 515, 2056)])
+@pytest.mark.parametrize("inplace", [False, True])
+def test_backward_in_several_launches(rows, d, inplace):
+    """More rows than one launch takes: dx has the bits of its parts' calls, dw is
+    the 64-bit sum."""
+    g = torch.Generator(device="cuda").manual_seed(rows + d)
+    draw = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    s, dy, res = (draw(rows, d).to(BF16) for _ in range(3))
+    w = draw(d)
+    cuts = [0, 1000, rows - 700, rows]
+    parts = [ops.rms_norm_backward(s[a:b], w, dy[a:b], d_res=res[a:b], dx_dtype=ops.OUT_BF16)[0]
+             for a, b in zip(cuts, cuts[1:])]
+    dw, mag = torch.zeros(d, dtype=D, device="cuda"), torch.zeros(d, dtype=D, device="cuda")
+    for a in range(0, rows, 1 << 16):
+        v = s[a:a + (1 << 16)].to(D)
+        t = dy[a:a + (1 << 16)].to(D) * v / torch.sqrt((v * v).mean(1, keepdim=True) + 1e-6)
+        dw, mag = dw + t.sum(0), mag + t.abs().sum(0)
+    got, gw = ops.rms_norm_backward(s, w, dy, d_res=res, dx_dtype=ops.OUT_BF16,
+                                    dx=dy if inplace else None)
+    assert torch.equal(got, torch.cat(parts))
+    near(gw, dw.cpu(), ((512 + 2) * 2.0 ** -24 * mag).cpu() + TINY[F32], "dw")
